@@ -77,11 +77,15 @@ enum {
   MOE_DEVERR_NONFINITE = 2,      /* a router score was NaN (ranked last, never chosen before a finite one) */
   MOE_DEVERR_SCHEDULE = 4,       /* a tile schedule disagreed with the dispatch offsets */
   MOE_DEVERR_TIMEOUT = 8,        /* a kernel's bounded wait expired; that kernel stopped early */
-  MOE_DEVERR_RANGE = 16          /* NVFP4 experts on the FP16 path (under 8 tokens, or above 64): a value
+  MOE_DEVERR_RANGE = 16,         /* NVFP4 experts on the FP16 path (under 8 tokens, or above 64): a value
                                     beyond FP16's range (|v| > 65504) reached an FP16 operand (expert
                                     input row or h); the affected outputs are not finite.  The FP4
                                     tensor path (8..64 tokens) carries each row's magnitude in its
                                     FP32 row scale and has no such limit */
+  MOE_DEVERR_PAGES = 32,         /* moe_paged_plan ran out of free pages, or a request out of its
+                                    block-table row */
+  MOE_DEVERR_CACHE = 64          /* a length, parent, page or slot of the paged-attention entry points
+                                    was out of range (that entry was clamped or skipped) */
 };
 
 typedef int32_t moe_dtype_t;
@@ -368,6 +372,146 @@ moe_status_t moe_block_backward(const moe_config_t* cfg, int32_t T, const void* 
                                 const int32_t* topk_ids, const float* topk_w, const float* scores,
                                 float* dx, const moe_grads_t* grads,
                                 const void* ws, size_t ws_bytes, void* bws, size_t bws_bytes,
+                                void* stream);
+
+/* ---- paged attention for verify blocks ------------------------------------
+ * The attention of a decoder layer over a paged KV cache, for single tokens,
+ * chains and trees of drafted tokens (page "Nemotron Is Not One Circuit:
+ * Mamba, Attention, and MoE Routing", section "The Four Layer Kinds CKE Must
+ * Preserve": the attention layer beside the MoE layer; page "NemotronH
+ * (Nemotron 3.5 Lightning, Bolt, Super VL)", section "Speculation": verify
+ * blocks of several drafted rows).  Three operators: moe_paged_plan builds the
+ * step's block tables and slot maps, moe_rope_append turns the rows by their
+ * positions and writes K and V into the cache, moe_tree_attention reads it.
+ *
+ * A step has R requests.  Request r holds ctx_len[r] tokens in the cache and
+ * brings n_r = new_len[r] >= 0 new ones, its nodes; the nodes of all requests
+ * are packed, request after request, as T = sum n_r rows, those of request r at
+ * q_start[r] .. q_start[r+1] - 1.  Node i of request r lies in the cache at
+ * token ctx_len[r] + i, and token p of request r at offset p % page_size of
+ * page block_table[r][p / page_size].  kv_len[r] = ctx_len[r] + n_r.
+ *
+ * Conventions beyond those above: integer arrays need their type's alignment
+ * only; rows and caches 16 bytes.  Row strides (q_ld, ...) are in elements, a
+ * multiple of 16 bytes, the heads of a row head_dim apart, so that q, k and v
+ * may be parts of one projection's rows.  `ws` is a workspace of
+ * moe_attn_workspace_bytes: zero its first MOE_ATTN_HEADER_BYTES once; calls
+ * that may overlap on the GPU need a workspace each.  Its error word is sticky:
+ * these entry points set bits and never clear it (moe_get_device_error,
+ * moe_clear_device_error).                                                   */
+#define MOE_ATTN_HEADER_BYTES 4096
+
+typedef struct moe_attn_config {
+  int32_t n_heads;           /* H: query heads, a multiple of n_kv_heads            */
+  int32_t n_kv_heads;        /* Hkv; H / Hkv <= 128 query heads share a KV head      */
+  int32_t head_dim;          /* D: 8..128, a multiple of 8                           */
+  int32_t page_size;         /* tokens a page: a power of two, 8..1024               */
+  int32_t n_pages;           /* pages of the cache                                   */
+  int32_t max_pages;         /* entries of a block-table row                         */
+  int32_t rot_dim;           /* leading dims of a head that rotate: even, 0..D       */
+  int32_t rope_interleaved;  /* pairs (2i, 2i+1); 0: (i, i + rot_dim/2)              */
+  float softmax_scale;       /* multiplies q.k; > 0                                  */
+  moe_dtype_t dtype;         /* MOE_DT_BF16 or MOE_DT_F32: rows and caches           */
+  /* where K and V of token offset o, head h of page p start in k_cache and in
+   * v_cache, in elements: p * page_stride + o * token_stride + h * head_stride
+   * (so both [page][token][head][D] and [page][head][token][D] caches fit)     */
+  int64_t page_stride, token_stride, head_stride;
+} moe_attn_config_t;
+
+/* Validates a configuration without touching any pointer. */
+moe_status_t moe_check_attn_config(const moe_attn_config_t* cfg);
+
+/* Bytes of the workspace of the entry points below (0 on an invalid
+ * configuration).  It depends on head_dim alone, not on lengths or batch.    */
+size_t moe_attn_workspace_bytes(const moe_attn_config_t* cfg);
+
+/* Block tables, slot maps, positions and tree masks of a step from its
+ * lengths, on the device.  With held(c) = ceil(c / page_size), request r needs
+ * held(ctx + n) - held(ctx) more pages.  Requests take them in ascending r from
+ * free_pages[*free_head], free_pages[*free_head + 1], ...
+ *   R          requests, 0..16384;  T: rows of the outputs, T >= sum n_r
+ *   ctx_len, new_len [R] int32
+ *   parents    [T] int32 or NULL: the node a node hangs from, an earlier one of
+ *              its request, or -1 (a root).  NULL: chains
+ *   block_table [R, max_pages] int32: entries held(ctx) .. held(ctx + n) - 1 are
+ *              written, the others kept
+ *   free_pages [n_free] int32 page ids;  free_head [1] int32: entries already used
+ *   free_head_out [1] int32 out: *free_head + pages taken; may be free_head
+ *   q_start    [R+1] int32 out: exclusive prefix sum of new_len
+ *   kv_len     [R] int32 out: ctx_len + new_len
+ *   positions  [T] int32 out: ctx_len + depth of the node (chain: + its index)
+ *   slot_map   [T] int64 out: page * page_size + offset, or -1
+ *   tree_mask  [T, mask_words] int32 out (with parents), bit j % 32 of word
+ *              j / 32: node j is the row's node or one of its ancestors
+ * Rows past the last node get position 0, slot -1 and an empty mask, so that a
+ * captured graph may run at a fixed T.  Out of free pages (or of the table's
+ * row): MOE_DEVERR_PAGES, entries and slots -1.  Bad lengths, parents and page
+ * ids: MOE_DEVERR_CACHE; a negative length counts as 0, a bad parent as -1,
+ * nodes past T or past 32 * mask_words are dropped from the rows or the mask. */
+moe_status_t moe_paged_plan(const moe_attn_config_t* cfg, int32_t R, int32_t T, const int32_t* ctx_len,
+                            const int32_t* new_len, const int32_t* parents, int32_t* block_table,
+                            const int32_t* free_pages, int32_t n_free, const int32_t* free_head,
+                            int32_t* free_head_out, int32_t* q_start, int32_t* kv_len, int32_t* positions,
+                            int64_t* slot_map, int32_t* tree_mask, int32_t mask_words, void* ws, size_t ws_bytes,
+                            void* stream);
+
+/* Rotary frequencies as turns: entry i < rot_dim / 2 of the HOST table is
+ * f_i / (2 pi) * 2^64, rounded, with f_i = theta^(-2i / rot_dim) radians a
+ * position, so that position * entry mod 2^64 is the angle's fraction of a turn
+ * exactly, however far the position.  Host arithmetic only; the caller copies
+ * the table to the device once.
+ *   scaling  MOE_ROPE_PLAIN; MOE_ROPE_LINEAR: f_i / factor; MOE_ROPE_YARN: the
+ *            method of "YaRN: Efficient Context Window Extension of Large
+ *            Language Models" (Peng et al., 2023): f_i / factor where a pair
+ *            turns fewer than 1 time over original_context tokens, f_i where it
+ *            turns more than 32 times, a ramp between, and *rot_scale =
+ *            0.1 ln(factor) + 1 (otherwise 1)                                  */
+enum { MOE_ROPE_PLAIN = 0, MOE_ROPE_LINEAR = 1, MOE_ROPE_YARN = 2 };
+moe_status_t moe_rope_table(int32_t rot_dim, double theta, int32_t scaling, double factor,
+                            int64_t original_context, uint64_t* table_host, float* rot_scale);
+
+/* Rotary positions of T rows of `heads` heads: each pair (a, b) of the first
+ * rot_dim dims becomes rot_scale * (a cos - b sin, a sin + b cos), the other dims
+ * are copied.  inverse: the transposed map, which is its backward (the gradient
+ * of the input from the gradient of the output).  FP32, rounded once.
+ *   x, out [T, heads, D] with row strides; out may be x;  positions [T] int32 >= 0
+ *   table  [rot_dim / 2] of moe_rope_table, on the device (NULL if rot_dim is 0) */
+moe_status_t moe_rope(const moe_attn_config_t* cfg, int32_t T, int32_t heads, const void* x, int64_t x_ld,
+                      const int32_t* positions, const uint64_t* table, float rot_scale, int32_t inverse, void* out,
+                      int64_t out_ld, void* stream);
+
+/* The rows of a step on their way into the attention: q rotated to q_out, k
+ * rotated into k_cache and v copied into v_cache at slot_map (one pass; rows
+ * with slot -1 are not cached, a slot outside the cache is skipped with
+ * MOE_DEVERR_CACHE).
+ *   q [T, H, D], k and v [T, Hkv, D] with row strides;  q_out [T, H, D], may be q */
+moe_status_t moe_rope_append(const moe_attn_config_t* cfg, int32_t T, const void* q, int64_t q_ld, const void* k,
+                             int64_t k_ld, const void* v, int64_t v_ld, const int32_t* positions,
+                             const uint64_t* table, float rot_scale, const int64_t* slot_map, void* q_out,
+                             int64_t q_out_ld, void* k_cache, void* v_cache, void* ws, size_t ws_bytes, void* stream);
+
+/* Attention of the step's rows over the cache.  Row i (node i - q_start[r] of
+ * request r) sees the tokens before its request's nodes, kv_len[r] - n_r of
+ * them, and the nodes that its mask row names; without a mask the nodes up to
+ * itself (a chain).  Head h reads KV head h / (H / Hkv).
+ *   out = sum_k softmax_k(softmax_scale q.k) v_k over the keys the row sees
+ *   R          requests, 0..4096;  T rows of q, T >= q_start[R]
+ *   q, out     [T, H, D] with row strides (out must not overlap q)
+ *   q_start [R+1], kv_len [R], block_table [R, max_pages] int32: moe_paged_plan's
+ *   tree_mask  [T, mask_words] int32 or NULL
+ *   lse        [T, H] FP32 out or NULL: the natural log of the sum of exponentials
+ * A row that sees no key, and a row that belongs to no request, gets zeros and
+ * lse = -inf.  Keys that no row sees (stale or unwritten cache memory) do not
+ * enter, whatever they hold, NaN and infinities included; nor do a node's K and
+ * V enter the rows that do not see that node.  FP32 scores and softmax; BF16:
+ * the probabilities enter the second product in BF16.  Lengths outside the block
+ * table's row are clamped and pages outside the cache read as zeros, both with
+ * MOE_DEVERR_CACHE.  T * Hkv * (key tiles of a full block-table row) must stay
+ * below 2^31 (MOE_ERR_UNSUPPORTED).                                          */
+moe_status_t moe_tree_attention(const moe_attn_config_t* cfg, int32_t R, int32_t T, const void* q, int64_t q_ld,
+                                const int32_t* q_start, const int32_t* kv_len, const int32_t* block_table,
+                                const void* k_cache, const void* v_cache, const int32_t* tree_mask,
+                                int32_t mask_words, void* out, int64_t out_ld, float* lse, void* ws, size_t ws_bytes,
                                 void* stream);
 
 /* Synchronises `stream`, copies the device error word of `ws` to *code (host

@@ -14,6 +14,9 @@ LIB_PATH = os.path.join(_PKG, "lib", "libmoe_gb300.so")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_CUDA, MOE_ERR_DEVICE = range(6)
 MOE_DEVERR_EXPERT_ID, MOE_DEVERR_NONFINITE, MOE_DEVERR_SCHEDULE, MOE_DEVERR_TIMEOUT, MOE_DEVERR_RANGE = 1, 2, 4, 8, 16
+MOE_DEVERR_PAGES, MOE_DEVERR_CACHE = 32, 64
+MOE_ATTN_HEADER_BYTES = 4096
+MOE_ROPE_PLAIN, MOE_ROPE_LINEAR, MOE_ROPE_YARN = 0, 1, 2
 MOE_DT_F32, MOE_DT_BF16, MOE_DT_NVFP4 = 0, 1, 2
 MOE_NOALLOC_MAX_ROUTER_ELEMS = 131072
 MOE_NOALLOC_MAX_SPLIT_ELEMS = 7340032
@@ -48,6 +51,24 @@ class MoeWeights(ctypes.Structure):
         "w_up_sf", "w_down_sf", "w_up_gs", "w_down_gs", "w_sh_up", "w_sh_down", "w_down_g", "w_down_g_sf")]
 
 
+class MoeAttnConfig(ctypes.Structure):
+    _fields_ = [
+        ("n_heads", ctypes.c_int32),
+        ("n_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("n_pages", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("rot_dim", ctypes.c_int32),
+        ("rope_interleaved", ctypes.c_int32),
+        ("softmax_scale", ctypes.c_float),
+        ("dtype", ctypes.c_int32),
+        ("page_stride", ctypes.c_int64),
+        ("token_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+    ]
+
+
 class MoeGrads(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in (
         "d_router", "d_lat_down", "d_lat_up", "d_up", "d_down", "d_sh_up", "d_sh_down", "d_norm_w")]
@@ -60,6 +81,8 @@ EXPORTS = (
     "moe_launch_count", "moe_router_noalloc", "moe_workspace_region", "moe_set_nvfp4_act_terms",
     "moe_nvfp4_act_terms_for", "moe_block_forward", "moe_sparse_down_bytes", "moe_sparse_down_layout",
     "moe_backward_workspace_bytes", "moe_layer_backward", "moe_block_backward", "moe_backward_workspace_region",
+    "moe_check_attn_config", "moe_attn_workspace_bytes", "moe_paged_plan", "moe_rope_table", "moe_rope",
+    "moe_rope_append", "moe_tree_attention",
 )
 
 _lib = None
@@ -77,7 +100,10 @@ def load() -> ctypes.CDLL:
     P = ctypes.c_void_p
     I32 = ctypes.c_int32
     S = ctypes.c_size_t
+    I64 = ctypes.c_int64
+    F = ctypes.c_float
     CFG = ctypes.POINTER(MoeConfig)
+    ACFG = ctypes.POINTER(MoeAttnConfig)
     W = ctypes.POINTER(MoeWeights)
     sig = {
         "moe_version": (I32, []),
@@ -108,6 +134,13 @@ def load() -> ctypes.CDLL:
         "moe_workspace_region": (I32, [CFG, I32, I32, ctypes.POINTER(S), ctypes.POINTER(S)]),
         "moe_set_nvfp4_act_terms": (I32, [I32]),
         "moe_nvfp4_act_terms_for": (I32, [I32]),
+        "moe_check_attn_config": (I32, [ACFG]),
+        "moe_attn_workspace_bytes": (S, [ACFG]),
+        "moe_paged_plan": (I32, [ACFG, I32, I32, P, P, P, P, P, I32, P, P, P, P, P, P, P, I32, P, S, P]),
+        "moe_rope_table": (I32, [I32, ctypes.c_double, I32, ctypes.c_double, I64, P, ctypes.POINTER(F)]),
+        "moe_rope": (I32, [ACFG, I32, I32, P, I64, P, P, F, I32, P, I64, P]),
+        "moe_rope_append": (I32, [ACFG, I32, P, I64, P, I64, P, I64, P, P, F, P, P, I64, P, P, P, S, P]),
+        "moe_tree_attention": (I32, [ACFG, I32, I32, P, I64, P, P, P, P, P, P, I32, P, I64, P, P, S, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)

@@ -1,0 +1,217 @@
+"""Paged attention for verify blocks: the Python entry points of moe_paged_plan,
+moe_rope, moe_rope_append and moe_tree_attention, and a holder of one layer's
+paged KV cache.
+
+As in ``layer``: each function checks tensor placement, types and shapes, takes
+data pointers and the current CUDA stream, and calls the library.  Rows
+([T, heads, head_dim]) may be parts of a wider row, such as one projection's
+q, k and v; caches are views [n_pages, page_size, n_kv_heads, head_dim] of any
+layout whose head_dim is contiguous.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+from dataclasses import dataclass
+from typing import Optional, Tuple
+
+import torch
+
+from . import _native as N
+from .layer import _s
+
+_TORCH = {N.MOE_DT_BF16: torch.bfloat16, N.MOE_DT_F32: torch.float32}
+_SCALING = {None: N.MOE_ROPE_PLAIN, "linear": N.MOE_ROPE_LINEAR, "yarn": N.MOE_ROPE_YARN}
+
+
+def make_attn_config(n_heads: int, n_kv_heads: int, head_dim: int, *, page_size: int = 16, n_pages: int = 0,
+                     max_pages: int = 0, rot_dim: int = 0, rope_interleaved: bool = False,
+                     softmax_scale: Optional[float] = None, dtype: int = N.MOE_DT_BF16,
+                     k_cache: Optional[torch.Tensor] = None) -> N.MoeAttnConfig:
+    """A moe_attn_config_t.  The cache's strides are those of ``k_cache``
+    [n_pages, page_size, n_kv_heads, head_dim], or of a contiguous one;
+    ``softmax_scale`` defaults to 1 / sqrt(head_dim)."""
+    strides = ((page_size * n_kv_heads * head_dim, n_kv_heads * head_dim, head_dim) if k_cache is None
+               else k_cache.stride()[:3])
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(head_dim) if head_dim > 0 else 1.0
+    return N.MoeAttnConfig(n_heads, n_kv_heads, head_dim, page_size, n_pages, max_pages, rot_dim,
+                           int(rope_interleaved), float(softmax_scale), dtype, *strides)
+
+
+def attn_workspace_bytes(cfg: N.MoeAttnConfig) -> int:
+    n = int(N.load().moe_attn_workspace_bytes(ctypes.byref(cfg)))
+    if n == 0:
+        N.check(N.load().moe_check_attn_config(ctypes.byref(cfg)), "moe_attn_workspace_bytes")
+    return n
+
+
+def new_attn_workspace(cfg: N.MoeAttnConfig, device="cuda") -> torch.Tensor:
+    ws = torch.empty(attn_workspace_bytes(cfg), dtype=torch.uint8, device=device)
+    ws[:N.MOE_ATTN_HEADER_BYTES].zero_()
+    return ws
+
+
+def _array(t: Optional[torch.Tensor], dtype, n: Optional[int], name: str):
+    """Pointer of a contiguous device array of n values (None: any number)."""
+    if t is None:
+        return None
+    if not t.is_cuda or t.dtype is not dtype or not t.is_contiguous() or (n is not None and t.numel() != n):
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor"
+                         + ("" if n is None else f" of {n} values"))
+    return t.data_ptr()
+
+
+def _rows(cfg, t: torch.Tensor, T: int, heads: int, name: str) -> Tuple[int, int]:
+    """(pointer, row stride) of rows [T, heads, head_dim]."""
+    D = cfg.head_dim
+    if not t.is_cuda or t.dtype is not _TORCH.get(cfg.dtype) or t.shape != (T, heads, D):
+        raise ValueError(f"{name} must be a {_TORCH.get(cfg.dtype)} CUDA tensor of shape {(T, heads, D)}")
+    ld, step, one = t.stride()
+    if (one != 1 and D > 1) or (heads > 1 and step != D):
+        raise ValueError(f"the heads of a row of {name} must be contiguous")
+    return t.data_ptr(), (ld if T > 1 else heads * D)
+
+
+def _cache(cfg, t: torch.Tensor, name: str) -> int:
+    shape = (cfg.n_pages, cfg.page_size, cfg.n_kv_heads, cfg.head_dim)
+    if not t.is_cuda or t.dtype is not _TORCH.get(cfg.dtype) or t.shape != shape:
+        raise ValueError(f"{name} must be a {_TORCH.get(cfg.dtype)} CUDA tensor of shape {shape}")
+    if t.stride() != (cfg.page_stride, cfg.token_stride, cfg.head_stride, 1):
+        raise ValueError(f"{name} does not have the configuration's strides")
+    return t.data_ptr()
+
+
+def moe_paged_plan(cfg, ctx_len, new_len, block_table, free_pages, free_head, q_start, kv_len, positions, slot_map,
+                   ws, free_head_out=None, parents=None, tree_mask=None, stream=None):
+    """Block tables, slots, positions and tree masks of a step, written into
+    block_table, q_start, kv_len, positions, slot_map, tree_mask and
+    free_head_out (default: free_head, in place)."""
+    R, T, i32 = ctx_len.shape[0], positions.shape[0], torch.int32
+    words = 0 if tree_mask is None else tree_mask.shape[1]
+    N.check(N.load().moe_paged_plan(
+        ctypes.byref(cfg), R, T, _array(ctx_len, i32, R, "ctx_len"), _array(new_len, i32, R, "new_len"),
+        _array(parents, i32, T, "parents"), _array(block_table, i32, R * cfg.max_pages, "block_table"),
+        _array(free_pages, i32, None, "free_pages"), free_pages.numel(), _array(free_head, i32, 1, "free_head"),
+        _array(free_head if free_head_out is None else free_head_out, i32, 1, "free_head_out"),
+        _array(q_start, i32, R + 1, "q_start"), _array(kv_len, i32, R, "kv_len"),
+        _array(positions, i32, T, "positions"), _array(slot_map, torch.int64, T, "slot_map"),
+        _array(tree_mask, i32, T * words, "tree_mask"), words, _array(ws, torch.uint8, None, "ws"), ws.numel(),
+        _s(stream)), "moe_paged_plan")
+
+
+def rope_table(rot_dim: int, theta: float, *, scaling: Optional[str] = None, factor: float = 1.0,
+               original_context: int = 0, device="cuda") -> Tuple[torch.Tensor, float]:
+    """(table on ``device``, rot_scale) of moe_rope_table; scaling: None, "linear" or "yarn"."""
+    if scaling not in _SCALING:
+        raise ValueError(f"unknown rotary scaling {scaling!r}")
+    host = torch.zeros(max(rot_dim // 2, 1), dtype=torch.int64)
+    scale = ctypes.c_float(1.0)
+    N.check(N.load().moe_rope_table(rot_dim, float(theta), _SCALING[scaling], float(factor), int(original_context),
+                                    host.data_ptr(), ctypes.byref(scale)), "moe_rope_table")
+    return host.to(device), float(scale.value)
+
+
+def _table(cfg, table):
+    if cfg.rot_dim == 0:
+        return None
+    if table is None:
+        raise ValueError("table is missing")
+    return _array(table, torch.int64, cfg.rot_dim // 2, "table")
+
+
+def moe_rope(cfg, x, positions, table, out, rot_scale: float = 1.0, inverse: bool = False, stream=None):
+    """Rows x [T, heads, head_dim] turned by their positions into ``out`` (which
+    may be x); ``inverse`` is the backward."""
+    T, heads = x.shape[0], x.shape[1]
+    xp, x_ld = _rows(cfg, x, T, heads, "x")
+    op, o_ld = _rows(cfg, out, T, heads, "out")
+    N.check(N.load().moe_rope(ctypes.byref(cfg), T, heads, xp, x_ld, _array(positions, torch.int32, T, "positions"),
+                              _table(cfg, table), rot_scale, int(inverse), op, o_ld, _s(stream)), "moe_rope")
+
+
+def moe_rope_append(cfg, q, k, v, positions, table, slot_map, k_cache, v_cache, q_out, ws, rot_scale: float = 1.0,
+                    stream=None):
+    """q turned into q_out (which may be q); k turned and v as it is into the
+    caches at slot_map."""
+    T = q.shape[0]
+    qp, q_ld = _rows(cfg, q, T, cfg.n_heads, "q")
+    kp, k_ld = _rows(cfg, k, T, cfg.n_kv_heads, "k")
+    vp, v_ld = _rows(cfg, v, T, cfg.n_kv_heads, "v")
+    op, o_ld = _rows(cfg, q_out, T, cfg.n_heads, "q_out")
+    N.check(N.load().moe_rope_append(ctypes.byref(cfg), T, qp, q_ld, kp, k_ld, vp, v_ld,
+                                     _array(positions, torch.int32, T, "positions"), _table(cfg, table), rot_scale,
+                                     _array(slot_map, torch.int64, T, "slot_map"), op, o_ld,
+                                     _cache(cfg, k_cache, "k_cache"), _cache(cfg, v_cache, "v_cache"),
+                                     _array(ws, torch.uint8, None, "ws"), ws.numel(), _s(stream)), "moe_rope_append")
+
+
+def moe_tree_attention(cfg, q, q_start, kv_len, block_table, k_cache, v_cache, out, ws, tree_mask=None, lse=None,
+                       stream=None):
+    """out [T, n_heads, head_dim] (and lse [T, n_heads] FP32) of the rows q over the cache."""
+    T, R, i32 = q.shape[0], kv_len.shape[0], torch.int32
+    words = 0 if tree_mask is None else tree_mask.shape[1]
+    qp, q_ld = _rows(cfg, q, T, cfg.n_heads, "q")
+    op, o_ld = _rows(cfg, out, T, cfg.n_heads, "out")
+    N.check(N.load().moe_tree_attention(
+        ctypes.byref(cfg), R, T, qp, q_ld, _array(q_start, i32, R + 1, "q_start"), _array(kv_len, i32, R, "kv_len"),
+        _array(block_table, i32, R * cfg.max_pages, "block_table"), _cache(cfg, k_cache, "k_cache"),
+        _cache(cfg, v_cache, "v_cache"), _array(tree_mask, i32, T * words, "tree_mask"), words, op, o_ld,
+        _array(lse, torch.float32, T * cfg.n_heads, "lse"), _array(ws, torch.uint8, None, "ws"), ws.numel(),
+        _s(stream)), "moe_tree_attention")
+
+
+@dataclass
+class PagedStep:
+    """What PagedKVCache.plan leaves for the other calls of a step."""
+    q_start: torch.Tensor               # [R + 1]
+    kv_len: torch.Tensor                # [R]
+    positions: torch.Tensor             # [T]
+    slot_map: torch.Tensor              # [T]
+    tree_mask: Optional[torch.Tensor]   # [T, words]
+
+
+class PagedKVCache:
+    """One attention layer's paged KV cache: the pages, the requests' block
+    tables, the free pages and the workspace.  A step is plan -> append -> attend,
+    all on the current stream, nothing on the host."""
+
+    def __init__(self, cfg: N.MoeAttnConfig, max_requests: int, device="cuda", theta: float = 10000.0, **scaling):
+        self.cfg = cfg
+        shape = (cfg.n_pages, cfg.page_size, cfg.n_kv_heads, cfg.head_dim)
+        dt = _TORCH[cfg.dtype]
+        self.k_cache = torch.zeros(shape, dtype=dt, device=device)
+        self.v_cache = torch.zeros(shape, dtype=dt, device=device)
+        self.block_table = torch.full((max_requests, cfg.max_pages), -1, dtype=torch.int32, device=device)
+        self.free_pages = torch.arange(cfg.n_pages, dtype=torch.int32, device=device)
+        self.free_head = torch.zeros(1, dtype=torch.int32, device=device)
+        self.ws = new_attn_workspace(cfg, device)
+        self.table, self.rot_scale = rope_table(cfg.rot_dim, theta, device=device, **scaling)
+
+    def plan(self, ctx_len, new_len, T: int, parents=None, max_nodes: int = 32, stream=None) -> PagedStep:
+        """ctx_len, new_len [R] (R = max_requests; idle requests bring 0 tokens);
+        T rows; parents [T]: trees of up to max_nodes nodes."""
+        R, dev = self.block_table.shape[0], self.block_table.device
+
+        def new(*shape, dtype=torch.int32):
+            return torch.empty(shape, dtype=dtype, device=dev)
+
+        step = PagedStep(new(R + 1), new(R), new(T), new(T, dtype=torch.int64),
+                         None if parents is None else new(T, -(-max_nodes // 32)))
+        moe_paged_plan(self.cfg, ctx_len, new_len, self.block_table, self.free_pages, self.free_head, step.q_start,
+                       step.kv_len, step.positions, step.slot_map, self.ws, parents=parents,
+                       tree_mask=step.tree_mask, stream=stream)
+        return step
+
+    def append(self, step: PagedStep, q, k, v, q_out=None, stream=None) -> torch.Tensor:
+        """Rotated queries; the keys and values of the step are in the cache after it."""
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+        moe_rope_append(self.cfg, q, k, v, step.positions, self.table, step.slot_map, self.k_cache, self.v_cache,
+                        q_out, self.ws, rot_scale=self.rot_scale, stream=stream)
+        return q_out
+
+    def attend(self, step: PagedStep, q, out=None, lse=None, stream=None) -> torch.Tensor:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else out
+        moe_tree_attention(self.cfg, q, step.q_start, step.kv_len, self.block_table, self.k_cache, self.v_cache, out,
+                           self.ws, tree_mask=step.tree_mask, lse=lse, stream=stream)
+        return out
