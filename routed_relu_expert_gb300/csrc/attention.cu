@@ -260,8 +260,5 @@ cudaError_t launch_t(const AttnArgs& a, cudaStream_t s) {
 cudaError_t launch_attention_f32(const AttnArgs& a, cudaStream_t s) {
   return a.T > 0 ? launch_t<float>(a, s) : cudaSuccess;
 }
-cudaError_t launch_attention_bf16(const AttnArgs& a, cudaStream_t s) {
-  return a.T > 0 ? launch_t<bf16>(a, s) : cudaSuccess;
-}
 
 }  // namespace moe

@@ -1,0 +1,851 @@
+// Tree attention over a paged cache on the tensor cores (tcgen05, BF16 rows and
+// caches, FP32 scores, softmax and sums).
+//
+//   S = Q K^T,  p = exp2(c S - m),  l = sum p,  O = sum p V,  out = O / l
+//   c = softmax_scale log2(e); m a running upper reference of c S (below)
+//
+// Rows.  A unit is (request, KV head, block of up to 128 / G nodes): its nodes'
+// G query heads are the 128 rows of one MMA tile, so a KV head's keys are read
+// once for all of them.
+//
+// Work.  A unit's keys are tiles of 128.  The tiles of all units, in order, are
+// cut into equal runs, one per CTA (one CTA an SM): the lengths are read on the
+// device, no call needs them on the host, and every SM streams the same number
+// of keys whatever the batch.  A unit cut by a run's end leaves FP32 partials (at
+// most two a CTA) and a second small kernel adds them in run order.
+//
+// Inside a CTA: warp 8 brings K and V tiles into a ring by TMA, a box per page
+// and 64-wide half (any page size from 8 on; the table's entries are fetched a
+// tile ahead); one thread of warp 9 issues the MMAs; warps 0-3 and 4-7 are two
+// softmax groups that take the unit's tiles in turn, a thread a row, each with
+// its own S, P and O in tensor memory and its own running maximum, so that one
+// group's exponentials run beside the other's products.  P goes back to tensor
+// memory as the A operand of P V; V is the MN-major B operand as it lies.
+//
+// The reference m of a row follows its maximum only when that rose by more than
+// 2^8: below that p and the sums just grow by at most 2^8, exactly undone by the
+// division, and O is left alone.
+//
+// Masked places.  Only the tiles that hold nodes or end past the last key look
+// at masks; there, V rows past the last key are zeroed in shared memory (P is 0,
+// but 0 x NaN is not), and V rows of nodes that are not finite are zeroed too and
+// added by hand to the rows that see them.
+#include "attn.h"
+#include "tc_common.cuh"
+
+#include <algorithm>
+
+namespace moe {
+
+namespace {
+
+using namespace tc;
+
+constexpr int kTile = 128;                     // keys a tile
+constexpr int kHalfBytes = kTile * 128;        // 128 rows of 64 BF16
+constexpr int kSoftWarps = 8;
+constexpr int kThreads = 32 * (kSoftWarps + 2);
+constexpr uint32_t kTmemCols = 512;
+constexpr float kRaise = 8.f;                  // log2 units by which a maximum may pass its reference
+constexpr int kMaxSmem = 232448;
+
+template <int DP>
+struct Geo {
+  static constexpr int NH = DP / 64;                       // 64-wide halves of a head
+  static constexpr int SLOT = NH * kHalfBytes;             // a K or V tile
+  static constexpr int SLOTS = DP == 128 ? 5 : 10;         // 160 KB in flight
+  static constexpr int RING = SLOTS * SLOT;
+  static constexpr uint32_t O0 = 256;
+  static constexpr bool ALIAS = DP == 128;                 // P lies in its S (tensor memory is full)
+  static __host__ __device__ constexpr uint32_t s_col(int w) { return 128u * w; }
+  static __host__ __device__ constexpr uint32_t p_col(int w) { return ALIAS ? 128u * w : 384u + 64u * w; }
+  static __host__ __device__ constexpr uint32_t o_col(int w) { return O0 + (uint32_t)(DP * w); }
+};
+
+struct Maps {
+  CUtensorMap q, k, v;
+};
+
+// fixed shared-memory words after the tiles
+struct Small {
+  uint64_t full[10], empty[10];
+  uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done[2], o_free, meet, group[2], drain;
+  float2 ml[2][2][kAttnRows];                  // [piece parity][group][row] (reference, sum)
+  uint32_t odd[2][4];                          // nodes of the tile whose V is not finite
+  uint32_t tmem;
+  int abort;
+  int scan[16];
+};
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+      : "memory");
+}
+
+// D[tmem] (+)= A[tmem] B[shared]
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+#define R32(r, o)                                                                                                   \
+  r[o + 0], r[o + 1], r[o + 2], r[o + 3], r[o + 4], r[o + 5], r[o + 6], r[o + 7], r[o + 8], r[o + 9], r[o + 10],     \
+      r[o + 11], r[o + 12], r[o + 13], r[o + 14], r[o + 15], r[o + 16], r[o + 17], r[o + 18], r[o + 19], r[o + 20],  \
+      r[o + 21], r[o + 22], r[o + 23], r[o + 24], r[o + 25], r[o + 26], r[o + 27], r[o + 28], r[o + 29], r[o + 30],  \
+      r[o + 31]
+
+// 32 columns of this thread's lane, without waiting for them
+template <int O, int N>
+__device__ __forceinline__ void ld32_async(uint32_t taddr, float (&v)[N]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(v[O + 0]), "=f"(v[O + 1]), "=f"(v[O + 2]), "=f"(v[O + 3]), "=f"(v[O + 4]), "=f"(v[O + 5]),
+        "=f"(v[O + 6]), "=f"(v[O + 7]), "=f"(v[O + 8]), "=f"(v[O + 9]), "=f"(v[O + 10]), "=f"(v[O + 11]),
+        "=f"(v[O + 12]), "=f"(v[O + 13]), "=f"(v[O + 14]), "=f"(v[O + 15]), "=f"(v[O + 16]), "=f"(v[O + 17]),
+        "=f"(v[O + 18]), "=f"(v[O + 19]), "=f"(v[O + 20]), "=f"(v[O + 21]), "=f"(v[O + 22]), "=f"(v[O + 23]),
+        "=f"(v[O + 24]), "=f"(v[O + 25]), "=f"(v[O + 26]), "=f"(v[O + 27]), "=f"(v[O + 28]), "=f"(v[O + 29]),
+        "=f"(v[O + 30]), "=f"(v[O + 31])
+      : "r"(taddr));
+}
+// waits for this thread's loads; the values pass through it, so that no use of
+// them can move above the wait
+template <int O, int N>
+__device__ __forceinline__ void ld32_wait(float (&v)[N]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[O + 0]), "+f"(v[O + 1]), "+f"(v[O + 2]), "+f"(v[O + 3]), "+f"(v[O + 4]), "+f"(v[O + 5]),
+                 "+f"(v[O + 6]), "+f"(v[O + 7]), "+f"(v[O + 8]), "+f"(v[O + 9]), "+f"(v[O + 10]), "+f"(v[O + 11]),
+                 "+f"(v[O + 12]), "+f"(v[O + 13]), "+f"(v[O + 14]), "+f"(v[O + 15]), "+f"(v[O + 16]), "+f"(v[O + 17]),
+                 "+f"(v[O + 18]), "+f"(v[O + 19]), "+f"(v[O + 20]), "+f"(v[O + 21]), "+f"(v[O + 22]), "+f"(v[O + 23]),
+                 "+f"(v[O + 24]), "+f"(v[O + 25]), "+f"(v[O + 26]), "+f"(v[O + 27]), "+f"(v[O + 28]), "+f"(v[O + 29]),
+                 "+f"(v[O + 30]), "+f"(v[O + 31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void st32(uint32_t taddr, const float (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+      "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]),
+      "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]),
+      "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31])
+      : "memory");
+}
+__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// shared-memory descriptor of V as the MN-major B operand: 64 values of a key
+// contiguous (one 128-byte swizzle row), 8-key groups 1024 B apart (stride), the
+// next 64 values of the head a half further (leading)
+__device__ __forceinline__ uint64_t v_desc(uint32_t addr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((addr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(kHalfBytes >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+// ---------------------------------------------------------------------------
+// the walk over a CTA's run of tiles
+// ---------------------------------------------------------------------------
+struct Req {
+  int q0, n, kv, ctx, tiles, blocks;
+};
+__device__ __forceinline__ Req request(const AttnArgs& a, int r, int tb, int* bad) {
+  Req q;
+  q.q0 = min(max(a.q_start[r], 0), a.T);
+  const int q1 = min(max(a.q_start[r + 1], q.q0), a.T);
+  q.n = q1 - q.q0;
+  const int64_t cap = (int64_t)a.max_pages << a.page_shift;
+  const int kv = a.kv_len[r];
+  q.kv = (int)min((int64_t)max(kv, q.n), cap);
+  if (bad && (q.kv != kv || q.q0 != a.q_start[r])) *bad = 1;
+  q.ctx = max(q.kv - q.n, 0);
+  q.tiles = max((q.kv + kTile - 1) / kTile, 1);
+  q.blocks = (q.n + tb - 1) / tb;
+  return q;
+}
+
+struct Piece {
+  Req q;
+  int r, h, tok0, ntok;    // the block's first node and its nodes
+  int t0, n;               // first tile and number of tiles (those that a chain's block can see)
+  int unit, parts;         // position of the unit's first tile; tiles of the whole unit
+  bool starts, ends;
+};
+
+// piece at position `pos` of a run that ends at `end`; moves pos behind it
+__device__ __forceinline__ Piece next_piece(const AttnArgs& a, const int* prefix, int tb, int& pos, int end) {
+  Piece p;
+  int lo = 0, hi = a.R;                        // prefix[lo] <= pos < prefix[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (prefix[mid] <= pos) lo = mid; else hi = mid;
+  }
+  p.r = lo;
+  p.q = request(a, lo, tb, nullptr);
+  const int local = pos - prefix[lo];
+  const int u = local / p.q.tiles;
+  p.t0 = local - u * p.q.tiles;
+  p.h = u / p.q.blocks;
+  p.tok0 = (u - p.h * p.q.blocks) * tb;
+  p.ntok = min(tb, p.q.n - p.tok0);
+  const int len = min(p.q.tiles - p.t0, end - pos);
+  p.starts = p.t0 == 0;
+  p.ends = p.t0 + len == p.q.tiles;
+  p.unit = pos - p.t0;
+  p.parts = p.q.tiles;
+  pos += len;
+  int t1 = p.t0 + len;
+  if (!a.tree_mask) t1 = min(t1, (p.q.ctx + p.tok0 + p.ntok + kTile - 1) / kTile);
+  p.n = max(t1 - p.t0, 0);
+  return p;
+}
+
+// order of a piece's tiles in the ring: K0, [K1, V0], [K2, V1], ..., V(n-1)
+__device__ __forceinline__ int v_item(int j, int n) { return j == n - 1 ? 2 * n - 1 : 2 * j + 2; }
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+    attention_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a, int tb) {
+  using X = Geo<DP>;
+  constexpr int NS = X::SLOTS;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t q_smem = (raw + 1023u) & ~1023u;
+  uint8_t* q_ptr = smem_raw + (q_smem - raw);
+  const uint32_t ring = q_smem + X::SLOT;
+  uint8_t* ring_ptr = q_ptr + X::SLOT;
+  Small& sm = *reinterpret_cast<Small*>(ring_ptr + X::RING);
+  int* prefix = reinterpret_cast<int*>(&sm + 1);           // [R + 1]
+  volatile int* abort_flag = &sm.abort;
+  int32_t* err = &a.hdr->err;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto bar = [&](uint64_t& b) { return smem_u32(&b); };
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(bar(sm.full[s]), 1);
+      mbar_init(bar(sm.empty[s]), 1);
+    }
+    mbar_init(bar(sm.q_full), 1);
+    mbar_init(bar(sm.q_empty), 1);
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(bar(sm.s_full[w]), 1);
+      mbar_init(bar(sm.p_full[w]), 4);
+      mbar_init(bar(sm.pv_done[w]), 1);
+      mbar_init(bar(sm.group[w]), 4);
+    }
+    mbar_init(bar(sm.o_free), kSoftWarps);
+    mbar_init(bar(sm.meet), kSoftWarps);
+    mbar_init(bar(sm.drain), 1);
+    sm.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  pdl_wait();
+  // tiles before each request
+  {
+    int bad = 0;
+    const int per = (a.R + kThreads - 1) / kThreads, r0 = min((int)threadIdx.x * per, a.R), r1 = min(r0 + per, a.R);
+    int local = 0;
+    for (int r = r0; r < r1; ++r) {
+      const Req q = request(a, r, tb, &bad);
+      local += q.tiles * q.blocks * a.Hkv;
+    }
+    int x = local;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, off);
+      if (lane >= off) x += y;
+    }
+    if (lane == 31) sm.scan[warp] = x;
+    __syncthreads();
+    int run = x - local;
+    for (int w = 0; w < warp; ++w) run += sm.scan[w];
+    for (int r = r0; r < r1; ++r) {
+      prefix[r] = run;
+      const Req q = request(a, r, tb, nullptr);
+      run += q.tiles * q.blocks * a.Hkv;
+    }
+    if (threadIdx.x == kThreads - 1) prefix[a.R] = run;
+    if (bad && blockIdx.x == 0) set_error(err, MOE_DEVERR_CACHE);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+  const int total = prefix[a.R];
+  const int runs = min((int)gridDim.x, max(total, 1));
+  auto run_start = [&](int c) { return (int)((int64_t)c * total / runs); };
+  // the run that holds position t
+  auto owner = [&](int t) { return (int)((((int64_t)t + 1) * runs - 1) / total); };
+  const bool idle = (int)blockIdx.x >= runs;
+  const int begin = idle ? 0 : run_start(blockIdx.x), end = idle ? 0 : run_start(blockIdx.x + 1);
+
+  if (warp == 8) {
+    // ---------------- K, V (and Q) into shared memory ----------------
+    const int page = 1 << a.page_shift, rows = min(page, kTile);
+    const int per_tile = kTile / rows;                     // boxes of a tile: lane l < per_tile has box l
+    int slot = 0, it = 0, pieces = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int pos = begin; pos < end && ok;) {
+      const Piece p = next_piece(a, prefix, tb, pos, end);
+      if (p.n == 0) continue;
+      const int32_t* table = a.block_table + (int64_t)p.r * a.max_pages;
+      // page of this lane's box of tile j (of the piece); -1: nothing to load
+      auto page_of = [&](int j) {
+        const int tok = (p.t0 + j) * kTile + lane * rows;
+        if (j >= p.n || lane >= per_tile || tok >= p.q.kv) return -1;
+        const int id = table[tok >> a.page_shift];
+        if (id >= 0 && id < a.n_pages) return id;
+        set_error(err, MOE_DEVERR_CACHE);
+        return a.n_pages;                                  // past the last page: TMA fills zeros
+      };
+      int id[3] = {page_of(0), page_of(1), -1};            // tiles j, j + 1, j + 2
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(sm.q_empty), (pieces & 1) ^ 1, abort_flag, err));
+      if (!ok) break;
+      if (lane == 0) {
+        mbar_expect_tx(bar(sm.q_full), (uint32_t)(X::NH * 128 * a.G * tb));
+#pragma unroll
+        for (int hh = 0; hh < X::NH; ++hh)
+          tma_load_3d(q_smem + hh * kHalfBytes, &maps.q, 64 * hh, p.h * a.G, p.q.q0 + p.tok0, bar(sm.q_full));
+      }
+      ++pieces;
+      auto load = [&](const CUtensorMap* map, int j, int pid) {
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(sm.empty[slot]), phase ^ 1u, abort_flag, err));
+        if (!ok) return;
+        const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, pid >= 0));
+        if (lane == 0) mbar_expect_tx(bar(sm.full[slot]), boxes * (uint32_t)(X::NH * 128 * rows));
+        __syncwarp();
+        if (pid >= 0) {
+          const int off = ((p.t0 + j) * kTile + lane * rows) & (page - 1);
+          const uint32_t dst = ring + (uint32_t)(slot * X::SLOT + lane * rows * 128);
+#pragma unroll
+          for (int hh = 0; hh < X::NH; ++hh)
+            tma_load_4d(dst + hh * kHalfBytes, map, 64 * hh, off, p.h, pid, bar(sm.full[slot]));
+        }
+        __syncwarp();
+        ++it;
+        if (++slot == NS) {
+          slot = 0;
+          phase ^= 1u;
+        }
+      };
+      load(&maps.k, 0, id[0]);
+      for (int j = 0; j < p.n && ok; ++j) {
+        id[2] = page_of(j + 2);
+        if (j + 1 < p.n) load(&maps.k, j + 1, id[1]);
+        if (ok) load(&maps.v, j, id[0]);
+        id[0] = id[1];
+        id[1] = id[2];
+      }
+    }
+    if (!ok && lane == 0) {
+      // copies in flight must land before the CTA leaves
+      auto land = [&](uint32_t b, uint32_t parity) {
+        const uint64_t t0 = globaltimer();
+        while (!mbar_try(b, parity) && globaltimer() - t0 < kWaitLimitNs) {
+        }
+      };
+      for (int s = 0; s < NS; ++s) {
+        const int uses = (it - s + NS - 1) / NS;           // times that slot s was filled
+        if (it > s) land(bar(sm.full[s]), (uint32_t)(uses - 1) & 1u);
+      }
+      if (pieces > 0) land(bar(sm.q_full), (uint32_t)(pieces - 1) & 1u);
+    }
+  } else if (warp == 9) {
+    // ---------------- MMA issuer ----------------
+    if (lane == 0) {
+      const uint32_t id_s = idesc_f16kind(kAttnRows, kTile, false);
+      const uint32_t id_o = idesc_f16kind(kAttnRows, DP, false) | (1u << 16);      // B is MN-major
+      int slot = 0, pieces = 0;
+      uint32_t phase = 0;
+      int done[2] = {0, 0};                                // tiles of each group so far
+      bool ok = true, issued = false;
+      auto wait = [&](uint64_t& b, uint32_t parity) {
+        ok = ok && mbar_wait<false, true>(bar(b), parity, abort_flag, err);
+        return ok;
+      };
+      auto advance = [&]() {
+        if (++slot == NS) {
+          slot = 0;
+          phase ^= 1u;
+        }
+      };
+      for (int pos = begin; pos < end && ok;) {
+        const Piece p = next_piece(a, prefix, tb, pos, end);
+        if (p.n == 0) continue;
+        if (!wait(sm.q_full, pieces & 1)) break;
+        auto scores = [&](int j) {
+          const int w = j & 1;
+          if (!wait(sm.full[slot], phase)) return;
+          // P lies in S: the products that read it must be done
+          if (X::ALIAS && done[w] > 0 && !wait(sm.pv_done[w], (done[w] - 1) & 1)) return;
+          tc_fence_after();
+          const uint32_t kb = ring + (uint32_t)(slot * X::SLOT);
+#pragma unroll
+          for (int hh = 0; hh < X::NH; ++hh) {
+            const uint64_t da = smem_desc_sw128(q_smem + hh * kHalfBytes), db = smem_desc_sw128(kb + hh * kHalfBytes);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              tc_mma<1>(tmem + X::s_col(w), da + 2u * k, db + 2u * k, id_s, (hh | k) != 0);
+          }
+          issued = true;
+          tc_commit<1>(bar(sm.empty[slot]));
+          tc_commit<1>(bar(sm.s_full[w]));
+          if (j == p.n - 1) tc_commit<1>(bar(sm.q_empty));
+          advance();
+        };
+        scores(0);
+        for (int j = 0; j < p.n && ok; ++j) {
+          if (j + 1 < p.n) scores(j + 1);
+          const int w = j & 1;
+          if (!wait(sm.full[slot], phase) || !wait(sm.p_full[w], done[w] & 1)) break;
+          // O of the previous piece has been read
+          if (j < 2 && !wait(sm.o_free, (pieces & 1) ^ 1)) break;
+          tc_fence_after();
+          const uint32_t vb = ring + (uint32_t)(slot * X::SLOT);
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k)
+            mma_ts(tmem + X::o_col(w), tmem + X::p_col(w) + 8u * k, v_desc(vb + 2048u * k), id_o, (j >= 2 || k) ? 1u : 0u);
+          tc_commit<1>(bar(sm.empty[slot]));
+          tc_commit<1>(bar(sm.pv_done[w]));
+          ++done[w];
+          advance();
+        }
+        ++pieces;
+      }
+      if (!ok && issued) {
+        tc_commit<1>(bar(sm.drain));
+        const uint64_t t0 = globaltimer();
+        while (!mbar_try(bar(sm.drain), 0u) && globaltimer() - t0 < kWaitLimitNs) {
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---------------- softmax: group w = warps 4w .. 4w + 3, a thread a row ----------------
+    const int w = warp >> 2, qd = warp & 3, row = 32 * qd + lane;
+    const uint32_t lane_addr = (uint32_t)(32 * qd) << 16;
+    const float c = a.scale * 1.4426950408889634f;
+    // rows that belong to no request
+    {
+      const int live = a.R > 0 ? min(max(a.q_start[a.R], 0), a.T) : 0;
+      for (int t = live + blockIdx.x; t < a.T; t += gridDim.x) {
+        bf16* o = reinterpret_cast<bf16*>(a.out) + (int64_t)t * a.out_ld;
+        for (int i = threadIdx.x * 8; i < a.H * a.D; i += 32 * kSoftWarps * 8)
+          *reinterpret_cast<uint4*>(o + i) = make_uint4(0, 0, 0, 0);
+        if (a.lse)
+          for (int i = threadIdx.x; i < a.H; i += 32 * kSoftWarps) a.lse[(int64_t)t * a.H + i] = -INFINITY;
+      }
+    }
+    int tiles = 0, other = 0, items = 0, meets = 0, groups = 0;
+    bool ok = true, joins = false;
+    auto wait = [&](uint64_t& b, uint32_t parity) {
+      ok = __all_sync(0xffffffffu, mbar_wait<false, true>(bar(b), parity, abort_flag, err));
+      return ok;
+    };
+    auto arrive = [&](uint64_t& b) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(b));
+    };
+    for (int pos = begin; pos < end && ok;) {
+      const Piece p = next_piece(a, prefix, tb, pos, end);
+      const int valid = p.ntok * a.G;
+      const bool live_warp = 32 * qd < valid;
+      const int node = p.tok0 + row / a.G;
+      const int32_t* mask = a.tree_mask ? a.tree_mask + (int64_t)(p.q.q0 + min(node, p.q.n - 1)) * a.mask_words : nullptr;
+      float mc = -INFINITY, l = 0.f;
+      for (int j = w; j < p.n; j += 2) {
+        const int key0 = (p.t0 + j) * kTile;
+        const bool special = key0 + kTile > p.q.ctx;
+        uint32_t odd[4] = {0, 0, 0, 0};
+        if (special) {
+          // V rows past the last key, and nodes' rows that are not finite, become zeros
+          const int item = items + v_item(j, p.n);
+          if (!wait(sm.full[item % NS], (uint32_t)(item / NS) & 1u)) break;
+          const int key = key0 + row;
+          uint4* v0 = reinterpret_cast<uint4*>(ring_ptr + (item % NS) * X::SLOT + row * 128);
+          bool zero = key >= p.q.kv, strange = false;
+          if (!zero && key >= p.q.ctx) {
+            uint32_t hit = 0;
+#pragma unroll
+            for (int hh = 0; hh < X::NH; ++hh)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const uint4 x = v0[hh * (kHalfBytes / 16) + i];
+                const uint32_t ws[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  hit |= ((ws[e] & 0x7F80u) == 0x7F80u) | ((ws[e] & 0x7F800000u) == 0x7F800000u);
+              }
+            strange = hit != 0;
+          }
+          if (zero || strange) {
+#pragma unroll
+            for (int hh = 0; hh < X::NH; ++hh)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v0[hh * (kHalfBytes / 16) + i] = make_uint4(0, 0, 0, 0);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          const uint32_t mine = __ballot_sync(0xffffffffu, strange);
+          if (lane == 0) sm.odd[w][qd] = mine;
+          arrive(sm.group[w]);
+          if (!wait(sm.group[w], groups & 1)) break;
+          ++groups;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) odd[i] = *reinterpret_cast<volatile uint32_t*>(&sm.odd[w][i]);
+        }
+        if (!wait(sm.s_full[w], tiles & 1)) break;
+        const bool any_odd = (odd[0] | odd[1] | odd[2] | odd[3]) != 0;
+        float pl[kTile];                       // the row's p where the tile has odd nodes; untouched otherwise
+        if (live_warp) {
+          tc_fence_after();
+          float v[kTile];
+          const uint32_t s_addr = tmem + lane_addr + X::s_col(w);
+          ld32_async<0>(s_addr, v);
+          ld32_async<32>(s_addr + 32, v);
+          ld32_async<64>(s_addr + 64, v);
+          ld32_async<96>(s_addr + 96, v);
+          ld32_wait<0>(v);
+          ld32_wait<32>(v);
+          ld32_wait<64>(v);
+          ld32_wait<96>(v);
+          if (special) {
+#pragma unroll
+            for (int cc = 0; cc < 4; ++cc) {
+              const int k0 = key0 + 32 * cc, j0 = k0 - p.q.ctx;   // first key of the word, as a node
+              auto low = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
+              uint32_t bits;
+              if (!mask) {
+                bits = low(node + 1 - j0);
+              } else {
+                auto word = [&](int i) { return i < 0 ? 0xffffffffu : i < a.mask_words ? (uint32_t)mask[i] : 0u; };
+                const int wi = j0 >> 5;
+                bits = j0 + 32 <= 0 ? 0xffffffffu : __funnelshift_r(word(wi), word(wi + 1), (uint32_t)(j0 & 31));
+              }
+              bits &= low(p.q.kv - k0);
+              if (bits != 0xffffffffu) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (!(bits >> i & 1u)) v[32 * cc + i] = -INFINITY;
+              }
+            }
+          }
+          float top = v[0];
+#pragma unroll
+          for (int i = 1; i < kTile; ++i) top = fmaxf(top, v[i]);
+          top *= c;
+          const bool first = j == w;
+          const bool raise = top > mc + kRaise || (mc == -INFINITY && top > mc);
+          const float f = raise ? (mc == -INFINITY ? 0.f : ex2(mc - top)) : 1.f;
+          if (raise) {
+            mc = top;
+            l *= f;
+          }
+          if (!first && __any_sync(0xffffffffu, raise)) {
+            // O of this group after its previous tile, scaled to the new reference
+            if (!wait(sm.pv_done[w], (tiles - 1) & 1)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int c0 = 0; c0 < DP; c0 += 32) {
+              float o[32];
+              const uint32_t addr = tmem + lane_addr + X::o_col(w) + c0;
+              ld32_async<0>(addr, o);
+              ld32_wait<0>(o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] *= f;
+              st32(addr, o);
+            }
+          }
+          const float base = mc == -INFINITY ? 0.f : mc;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int cc = 0; cc < 4; ++cc) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float x = ex2(fmaf(v[32 * cc + 2 * i], c, -base)), y = ex2(fmaf(v[32 * cc + 2 * i + 1], c, -base));
+              sum[(2 * i) & 3] += x;
+              sum[(2 * i + 1) & 3] += y;
+              pk[i] = pack_bf16(x, y);
+              v[32 * cc + 2 * i] = x;
+              v[32 * cc + 2 * i + 1] = y;
+            }
+            if (any_odd) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) pl[32 * cc + i] = v[32 * cc + i];
+            }
+            st16(tmem + lane_addr + X::p_col(w) + 16 * cc, pk);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          st_wait();
+          tc_fence_before();
+        }
+        arrive(sm.p_full[w]);
+        ++tiles;
+        if (live_warp && any_odd) {
+          // p v of the nodes whose V is not finite, for the rows that see them (p = 0 where a row does not)
+          if (!wait(sm.pv_done[w], (tiles - 1) & 1)) break;
+          tc_fence_after();
+          for (int i = 0; i < kTile; ++i) {
+            if (!(odd[i >> 5] >> (i & 31) & 1u)) continue;
+            const int key = key0 + i;
+            const int pg = a.block_table[(int64_t)p.r * a.max_pages + (key >> a.page_shift)];
+            if (pg < 0 || pg >= a.n_pages) continue;
+            const bf16* vp = reinterpret_cast<const bf16*>(a.v) + (int64_t)pg * a.page_stride +
+                             (int64_t)(key & ((1 << a.page_shift) - 1)) * a.token_stride + (int64_t)p.h * a.head_stride;
+            const float pi = pl[i];
+            for (int c0 = 0; c0 < DP; c0 += 32) {
+              float o[32];
+              const uint32_t addr = tmem + lane_addr + X::o_col(w) + c0;
+              ld32_async<0>(addr, o);
+              ld32_wait<0>(o);
+              for (int e = 0; e < 32; ++e)
+                if (pi != 0.f && c0 + e < a.D) o[e] = fmaf(pi, __bfloat162float(vp[c0 + e]), o[e]);
+              st32(addr, o);
+              st_wait();
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+        }
+      }
+      if (!ok) break;
+
+      // ---- the piece's end: join the groups, write the rows or their partials ----
+      const int n_mine = w ? p.n / 2 : p.n - p.n / 2, n_other = p.n - n_mine;
+      other += n_other;
+      items += 2 * p.n;
+      if (n_mine > 0 && !wait(sm.pv_done[w], (tiles - 1) & 1)) break;
+      float2(&ml)[2][kAttnRows] = sm.ml[meets & 1];
+      ml[w][row] = make_float2(mc, l);
+      arrive(sm.meet);
+      // both groups' sums are written; then the other group's O (its barrier is at most this phase behind: the
+      // other group waited for it before it arrived)
+      if (!wait(sm.meet, meets & 1)) break;
+      ++meets;
+      if (n_other > 0 && !wait(sm.pv_done[w ^ 1], (other - 1) & 1)) break;
+      tc_fence_after();
+      const bool whole = p.starts && p.ends;
+      const int slot = 2 * (int)blockIdx.x + (p.starts ? 1 : 0);
+      if (live_warp) {
+        const float2 x0 = ml[0][row], x1 = ml[1][row];
+        const float top = fmaxf(x0.x, x1.x);
+        // a group without a visible key has sum 0 (and an O that may never have been written)
+        const float f0 = x0.y == 0.f ? 0.f : ex2(x0.x - top), f1 = x1.y == 0.f ? 0.f : ex2(x1.x - top);
+        const float sum = x0.y * f0 + x1.y * f1;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const float g0 = whole ? f0 * inv : f0, g1 = whole ? f1 * inv : f1;
+        const bool mine = row < valid;
+        const int64_t tok = p.q.q0 + p.tok0 + row / a.G;
+        const int head = p.h * a.G + row % a.G;
+        // group w writes half of the head's columns
+#pragma unroll
+        for (int cc = 0; cc < DP / 64; ++cc) {
+          const int c0 = w * (DP / 2) + 32 * cc;
+          float o[32], u[32];
+          if (p.n > 0) {
+            ld32_async<0>(tmem + lane_addr + X::o_col(0) + c0, o);
+            if (p.n > 1) ld32_async<0>(tmem + lane_addr + X::o_col(1) + c0, u);
+            ld32_wait<0>(o);
+            if (p.n > 1) ld32_wait<0>(u);
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            o[i] = x0.y == 0.f ? 0.f : o[i] * g0;
+            if (p.n > 1 && x1.y != 0.f) o[i] = fmaf(u[i], g1, o[i]);
+          }
+          if (mine && whole) {
+            bf16* out = reinterpret_cast<bf16*>(a.out) + tok * a.out_ld + (int64_t)head * a.D + c0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (c0 + 8 * i < a.D)
+                *reinterpret_cast<uint4*>(out + 8 * i) =
+                    make_uint4(pack_bf16(o[8 * i], o[8 * i + 1]), pack_bf16(o[8 * i + 2], o[8 * i + 3]),
+                               pack_bf16(o[8 * i + 4], o[8 * i + 5]), pack_bf16(o[8 * i + 6], o[8 * i + 7]));
+          } else if (mine) {
+            float* out = a.part + ((int64_t)slot * kAttnRows + row) * kAttnPartDim + c0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<float4*>(out + 4 * i) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+        }
+        if (mine && w == 0) {
+          if (!whole) a.part_ml[slot * kAttnRows + row] = make_float2(top, sum);
+          else if (a.lse) a.lse[tok * a.H + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+        }
+      }
+      if (p.starts && !p.ends && threadIdx.x == 0)
+        a.joins[blockIdx.x] = make_int4(owner(p.unit + p.parts - 1) - (int)blockIdx.x + 1, p.q.q0 + p.tok0, p.ntok, p.h);
+      joins = joins || (p.starts && !p.ends);
+      if (p.n > 0) {
+        tc_fence_before();
+        arrive(sm.o_free);
+      }
+    }
+    if (threadIdx.x == 0 && !joins) a.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+  }
+}
+
+// Units that a run's end cut: run c's unit that began but did not end in it has
+// its partials in slot 2c + 1 (its own) and 2 (c + 1), 2 (c + 2), ... of the runs
+// after it.  A warp a row, a lane four columns, parts in ascending order.
+constexpr int kJoinWarps = 8, kJoinRows = 16;
+__global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const AttnArgs a) {
+  pdl_wait();
+  const int4 u = a.joins[blockIdx.x];
+  const int lane = threadIdx.x & 31, valid = u.z * a.G;
+  if (u.x < 2) return;
+  for (int i = 0; i < kJoinRows / kJoinWarps; ++i) {
+    const int row = blockIdx.y * kJoinRows + i * kJoinWarps + (threadIdx.x >> 5);
+    if (row >= valid) return;
+    auto slot = [&](int p) { return 2 * ((int)blockIdx.x + p) + (p == 0 ? 1 : 0); };
+    float top = -INFINITY;
+    for (int p = lane; p < u.x; p += 32) {
+      const float2 ml = a.part_ml[slot(p) * kAttnRows + row];
+      if (ml.y != 0.f) top = fmaxf(top, ml.x);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    float sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p0 = 0; p0 < u.x; p0 += 32) {
+      const int np = min(32, u.x - p0);
+      float f = 0.f, l = 0.f;
+      if (lane < np) {
+        const float2 ml = a.part_ml[slot(p0 + lane) * kAttnRows + row];
+        l = ml.y;
+        f = l == 0.f ? 0.f : ex2(ml.x - top);
+      }
+      for (int p = 0; p < np; p += 8) {
+        float4 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          v[k] = p + k < np && 4 * lane < a.D
+                     ? *reinterpret_cast<const float4*>(a.part + ((int64_t)slot(p0 + p + k) * kAttnRows + row) *
+                                                                     kAttnPartDim + 4 * lane)
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float fk = __shfl_sync(0xffffffffu, f, (p + k) & 31), lk = __shfl_sync(0xffffffffu, l, (p + k) & 31);
+          if (p + k >= np) continue;
+          sum = fmaf(lk, fk, sum);
+          acc.x = fmaf(v[k].x, fk, acc.x);
+          acc.y = fmaf(v[k].y, fk, acc.y);
+          acc.z = fmaf(v[k].z, fk, acc.z);
+          acc.w = fmaf(v[k].w, fk, acc.w);
+        }
+      }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int64_t tok = u.y + row / a.G;
+    const int head = u.w * a.G + row % a.G;
+    if (4 * lane < a.D)
+      *reinterpret_cast<uint2*>(reinterpret_cast<bf16*>(a.out) + tok * a.out_ld + (int64_t)head * a.D + 4 * lane) =
+          make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+    if (a.lse && lane == 0)
+      a.lse[tok * a.H + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+// BF16 tensor of up to four dims (the first contiguous), 128-byte swizzled boxes 64 wide
+bool make_map(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+              const cuuint32_t* box) {
+  EncodeTiledFn fn = encode_fn();
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(ptr), dims, strides, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DP>
+cudaError_t launch_dp(const AttnArgs& a, cudaStream_t s) {
+  using X = Geo<DP>;
+  const int tb = kAttnRows / a.G, page = 1 << a.page_shift;
+  Maps maps;
+  {
+    const cuuint64_t dims[3] = {(cuuint64_t)a.D, (cuuint64_t)a.H, (cuuint64_t)a.T};
+    const cuuint64_t strides[2] = {(cuuint64_t)a.D * 2, (cuuint64_t)(a.T > 1 ? a.q_ld : (int64_t)a.H * a.D) * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)a.G, (cuuint32_t)tb};
+    if (!make_map(&maps.q, a.q, 3, dims, strides, box)) return cudaErrorInvalidValue;
+  }
+  {
+    const cuuint64_t dims[4] = {(cuuint64_t)a.D, (cuuint64_t)page, (cuuint64_t)a.Hkv, (cuuint64_t)a.n_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)a.token_stride * 2,
+                                   (cuuint64_t)(a.Hkv > 1 ? a.head_stride : a.token_stride) * 2,
+                                   (cuuint64_t)a.page_stride * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)std::min(page, kTile), 1, 1};
+    if (!make_map(&maps.k, a.k, 4, dims, strides, box) || !make_map(&maps.v, a.v, 4, dims, strides, box))
+      return cudaErrorInvalidValue;
+  }
+  const size_t smem = 1024 + X::SLOT + X::RING + sizeof(Small) + ((size_t)a.R + 1) * 4;
+  static_assert(1024 + X::SLOT + X::RING + sizeof(Small) + 4097 * 4 <= kMaxSmem, "shared memory");
+  static PerDeviceOnce once;
+  int sms = 0;
+  cudaError_t e = once.run(
+      [](int& v) {
+        v = std::min(num_sms(), kAttnMaxCtas);
+        return cudaFuncSetAttribute(attention_tc_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+      },
+      &sms);
+  if (e != cudaSuccess) return e;
+  e = launch_k(attention_tc_kernel<DP>, dim3((unsigned)sms), dim3(kThreads), smem, s, maps, a, tb);
+  if (e != cudaSuccess) return e;
+  return launch_k(attention_join_kernel, dim3((unsigned)sms, (unsigned)ceil_div(tb * a.G, kJoinRows)),
+                  dim3(32 * kJoinWarps), 0, s, a);
+}
+
+}  // namespace
+
+cudaError_t launch_attention_bf16(const AttnArgs& a, cudaStream_t s) {
+  if (a.T <= 0) return cudaSuccess;
+  return a.D <= 64 ? launch_dp<64>(a, s) : launch_dp<128>(a, s);
+}
+
+}  // namespace moe

@@ -25,6 +25,7 @@ constexpr int kAttnRows = 128;
 constexpr int kAttnPartDim = 128;
 constexpr size_t kAttnPartSlots = 2 * kAttnMaxCtas;
 constexpr size_t kAttnPartBytes = kAttnPartSlots * kAttnRows * (kAttnPartDim + 2) * 4;
+constexpr size_t kAttnJoinBytes = kAttnMaxCtas * 16;   // a record a run: what the join kernel adds
 
 struct PlanArgs {
   const int32_t *ctx_len, *new_len, *parents;
@@ -70,6 +71,7 @@ struct AttnArgs {
   AttnHeader* hdr;
   float* part;              // [slots][128 rows][kAttnPartDim]
   float2* part_ml;          // [slots][128 rows] (max, sum)
+  int4* joins;              // [runs] (parts or 0, first row, nodes, KV head)
   int64_t q_ld, out_ld, page_stride, token_stride, head_stride;
   float scale;
   int R, T, H, Hkv, G, D, n_pages, max_pages, page_shift, mask_words;

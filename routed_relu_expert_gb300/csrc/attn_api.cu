@@ -52,7 +52,7 @@ bool bad_array(const T* p) {
   return !p || !aligned(p, sizeof(T));
 }
 
-constexpr size_t kWorkspaceBytes = MOE_ATTN_HEADER_BYTES + kAttnPartBytes;
+constexpr size_t kWorkspaceBytes = MOE_ATTN_HEADER_BYTES + kAttnPartBytes + kAttnJoinBytes;
 
 moe_status_t check_ws(const void* ws, size_t ws_bytes) {
   if (!ws || !aligned(ws, 16)) return MOE_ERR_INVALID_ARG;
@@ -250,6 +250,7 @@ moe_status_t moe_tree_attention(const moe_attn_config_t* cfg, int32_t R, int32_t
   a.hdr = reinterpret_cast<AttnHeader*>(ws);
   a.part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(ws) + MOE_ATTN_HEADER_BYTES);
   a.part_ml = reinterpret_cast<float2*>(a.part + kAttnPartSlots * kAttnRows * kAttnPartDim);
+  a.joins = reinterpret_cast<int4*>(a.part_ml + kAttnPartSlots * kAttnRows);
   a.q_ld = q_ld;
   a.out_ld = out_ld;
   a.page_stride = cfg->page_stride;
