@@ -16,11 +16,12 @@
 //
 // Inside a CTA: warp 8 brings K and V tiles into a ring by TMA, a box per page
 // and 64-wide half (any page size from 8 on; the table's entries are fetched a
-// tile ahead); one thread of warp 9 issues the MMAs; warps 0-3 and 4-7 are two
-// softmax groups that take the unit's tiles in turn, a thread a row, each with
-// its own S, P and O in tensor memory and its own running maximum, so that one
-// group's exponentials run beside the other's products.  P goes back to tensor
-// memory as the A operand of P V; V is the MN-major B operand as it lies.
+// tile ahead); warp 9 issues the MMAs; warps 0-3 and 4-7 are two softmax groups,
+// a thread a row and half of the tile's keys.  S and P have two buffers each in
+// tensor memory (with O they fill it), so the products of the next tile's S and
+// of the last tile's P V run beside the exponentials of this one.  P goes back
+// to tensor memory as the A operand of P V; V is the MN-major B operand as it
+// lies.  A row's two threads exchange their maxima through shared memory.
 //
 // The reference m of a row follows its maximum only when that rose by more than
 // 2^8: below that p and the sums just grow by at most 2^8, exactly undone by the
@@ -55,11 +56,10 @@ struct Geo {
   static constexpr int SLOT = NH * kHalfBytes;             // a K or V tile
   static constexpr int SLOTS = DP == 128 ? 5 : 10;         // 160 KB in flight
   static constexpr int RING = SLOTS * SLOT;
-  static constexpr uint32_t O0 = 256;
-  static constexpr bool ALIAS = DP == 128;                 // P lies in its S (tensor memory is full)
-  static __host__ __device__ constexpr uint32_t s_col(int w) { return 128u * w; }
-  static __host__ __device__ constexpr uint32_t p_col(int w) { return ALIAS ? 128u * w : 384u + 64u * w; }
-  static __host__ __device__ constexpr uint32_t o_col(int w) { return O0 + (uint32_t)(DP * w); }
+  // tensor memory columns: S0 S1 (128 each), P0 P1 (64 each, BF16 pairs), O
+  static __host__ __device__ constexpr uint32_t s_col(int b) { return 128u * b; }
+  static __host__ __device__ constexpr uint32_t p_col(int b) { return 256u + 64u * b; }
+  static constexpr uint32_t O = 384;
 };
 
 struct Maps {
@@ -69,9 +69,10 @@ struct Maps {
 // fixed shared-memory words after the tiles
 struct Small {
   uint64_t full[10], empty[10];
-  uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done[2], o_free, meet, group[2], drain;
-  float2 ml[2][2][kAttnRows];                  // [piece parity][group][row] (reference, sum)
-  uint32_t odd[2][4];                          // nodes of the tile whose V is not finite
+  uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done[2], o_free, meet, group, pair[4], drain;
+  float top[2][2][kAttnRows];                  // [tile parity][group][row] maxima of the halves
+  float sum[2][2][kAttnRows];                  // [piece parity][group][row]
+  uint32_t odd[2][2][4];                       // [tile parity][half of the head]: nodes whose V is not finite
   uint32_t tmem;
   int abort;
   int scan[16];
@@ -94,11 +95,12 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       : "memory");
 }
 
-#define R32(r, o)                                                                                                   \
-  r[o + 0], r[o + 1], r[o + 2], r[o + 3], r[o + 4], r[o + 5], r[o + 6], r[o + 7], r[o + 8], r[o + 9], r[o + 10],     \
-      r[o + 11], r[o + 12], r[o + 13], r[o + 14], r[o + 15], r[o + 16], r[o + 17], r[o + 18], r[o + 19], r[o + 20],  \
-      r[o + 21], r[o + 22], r[o + 23], r[o + 24], r[o + 25], r[o + 26], r[o + 27], r[o + 28], r[o + 29], r[o + 30],  \
-      r[o + 31]
+// one thread of a converged warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
 
 // 32 columns of this thread's lane, without waiting for them
 template <int O, int N>
@@ -172,6 +174,34 @@ __device__ __forceinline__ uint64_t v_desc(uint32_t addr) {
   d |= (uint64_t)1 << 46;
   d |= (uint64_t)2 << 61;
   return d;
+}
+
+// ---------------------------------------------------------------------------
+// nodes whose V is not finite (out of the hot path's registers)
+// ---------------------------------------------------------------------------
+// O += p V, columns c0 .. c0 + 63 of the head, for the rows that see them (p, read
+// back from tensor memory, is 0 where a row does not)
+__device__ __noinline__ void add_odd(const AttnArgs& a, int r, int h, int key0, const uint32_t* odd, int c0,
+                                     uint32_t p_addr, uint32_t o_addr) {
+  for (int i = 0; i < kTile; ++i) {
+    if (!(odd[i >> 5] >> (i & 31) & 1u)) continue;
+    const int key = key0 + i;
+    const int pg = a.block_table[(int64_t)r * a.max_pages + (key >> a.page_shift)];
+    if (pg < 0 || pg >= a.n_pages) continue;
+    const bf16* vp = reinterpret_cast<const bf16*>(a.v) + (int64_t)pg * a.page_stride +
+                     (int64_t)(key & ((1 << a.page_shift) - 1)) * a.token_stride + (int64_t)h * a.head_stride;
+    uint32_t x;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(x) : "r"(p_addr + (uint32_t)(i >> 1)));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(x) : : "memory");
+    const float pi = i & 1 ? bf16_hi(x) : bf16_lo(x);
+    for (int c = c0; c < c0 + 64; ++c) {
+      asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(x) : "r"(o_addr + (uint32_t)c));
+      asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(x) : : "memory");
+      if (pi != 0.f && c < a.D) x = __float_as_uint(fmaf(pi, __bfloat162float(vp[c]), __uint_as_float(x)));
+      asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(o_addr + (uint32_t)c), "r"(x) : "memory");
+      st_wait();
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -261,10 +291,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(sm.q_empty), 1);
     for (int w = 0; w < 2; ++w) {
       mbar_init(bar(sm.s_full[w]), 1);
-      mbar_init(bar(sm.p_full[w]), 4);
+      mbar_init(bar(sm.p_full[w]), kSoftWarps);
       mbar_init(bar(sm.pv_done[w]), 1);
-      mbar_init(bar(sm.group[w]), 4);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(bar(sm.pair[i]), 2);
+    mbar_init(bar(sm.group), kSoftWarps);
     mbar_init(bar(sm.o_free), kSoftWarps);
     mbar_init(bar(sm.meet), kSoftWarps);
     mbar_init(bar(sm.drain), 1);
@@ -340,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int id[3] = {page_of(0), page_of(1), -1};            // tiles j, j + 1, j + 2
       ok = __all_sync(0xffffffffu, mbar_wait(bar(sm.q_empty), (pieces & 1) ^ 1, abort_flag, err));
       if (!ok) break;
-      if (lane == 0) {
+      if (elect_one()) {
         mbar_expect_tx(bar(sm.q_full), (uint32_t)(X::NH * 128 * a.G * tb));
 #pragma unroll
         for (int hh = 0; hh < X::NH; ++hh)
@@ -350,15 +381,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto load = [&](const CUtensorMap* map, int j, int pid) {
         ok = __all_sync(0xffffffffu, mbar_wait(bar(sm.empty[slot]), phase ^ 1u, abort_flag, err));
         if (!ok) return;
-        const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, pid >= 0));
-        if (lane == 0) mbar_expect_tx(bar(sm.full[slot]), boxes * (uint32_t)(X::NH * 128 * rows));
-        __syncwarp();
-        if (pid >= 0) {
-          const int off = ((p.t0 + j) * kTile + lane * rows) & (page - 1);
-          const uint32_t dst = ring + (uint32_t)(slot * X::SLOT + lane * rows * 128);
+        const int boxes = __popc(__ballot_sync(0xffffffffu, pid >= 0));   // lanes 0 .. boxes - 1
+        const int off = ((p.t0 + j) * kTile) & (page - 1);                // pages larger than a tile
+        const uint32_t dst = ring + (uint32_t)(slot * X::SLOT), b = bar(sm.full[slot]);
+        if (elect_one()) mbar_expect_tx(b, (uint32_t)(boxes * X::NH * 128 * rows));
+        for (int i = 0; i < boxes; ++i) {
+          const int pg = __shfl_sync(0xffffffffu, pid, i);
+          if (elect_one()) {
 #pragma unroll
-          for (int hh = 0; hh < X::NH; ++hh)
-            tma_load_4d(dst + hh * kHalfBytes, map, 64 * hh, off, p.h, pid, bar(sm.full[slot]));
+            for (int hh = 0; hh < X::NH; ++hh)
+              tma_load_4d(dst + (uint32_t)(hh * kHalfBytes + i * rows * 128), map, 64 * hh, off, p.h, pg, b);
+          }
         }
         __syncwarp();
         ++it;
@@ -391,76 +424,83 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 9) {
     // ---------------- MMA issuer ----------------
-    if (lane == 0) {
-      const uint32_t id_s = idesc_f16kind(kAttnRows, kTile, false);
-      const uint32_t id_o = idesc_f16kind(kAttnRows, DP, false) | (1u << 16);      // B is MN-major
-      int slot = 0, pieces = 0;
-      uint32_t phase = 0;
-      int done[2] = {0, 0};                                // tiles of each group so far
-      bool ok = true, issued = false;
-      auto wait = [&](uint64_t& b, uint32_t parity) {
-        ok = ok && mbar_wait<false, true>(bar(b), parity, abort_flag, err);
-        return ok;
-      };
-      auto advance = [&]() {
-        if (++slot == NS) {
-          slot = 0;
-          phase ^= 1u;
-        }
-      };
-      for (int pos = begin; pos < end && ok;) {
-        const Piece p = next_piece(a, prefix, tb, pos, end);
-        if (p.n == 0) continue;
-        if (!wait(sm.q_full, pieces & 1)) break;
-        auto scores = [&](int j) {
-          const int w = j & 1;
-          if (!wait(sm.full[slot], phase)) return;
-          // P lies in S: the products that read it must be done
-          if (X::ALIAS && done[w] > 0 && !wait(sm.pv_done[w], (done[w] - 1) & 1)) return;
-          tc_fence_after();
-          const uint32_t kb = ring + (uint32_t)(slot * X::SLOT);
+    // the whole warp walks and waits; one elected thread issues (a branch on the
+    // lane number instead costs 170 to 250 cycles an MMA: the operands then reach
+    // the uniform registers that the instruction takes one lane at a time)
+    const uint32_t id_s = idesc_f16kind(kAttnRows, kTile, false);
+    const uint32_t id_o = idesc_f16kind(kAttnRows, DP, false) | (1u << 16);      // B is MN-major
+    int slot = 0, pieces = 0;
+    uint32_t phase = 0;
+    int tiles = 0;                                       // of all pieces so far; buffer b = tile & 1
+    bool ok = true, issued = false;
+    auto wait = [&](uint64_t& b, uint32_t parity) {
+      ok = ok && __all_sync(0xffffffffu, mbar_wait<false, true>(bar(b), parity, abort_flag, err));
+      return ok;
+    };
+    auto advance = [&]() {
+      if (++slot == NS) {
+        slot = 0;
+        phase ^= 1u;
+      }
+    };
+    for (int pos = begin; pos < end && ok;) {
+      const Piece p = next_piece(a, prefix, tb, pos, end);
+      if (p.n == 0) continue;
+      if (!wait(sm.q_full, pieces & 1)) break;
+      auto scores = [&](int j) {
+        const int b = (tiles + j) & 1;
+        // the buffer is free: its last S was read before its P, which PV waited for
+        if (!wait(sm.full[slot], phase)) return;
+        tc_fence_after();
+        issued = true;
+        if (elect_one()) {
+          const uint64_t da = smem_desc_sw128(q_smem), db = smem_desc_sw128(ring + (uint32_t)(slot * X::SLOT));
+          const uint32_t d = tmem + X::s_col(b);
 #pragma unroll
-          for (int hh = 0; hh < X::NH; ++hh) {
-            const uint64_t da = smem_desc_sw128(q_smem + hh * kHalfBytes), db = smem_desc_sw128(kb + hh * kHalfBytes);
+          for (int hh = 0; hh < X::NH; ++hh)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              tc_mma<1>(tmem + X::s_col(w), da + 2u * k, db + 2u * k, id_s, (hh | k) != 0);
-          }
-          issued = true;
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t step = hh * (kHalfBytes >> 4) + 2 * k;
+              tc_mma<1>(d, da + step, db + step, id_s, (hh | k) != 0);
+            }
           tc_commit<1>(bar(sm.empty[slot]));
-          tc_commit<1>(bar(sm.s_full[w]));
+          tc_commit<1>(bar(sm.s_full[b]));
           if (j == p.n - 1) tc_commit<1>(bar(sm.q_empty));
-          advance();
-        };
-        scores(0);
-        for (int j = 0; j < p.n && ok; ++j) {
-          if (j + 1 < p.n) scores(j + 1);
-          const int w = j & 1;
-          if (!wait(sm.full[slot], phase) || !wait(sm.p_full[w], done[w] & 1)) break;
-          // O of the previous piece has been read
-          if (j < 2 && !wait(sm.o_free, (pieces & 1) ^ 1)) break;
-          tc_fence_after();
-          const uint32_t vb = ring + (uint32_t)(slot * X::SLOT);
+        }
+        __syncwarp();
+        advance();
+      };
+      scores(0);
+      for (int j = 0; j < p.n && ok; ++j) {
+        if (j + 1 < p.n) scores(j + 1);
+        const int b = (tiles + j) & 1;
+        if (!wait(sm.full[slot], phase) || !wait(sm.p_full[b], (uint32_t)((tiles + j) >> 1) & 1u)) break;
+        // O of the previous piece has been read
+        if (j == 0 && !wait(sm.o_free, (pieces & 1) ^ 1)) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t db = v_desc(ring + (uint32_t)(slot * X::SLOT));
+          const uint32_t d = tmem + X::O, pa = tmem + X::p_col(b);
 #pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            mma_ts(tmem + X::o_col(w), tmem + X::p_col(w) + 8u * k, v_desc(vb + 2048u * k), id_o, (j >= 2 || k) ? 1u : 0u);
+          for (int k = 0; k < kTile / 16; ++k) mma_ts(d, pa + 8u * k, db + 128u * k, id_o, (j | k) ? 1u : 0u);
           tc_commit<1>(bar(sm.empty[slot]));
-          tc_commit<1>(bar(sm.pv_done[w]));
-          ++done[w];
-          advance();
+          tc_commit<1>(bar(sm.pv_done[b]));
         }
-        ++pieces;
+        __syncwarp();
+        advance();
       }
-      if (!ok && issued) {
-        tc_commit<1>(bar(sm.drain));
-        const uint64_t t0 = globaltimer();
-        while (!mbar_try(bar(sm.drain), 0u) && globaltimer() - t0 < kWaitLimitNs) {
-        }
-      }
+      tiles += p.n;
+      ++pieces;
     }
-    __syncwarp();
+    if (!ok && issued) {
+      if (elect_one()) tc_commit<1>(bar(sm.drain));
+      const uint64_t t0 = globaltimer();
+      while (!mbar_try(bar(sm.drain), 0u) && globaltimer() - t0 < kWaitLimitNs) {
+      }
+      __syncwarp();
+    }
   } else {
-    // ---------------- softmax: group w = warps 4w .. 4w + 3, a thread a row ----------------
+    // ---------------- softmax: warps q and q + 4 share rows 32 q .. 32 q + 31, group w has keys 64 w .. 64 w + 63 ----
     const int w = warp >> 2, qd = warp & 3, row = 32 * qd + lane;
     const uint32_t lane_addr = (uint32_t)(32 * qd) << 16;
     const float c = a.scale * 1.4426950408889634f;
@@ -475,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = threadIdx.x; i < a.H; i += 32 * kSoftWarps) a.lse[(int64_t)t * a.H + i] = -INFINITY;
       }
     }
-    int tiles = 0, other = 0, items = 0, meets = 0, groups = 0;
+    int tiles = 0, items = 0, meets = 0, groups = 0, pairs = 0;
     bool ok = true, joins = false;
     auto wait = [&](uint64_t& b, uint32_t parity) {
       ok = __all_sync(0xffffffffu, mbar_wait<false, true>(bar(b), parity, abort_flag, err));
@@ -492,65 +532,59 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int node = p.tok0 + row / a.G;
       const int32_t* mask = a.tree_mask ? a.tree_mask + (int64_t)(p.q.q0 + min(node, p.q.n - 1)) * a.mask_words : nullptr;
       float mc = -INFINITY, l = 0.f;
-      for (int j = w; j < p.n; j += 2) {
+      for (int j = 0; j < p.n; ++j, ++tiles) {
+        const int b = tiles & 1;
+        const uint32_t use = (uint32_t)(tiles >> 1);         // times that buffer b was used before
         const int key0 = (p.t0 + j) * kTile;
         const bool special = key0 + kTile > p.q.ctx;
-        uint32_t odd[4] = {0, 0, 0, 0};
+        bool any_odd = false;
         if (special) {
-          // V rows past the last key, and nodes' rows that are not finite, become zeros
+          // V rows past the last key, and nodes' rows that are not finite, become zeros (by halves of the head)
           const int item = items + v_item(j, p.n);
           if (!wait(sm.full[item % NS], (uint32_t)(item / NS) & 1u)) break;
           const int key = key0 + row;
-          uint4* v0 = reinterpret_cast<uint4*>(ring_ptr + (item % NS) * X::SLOT + row * 128);
+          uint4* v0 = reinterpret_cast<uint4*>(ring_ptr + (item % NS) * X::SLOT + w * kHalfBytes + row * 128);
           bool zero = key >= p.q.kv, strange = false;
-          if (!zero && key >= p.q.ctx) {
-            uint32_t hit = 0;
-#pragma unroll
-            for (int hh = 0; hh < X::NH; ++hh)
+          if (w < X::NH) {
+            if (!zero && key >= p.q.ctx) {
+              uint32_t hit = 0;
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
-                const uint4 x = v0[hh * (kHalfBytes / 16) + i];
+                const uint4 x = v0[i];
                 const uint32_t ws[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                   hit |= ((ws[e] & 0x7F80u) == 0x7F80u) | ((ws[e] & 0x7F800000u) == 0x7F800000u);
               }
-            strange = hit != 0;
-          }
-          if (zero || strange) {
+              strange = hit != 0;
+            }
+            if (zero || strange) {
 #pragma unroll
-            for (int hh = 0; hh < X::NH; ++hh)
-#pragma unroll
-              for (int i = 0; i < 8; ++i) v0[hh * (kHalfBytes / 16) + i] = make_uint4(0, 0, 0, 0);
+              for (int i = 0; i < 8; ++i) v0[i] = make_uint4(0, 0, 0, 0);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           const uint32_t mine = __ballot_sync(0xffffffffu, strange);
-          if (lane == 0) sm.odd[w][qd] = mine;
-          arrive(sm.group[w]);
-          if (!wait(sm.group[w], groups & 1)) break;
+          if (lane == 0) sm.odd[b][w][qd] = mine;
+          arrive(sm.group);
+          if (!wait(sm.group, groups & 1)) break;
           ++groups;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) odd[i] = *reinterpret_cast<volatile uint32_t*>(&sm.odd[w][i]);
+          for (int i = 0; i < 4; ++i) any_odd |= sm.odd[b][w][i] != 0;
         }
-        if (!wait(sm.s_full[w], tiles & 1)) break;
-        const bool any_odd = (odd[0] | odd[1] | odd[2] | odd[3]) != 0;
-        float pl[kTile];                       // the row's p where the tile has odd nodes; untouched otherwise
+        if (!wait(sm.s_full[b], use & 1u)) break;
         if (live_warp) {
           tc_fence_after();
-          float v[kTile];
-          const uint32_t s_addr = tmem + lane_addr + X::s_col(w);
+          float v[64];
+          const uint32_t s_addr = tmem + lane_addr + X::s_col(b) + 64u * w;
           ld32_async<0>(s_addr, v);
           ld32_async<32>(s_addr + 32, v);
-          ld32_async<64>(s_addr + 64, v);
-          ld32_async<96>(s_addr + 96, v);
           ld32_wait<0>(v);
           ld32_wait<32>(v);
-          ld32_wait<64>(v);
-          ld32_wait<96>(v);
           if (special) {
 #pragma unroll
-            for (int cc = 0; cc < 4; ++cc) {
-              const int k0 = key0 + 32 * cc, j0 = k0 - p.q.ctx;   // first key of the word, as a node
+            for (int cc = 0; cc < 2; ++cc) {
+              const int k0 = key0 + 64 * w + 32 * cc, j0 = k0 - p.q.ctx;   // first key of the word, as a node
               auto low = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
               uint32_t bits;
               if (!mask) {
@@ -561,43 +595,48 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bits = j0 + 32 <= 0 ? 0xffffffffu : __funnelshift_r(word(wi), word(wi + 1), (uint32_t)(j0 & 31));
               }
               bits &= low(p.q.kv - k0);
-              if (bits != 0xffffffffu) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (!(bits >> i & 1u)) v[32 * cc + i] = -INFINITY;
+              for (int i = 0; i < 32; ++i)
+                if (!(bits >> i & 1u)) v[32 * cc + i] = -INFINITY;
+            }
+          }
+          float t4[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+          for (int i = 4; i < 64; ++i) t4[i & 3] = fmaxf(t4[i & 3], v[i]);
+          float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+          // the other half's maximum
+          sm.top[pairs & 1][w][row] = top;
+          arrive(sm.pair[qd]);
+          if (!wait(sm.pair[qd], pairs & 1)) break;
+          top = fmaxf(top, sm.top[pairs & 1][w ^ 1][row]) * c;
+          ++pairs;
+          const bool raise = top > mc + kRaise || (mc == -INFINITY && top > mc);
+          if (__any_sync(0xffffffffu, raise)) {
+            const float f = raise ? (mc == -INFINITY ? 0.f : ex2(mc - top)) : 1.f;
+            if (raise) mc = top;
+            l *= f;
+            if (j > 0) {
+              // O so far (this group's columns) scaled to the new reference
+              if (!wait(sm.pv_done[b ^ 1], (uint32_t)((tiles - 1) >> 1) & 1u)) break;
+              tc_fence_after();
+#pragma unroll
+              for (int c0 = 0; c0 < DP / 2; c0 += 32) {
+                float o[32];
+                const uint32_t addr = tmem + lane_addr + X::O + (uint32_t)(w * (DP / 2) + c0);
+                ld32_async<0>(addr, o);
+                ld32_wait<0>(o);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] *= f;
+                st32(addr, o);
               }
             }
           }
-          float top = v[0];
-#pragma unroll
-          for (int i = 1; i < kTile; ++i) top = fmaxf(top, v[i]);
-          top *= c;
-          const bool first = j == w;
-          const bool raise = top > mc + kRaise || (mc == -INFINITY && top > mc);
-          const float f = raise ? (mc == -INFINITY ? 0.f : ex2(mc - top)) : 1.f;
-          if (raise) {
-            mc = top;
-            l *= f;
-          }
-          if (!first && __any_sync(0xffffffffu, raise)) {
-            // O of this group after its previous tile, scaled to the new reference
-            if (!wait(sm.pv_done[w], (tiles - 1) & 1)) break;
-            tc_fence_after();
-#pragma unroll
-            for (int c0 = 0; c0 < DP; c0 += 32) {
-              float o[32];
-              const uint32_t addr = tmem + lane_addr + X::o_col(w) + c0;
-              ld32_async<0>(addr, o);
-              ld32_wait<0>(o);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] *= f;
-              st32(addr, o);
-            }
-          }
+          // the P of two tiles ago has been multiplied
+          if (use > 0 && !wait(sm.pv_done[b], (use - 1) & 1u)) break;
           const float base = mc == -INFINITY ? 0.f : mc;
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int cc = 0; cc < 4; ++cc) {
+          for (int cc = 0; cc < 2; ++cc) {
             uint32_t pk[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -605,74 +644,40 @@ __global__ void __launch_bounds__(kThreads, 1)
               sum[(2 * i) & 3] += x;
               sum[(2 * i + 1) & 3] += y;
               pk[i] = pack_bf16(x, y);
-              v[32 * cc + 2 * i] = x;
-              v[32 * cc + 2 * i + 1] = y;
             }
-            if (any_odd) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) pl[32 * cc + i] = v[32 * cc + i];
-            }
-            st16(tmem + lane_addr + X::p_col(w) + 16 * cc, pk);
+            st16(tmem + lane_addr + X::p_col(b) + 32u * w + 16u * cc, pk);
           }
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           st_wait();
           tc_fence_before();
         }
-        arrive(sm.p_full[w]);
-        ++tiles;
+        arrive(sm.p_full[b]);
         if (live_warp && any_odd) {
-          // p v of the nodes whose V is not finite, for the rows that see them (p = 0 where a row does not)
-          if (!wait(sm.pv_done[w], (tiles - 1) & 1)) break;
+          // p v of the nodes whose V is not finite
+          if (!wait(sm.pv_done[b], use & 1u)) break;
           tc_fence_after();
-          for (int i = 0; i < kTile; ++i) {
-            if (!(odd[i >> 5] >> (i & 31) & 1u)) continue;
-            const int key = key0 + i;
-            const int pg = a.block_table[(int64_t)p.r * a.max_pages + (key >> a.page_shift)];
-            if (pg < 0 || pg >= a.n_pages) continue;
-            const bf16* vp = reinterpret_cast<const bf16*>(a.v) + (int64_t)pg * a.page_stride +
-                             (int64_t)(key & ((1 << a.page_shift) - 1)) * a.token_stride + (int64_t)p.h * a.head_stride;
-            const float pi = pl[i];
-            for (int c0 = 0; c0 < DP; c0 += 32) {
-              float o[32];
-              const uint32_t addr = tmem + lane_addr + X::o_col(w) + c0;
-              ld32_async<0>(addr, o);
-              ld32_wait<0>(o);
-              for (int e = 0; e < 32; ++e)
-                if (pi != 0.f && c0 + e < a.D) o[e] = fmaf(pi, __bfloat162float(vp[c0 + e]), o[e]);
-              st32(addr, o);
-              st_wait();
-            }
-          }
+          add_odd(a, p.r, p.h, key0, sm.odd[b][w], 64 * w, tmem + lane_addr + X::p_col(b), tmem + lane_addr + X::O);
           tc_fence_before();
           __syncwarp();
         }
       }
       if (!ok) break;
 
-      // ---- the piece's end: join the groups, write the rows or their partials ----
-      const int n_mine = w ? p.n / 2 : p.n - p.n / 2, n_other = p.n - n_mine;
-      other += n_other;
+      // ---- the piece's end: write the rows or their partials ----
       items += 2 * p.n;
-      if (n_mine > 0 && !wait(sm.pv_done[w], (tiles - 1) & 1)) break;
-      float2(&ml)[2][kAttnRows] = sm.ml[meets & 1];
-      ml[w][row] = make_float2(mc, l);
+      float(&sums)[2][kAttnRows] = sm.sum[meets & 1];
+      sums[w][row] = l;
+      if (p.n > 0 && !wait(sm.pv_done[(tiles - 1) & 1], (uint32_t)((tiles - 1) >> 1) & 1u)) break;
       arrive(sm.meet);
-      // both groups' sums are written; then the other group's O (its barrier is at most this phase behind: the
-      // other group waited for it before it arrived)
-      if (!wait(sm.meet, meets & 1)) break;
+      if (!wait(sm.meet, meets & 1)) break;    // both halves' sums are there (and odd nodes are added)
       ++meets;
-      if (n_other > 0 && !wait(sm.pv_done[w ^ 1], (other - 1) & 1)) break;
       tc_fence_after();
       const bool whole = p.starts && p.ends;
       const int slot = 2 * (int)blockIdx.x + (p.starts ? 1 : 0);
       if (live_warp) {
-        const float2 x0 = ml[0][row], x1 = ml[1][row];
-        const float top = fmaxf(x0.x, x1.x);
-        // a group without a visible key has sum 0 (and an O that may never have been written)
-        const float f0 = x0.y == 0.f ? 0.f : ex2(x0.x - top), f1 = x1.y == 0.f ? 0.f : ex2(x1.x - top);
-        const float sum = x0.y * f0 + x1.y * f1;
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const float g0 = whole ? f0 * inv : f0, g1 = whole ? f1 * inv : f1;
+        const float sum = sums[0][row] + sums[1][row];
+        // a row without a visible key has sum 0 and O = 0 (never written if the piece has no tile)
+        const float g = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
         const bool mine = row < valid;
         const int64_t tok = p.q.q0 + p.tok0 + row / a.G;
         const int head = p.h * a.G + row % a.G;
@@ -680,18 +685,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int cc = 0; cc < DP / 64; ++cc) {
           const int c0 = w * (DP / 2) + 32 * cc;
-          float o[32], u[32];
+          float o[32];
           if (p.n > 0) {
-            ld32_async<0>(tmem + lane_addr + X::o_col(0) + c0, o);
-            if (p.n > 1) ld32_async<0>(tmem + lane_addr + X::o_col(1) + c0, u);
+            ld32_async<0>(tmem + lane_addr + X::O + c0, o);
             ld32_wait<0>(o);
-            if (p.n > 1) ld32_wait<0>(u);
           }
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            o[i] = x0.y == 0.f ? 0.f : o[i] * g0;
-            if (p.n > 1 && x1.y != 0.f) o[i] = fmaf(u[i], g1, o[i]);
-          }
+          for (int i = 0; i < 32; ++i) o[i] = sum == 0.f ? 0.f : o[i] * g;
           if (mine && whole) {
             bf16* out = reinterpret_cast<bf16*>(a.out) + tok * a.out_ld + (int64_t)head * a.D + c0;
 #pragma unroll
@@ -708,8 +708,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (mine && w == 0) {
-          if (!whole) a.part_ml[slot * kAttnRows + row] = make_float2(top, sum);
-          else if (a.lse) a.lse[tok * a.H + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+          if (!whole) a.part_ml[slot * kAttnRows + row] = make_float2(mc, sum);
+          else if (a.lse) a.lse[tok * a.H + head] = sum == 0.f ? -INFINITY : (mc + log2f(sum)) * 0.6931471805599453f;
         }
       }
       if (p.starts && !p.ends && threadIdx.x == 0)
@@ -733,62 +733,60 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Units that a run's end cut: run c's unit that began but did not end in it has
 // its partials in slot 2c + 1 (its own) and 2 (c + 1), 2 (c + 2), ... of the runs
 // after it.  A warp a row, a lane four columns, parts in ascending order.
-constexpr int kJoinWarps = 8, kJoinRows = 16;
+constexpr int kJoinWarps = 8;
 __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const AttnArgs a) {
   pdl_wait();
   const int4 u = a.joins[blockIdx.x];
   const int lane = threadIdx.x & 31, valid = u.z * a.G;
   if (u.x < 2) return;
-  for (int i = 0; i < kJoinRows / kJoinWarps; ++i) {
-    const int row = blockIdx.y * kJoinRows + i * kJoinWarps + (threadIdx.x >> 5);
-    if (row >= valid) return;
-    auto slot = [&](int p) { return 2 * ((int)blockIdx.x + p) + (p == 0 ? 1 : 0); };
-    float top = -INFINITY;
-    for (int p = lane; p < u.x; p += 32) {
-      const float2 ml = a.part_ml[slot(p) * kAttnRows + row];
-      if (ml.y != 0.f) top = fmaxf(top, ml.x);
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    float sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int p0 = 0; p0 < u.x; p0 += 32) {
-      const int np = min(32, u.x - p0);
-      float f = 0.f, l = 0.f;
-      if (lane < np) {
-        const float2 ml = a.part_ml[slot(p0 + lane) * kAttnRows + row];
-        l = ml.y;
-        f = l == 0.f ? 0.f : ex2(ml.x - top);
-      }
-      for (int p = 0; p < np; p += 8) {
-        float4 v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          v[k] = p + k < np && 4 * lane < a.D
-                     ? *reinterpret_cast<const float4*>(a.part + ((int64_t)slot(p0 + p + k) * kAttnRows + row) *
-                                                                     kAttnPartDim + 4 * lane)
-                     : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float fk = __shfl_sync(0xffffffffu, f, (p + k) & 31), lk = __shfl_sync(0xffffffffu, l, (p + k) & 31);
-          if (p + k >= np) continue;
-          sum = fmaf(lk, fk, sum);
-          acc.x = fmaf(v[k].x, fk, acc.x);
-          acc.y = fmaf(v[k].y, fk, acc.y);
-          acc.z = fmaf(v[k].z, fk, acc.z);
-          acc.w = fmaf(v[k].w, fk, acc.w);
-        }
-      }
-    }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const int64_t tok = u.y + row / a.G;
-    const int head = u.w * a.G + row % a.G;
-    if (4 * lane < a.D)
-      *reinterpret_cast<uint2*>(reinterpret_cast<bf16*>(a.out) + tok * a.out_ld + (int64_t)head * a.D + 4 * lane) =
-          make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-    if (a.lse && lane == 0)
-      a.lse[tok * a.H + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+  const int row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
+  if (row >= valid) return;
+  auto slot = [&](int p) { return 2 * ((int)blockIdx.x + p) + (p == 0 ? 1 : 0); };
+  float top = -INFINITY;
+  for (int p = lane; p < u.x; p += 32) {
+    const float2 ml = a.part_ml[slot(p) * kAttnRows + row];
+    if (ml.y != 0.f) top = fmaxf(top, ml.x);
   }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  float sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int p0 = 0; p0 < u.x; p0 += 32) {
+    const int np = min(32, u.x - p0);
+    float f = 0.f, l = 0.f;
+    if (lane < np) {
+      const float2 ml = a.part_ml[slot(p0 + lane) * kAttnRows + row];
+      l = ml.y;
+      f = l == 0.f ? 0.f : ex2(ml.x - top);
+    }
+    for (int p = 0; p < np; p += 16) {
+      float4 v[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        v[k] = p + k < np && 4 * lane < a.D
+                   ? *reinterpret_cast<const float4*>(a.part + ((int64_t)slot(p0 + p + k) * kAttnRows + row) *
+                                                                   kAttnPartDim + 4 * lane)
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const float fk = __shfl_sync(0xffffffffu, f, (p + k) & 31), lk = __shfl_sync(0xffffffffu, l, (p + k) & 31);
+        if (p + k >= np) continue;
+        sum = fmaf(lk, fk, sum);
+        acc.x = fmaf(v[k].x, fk, acc.x);
+        acc.y = fmaf(v[k].y, fk, acc.y);
+        acc.z = fmaf(v[k].z, fk, acc.z);
+        acc.w = fmaf(v[k].w, fk, acc.w);
+      }
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int64_t tok = u.y + row / a.G;
+  const int head = u.w * a.G + row % a.G;
+  if (4 * lane < a.D)
+    *reinterpret_cast<uint2*>(reinterpret_cast<bf16*>(a.out) + tok * a.out_ld + (int64_t)head * a.D + 4 * lane) =
+        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  if (a.lse && lane == 0)
+    a.lse[tok * a.H + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 // ---------------------------------------------------------------------------
@@ -837,7 +835,7 @@ cudaError_t launch_dp(const AttnArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   e = launch_k(attention_tc_kernel<DP>, dim3((unsigned)sms), dim3(kThreads), smem, s, maps, a, tb);
   if (e != cudaSuccess) return e;
-  return launch_k(attention_join_kernel, dim3((unsigned)sms, (unsigned)ceil_div(tb * a.G, kJoinRows)),
+  return launch_k(attention_join_kernel, dim3((unsigned)sms, (unsigned)ceil_div(tb * a.G, kJoinWarps)),
                   dim3(32 * kJoinWarps), 0, s, a);
 }
 
