@@ -45,7 +45,10 @@ using namespace tc;
 constexpr int kTile = 128;                     // keys a tile
 constexpr int kHalfBytes = kTile * 128;        // 128 rows of 64 BF16
 constexpr int kSoftWarps = 8;
-constexpr int kThreads = 32 * (kSoftWarps + 2);
+constexpr int kThreads = 32 * (kSoftWarps + 4);
+constexpr int kLoaders = 2;                    // warps that issue the TMA copies
+constexpr int kQueue = 4;                      // pieces worked out ahead
+
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRaise = 8.f;                  // log2 units by which a maximum may pass its reference
 constexpr int kMaxSmem = 232448;
@@ -66,13 +69,26 @@ struct Maps {
   CUtensorMap q, k, v;
 };
 
+// a run's part of one unit
+struct Piece {
+  int r, h;                // request, KV head
+  int row0, tok0, ntok;    // first row of the block in q; its first node and its nodes
+  int ctx, kv;             // tokens before the nodes; all tokens
+  int t0, n;               // first tile and number of tiles (those that a chain's block can see)
+  int flags;               // kStarts, kEnds, kLast
+  int parts;               // of a unit that starts here and ends in a later run: its runs
+};
+constexpr int kStarts = 1, kEnds = 2, kLast = 4;
+
 // fixed shared-memory words after the tiles
 struct Small {
   uint64_t full[10], empty[10];
+  uint64_t piece_full[kQueue], piece_empty[kQueue];
   uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done[2], o_free, meet, group, pair[4], drain;
   float top[2][2][kAttnRows];                  // [tile parity][group][row] maxima of the halves
   float sum[2][2][kAttnRows];                  // [piece parity][group][row]
   uint32_t odd[2][2][4];                       // [tile parity][half of the head]: nodes whose V is not finite
+  Piece piece[kQueue];
   uint32_t tmem;
   int abort;
   int scan[16];
@@ -205,7 +221,7 @@ __device__ __noinline__ void add_odd(const AttnArgs& a, int r, int h, int key0, 
 }
 
 // ---------------------------------------------------------------------------
-// the walk over a CTA's run of tiles
+// requests and units
 // ---------------------------------------------------------------------------
 struct Req {
   int q0, n, kv, ctx, tiles, blocks;
@@ -223,42 +239,6 @@ __device__ __forceinline__ Req request(const AttnArgs& a, int r, int tb, int* ba
   q.tiles = max((q.kv + kTile - 1) / kTile, 1);
   q.blocks = (q.n + tb - 1) / tb;
   return q;
-}
-
-struct Piece {
-  Req q;
-  int r, h, tok0, ntok;    // the block's first node and its nodes
-  int t0, n;               // first tile and number of tiles (those that a chain's block can see)
-  int unit, parts;         // position of the unit's first tile; tiles of the whole unit
-  bool starts, ends;
-};
-
-// piece at position `pos` of a run that ends at `end`; moves pos behind it
-__device__ __forceinline__ Piece next_piece(const AttnArgs& a, const int* prefix, int tb, int& pos, int end) {
-  Piece p;
-  int lo = 0, hi = a.R;                        // prefix[lo] <= pos < prefix[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (prefix[mid] <= pos) lo = mid; else hi = mid;
-  }
-  p.r = lo;
-  p.q = request(a, lo, tb, nullptr);
-  const int local = pos - prefix[lo];
-  const int u = local / p.q.tiles;
-  p.t0 = local - u * p.q.tiles;
-  p.h = u / p.q.blocks;
-  p.tok0 = (u - p.h * p.q.blocks) * tb;
-  p.ntok = min(tb, p.q.n - p.tok0);
-  const int len = min(p.q.tiles - p.t0, end - pos);
-  p.starts = p.t0 == 0;
-  p.ends = p.t0 + len == p.q.tiles;
-  p.unit = pos - p.t0;
-  p.parts = p.q.tiles;
-  pos += len;
-  int t1 = p.t0 + len;
-  if (!a.tree_mask) t1 = min(t1, (p.q.ctx + p.tok0 + p.ntok + kTile - 1) / kTile);
-  p.n = max(t1 - p.t0, 0);
-  return p;
 }
 
 // order of a piece's tiles in the ring: K0, [K1, V0], [K2, V1], ..., V(n-1)
@@ -284,8 +264,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar = [&](uint64_t& b) { return smem_u32(&b); };
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
-      mbar_init(bar(sm.full[s]), 1);
+      mbar_init(bar(sm.full[s]), kLoaders);
       mbar_init(bar(sm.empty[s]), 1);
+    }
+    for (int i = 0; i < kQueue; ++i) {
+      mbar_init(bar(sm.piece_full[i]), 1);
+      mbar_init(bar(sm.piece_empty[i]), kSoftWarps + 1 + kLoaders);
     }
     mbar_init(bar(sm.q_full), 1);
     mbar_init(bar(sm.q_empty), 1);
@@ -309,14 +293,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   pdl_wait();
-  // tiles before each request
+  // cost before each request: its units' tiles and fixed costs
   {
     int bad = 0;
     const int per = (a.R + kThreads - 1) / kThreads, r0 = min((int)threadIdx.x * per, a.R), r1 = min(r0 + per, a.R);
     int local = 0;
     for (int r = r0; r < r1; ++r) {
       const Req q = request(a, r, tb, &bad);
-      local += q.tiles * q.blocks * a.Hkv;
+      local += (q.tiles + kAttnPieceCost) * q.blocks * a.Hkv;
     }
     int x = local;
 #pragma unroll
@@ -331,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int r = r0; r < r1; ++r) {
       prefix[r] = run;
       const Req q = request(a, r, tb, nullptr);
-      run += q.tiles * q.blocks * a.Hkv;
+      run += (q.tiles + kAttnPieceCost) * q.blocks * a.Hkv;
     }
     if (threadIdx.x == kThreads - 1) prefix[a.R] = run;
     if (bad && blockIdx.x == 0) set_error(err, MOE_DEVERR_CACHE);
@@ -343,39 +327,105 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int total = prefix[a.R];
   const int runs = min((int)gridDim.x, max(total, 1));
   auto run_start = [&](int c) { return (int)((int64_t)c * total / runs); };
-  // the run that holds position t
-  auto owner = [&](int t) { return (int)((((int64_t)t + 1) * runs - 1) / total); };
   const bool idle = (int)blockIdx.x >= runs;
   const int begin = idle ? 0 : run_start(blockIdx.x), end = idle ? 0 : run_start(blockIdx.x + 1);
 
-  if (warp == 8) {
+  // the next piece of the queue, for every warp but the one that fills it
+  int taken = 0;
+  auto next = [&](Piece& p) {
+    const int e = taken % kQueue;
+    if (!__all_sync(0xffffffffu, mbar_wait(bar(sm.piece_full[e]), (uint32_t)(taken / kQueue) & 1u, abort_flag, err)))
+      return false;
+    p = sm.piece[e];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(sm.piece_empty[e]));
+    ++taken;
+    return !(p.flags & kLast);
+  };
+
+  if (warp == 11) {
+    // ---------------- the run's pieces, worked out ahead of the other warps ----------------
+    // a unit's cost is kAttnPieceCost, then a tile each
+    auto owner = [&](int at) { return (int)((((int64_t)at + 1) * runs - 1) / total); };
+    int r = 0;
+    for (int hi = a.R; hi - r > 1;) {                      // prefix[r] <= begin < prefix[r + 1]
+      const int mid = (r + hi) >> 1;
+      if (prefix[mid] <= begin) r = mid; else hi = mid;
+    }
+    int pos = begin, made = 0;
+    bool last = false;
+    Req q;
+    int have = -1;
+    while (!last) {
+      Piece p;
+      last = pos >= end;
+      p.flags = kLast;
+      if (!last) {
+        while (prefix[r + 1] <= pos) ++r;
+        if (have != r) q = request(a, r, tb, nullptr);
+        have = r;
+        const int per = q.tiles + kAttnPieceCost, u = (pos - prefix[r]) / per, off = pos - prefix[r] - u * per;
+        const int len = min(per - off, end - pos), t0 = max(off - kAttnPieceCost, 0);
+        int t1 = off + len - kAttnPieceCost;
+        const int unit_end = pos - off + per;
+        pos += len;
+        if (t1 <= t0) continue;                            // the fixed cost alone
+        p.r = r;
+        p.h = u / q.blocks;
+        p.tok0 = (u - p.h * q.blocks) * tb;
+        p.ntok = min(tb, q.n - p.tok0);
+        p.row0 = q.q0 + p.tok0;
+        p.ctx = q.ctx;
+        p.kv = q.kv;
+        p.t0 = t0;
+        p.flags = (t0 == 0 ? kStarts : 0) | (t1 == q.tiles ? kEnds : 0);
+        p.parts = p.flags == kStarts ? owner(unit_end - 1) - (int)blockIdx.x + 1 : 0;
+        if (!a.tree_mask) t1 = min(t1, (q.ctx + p.tok0 + p.ntok + kTile - 1) / kTile);
+        p.n = max(t1 - t0, 0);
+      }
+      const int e = made % kQueue;
+      if (!__all_sync(0xffffffffu,
+                      mbar_wait(bar(sm.piece_empty[e]), ((uint32_t)(made / kQueue) & 1u) ^ 1u, abort_flag, err)))
+        break;
+      if (lane == 0) {
+        sm.piece[e] = p;
+        mbar_arrive(bar(sm.piece_full[e]));
+      }
+      __syncwarp();
+      ++made;
+    }
+  } else if (warp == 8 || warp == 10) {
     // ---------------- K, V (and Q) into shared memory ----------------
+    // the boxes of a tile (page by page, half by half) are shared between the two loaders
+    const int who = warp == 8 ? 0 : 1;
     const int page = 1 << a.page_shift, rows = min(page, kTile);
-    const int per_tile = kTile / rows;                     // boxes of a tile: lane l < per_tile has box l
+    const int per_tile = kTile / rows;                     // boxes of a half: lane l < per_tile has box l
     int slot = 0, it = 0, pieces = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int pos = begin; pos < end && ok;) {
-      const Piece p = next_piece(a, prefix, tb, pos, end);
+    for (Piece p; ok && next(p);) {
       if (p.n == 0) continue;
       const int32_t* table = a.block_table + (int64_t)p.r * a.max_pages;
       // page of this lane's box of tile j (of the piece); -1: nothing to load
       auto page_of = [&](int j) {
         const int tok = (p.t0 + j) * kTile + lane * rows;
-        if (j >= p.n || lane >= per_tile || tok >= p.q.kv) return -1;
+        if (j >= p.n || lane >= per_tile || tok >= p.kv) return -1;
         const int id = table[tok >> a.page_shift];
         if (id >= 0 && id < a.n_pages) return id;
         set_error(err, MOE_DEVERR_CACHE);
         return a.n_pages;                                  // past the last page: TMA fills zeros
       };
       int id[3] = {page_of(0), page_of(1), -1};            // tiles j, j + 1, j + 2
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(sm.q_empty), (pieces & 1) ^ 1, abort_flag, err));
-      if (!ok) break;
-      if (elect_one()) {
-        mbar_expect_tx(bar(sm.q_full), (uint32_t)(X::NH * 128 * a.G * tb));
+      if (who == 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(sm.q_empty), (pieces & 1) ^ 1, abort_flag, err));
+        if (!ok) break;
+        if (elect_one()) {
+          mbar_expect_tx(bar(sm.q_full), (uint32_t)(X::NH * 128 * a.G * tb));
 #pragma unroll
-        for (int hh = 0; hh < X::NH; ++hh)
-          tma_load_3d(q_smem + hh * kHalfBytes, &maps.q, 64 * hh, p.h * a.G, p.q.q0 + p.tok0, bar(sm.q_full));
+          for (int hh = 0; hh < X::NH; ++hh)
+            tma_load_3d(q_smem + hh * kHalfBytes, &maps.q, 64 * hh, p.h * a.G, p.row0, bar(sm.q_full));
+        }
+        __syncwarp();
       }
       ++pieces;
       auto load = [&](const CUtensorMap* map, int j, int pid) {
@@ -383,15 +433,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) return;
         const int boxes = __popc(__ballot_sync(0xffffffffu, pid >= 0));   // lanes 0 .. boxes - 1
         const int off = ((p.t0 + j) * kTile) & (page - 1);                // pages larger than a tile
-        const uint32_t dst = ring + (uint32_t)(slot * X::SLOT), b = bar(sm.full[slot]);
-        if (elect_one()) mbar_expect_tx(b, (uint32_t)(boxes * X::NH * 128 * rows));
-        for (int i = 0; i < boxes; ++i) {
+        const uint32_t b = bar(sm.full[slot]);
+        // two halves: one each; one half: every other box
+        const int hh = X::NH == 2 ? who : 0, first = X::NH == 2 ? 0 : who, step = X::NH == 2 ? 1 : kLoaders;
+        const uint32_t dst = ring + (uint32_t)(slot * X::SLOT + hh * kHalfBytes);
+        if (elect_one()) mbar_expect_tx(b, (uint32_t)((boxes - first + step - 1) / step * 128 * rows));
+        __syncwarp();
+        for (int i = first; i < boxes; i += step) {
           const int pg = __shfl_sync(0xffffffffu, pid, i);
-          if (elect_one()) {
-#pragma unroll
-            for (int hh = 0; hh < X::NH; ++hh)
-              tma_load_4d(dst + (uint32_t)(hh * kHalfBytes + i * rows * 128), map, 64 * hh, off, p.h, pg, b);
-          }
+          if (elect_one()) tma_load_4d(dst + (uint32_t)(i * rows * 128), map, 64 * hh, off, p.h, pg, b);
         }
         __syncwarp();
         ++it;
@@ -409,10 +459,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         id[1] = id[2];
       }
     }
-    if (!ok && lane == 0) {
+    if (*abort_flag && lane == 0) {
       // copies in flight must land before the CTA leaves
+      const uint64_t t0 = globaltimer();
       auto land = [&](uint32_t b, uint32_t parity) {
-        const uint64_t t0 = globaltimer();
         while (!mbar_try(b, parity) && globaltimer() - t0 < kWaitLimitNs) {
         }
       };
@@ -420,8 +470,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int uses = (it - s + NS - 1) / NS;           // times that slot s was filled
         if (it > s) land(bar(sm.full[s]), (uint32_t)(uses - 1) & 1u);
       }
-      if (pieces > 0) land(bar(sm.q_full), (uint32_t)(pieces - 1) & 1u);
+      if (who == 0 && pieces > 0) land(bar(sm.q_full), (uint32_t)(pieces - 1) & 1u);
     }
+    __syncwarp();
   } else if (warp == 9) {
     // ---------------- MMA issuer ----------------
     // the whole warp walks and waits; one elected thread issues (a branch on the
@@ -443,8 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         phase ^= 1u;
       }
     };
-    for (int pos = begin; pos < end && ok;) {
-      const Piece p = next_piece(a, prefix, tb, pos, end);
+    for (Piece p; ok && next(p);) {
       if (p.n == 0) continue;
       if (!wait(sm.q_full, pieces & 1)) break;
       auto scores = [&](int j) {
@@ -492,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tiles += p.n;
       ++pieces;
     }
-    if (!ok && issued) {
+    if (*abort_flag && issued) {
       if (elect_one()) tc_commit<1>(bar(sm.drain));
       const uint64_t t0 = globaltimer();
       while (!mbar_try(bar(sm.drain), 0u) && globaltimer() - t0 < kWaitLimitNs) {
@@ -525,18 +575,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(b));
     };
-    for (int pos = begin; pos < end && ok;) {
-      const Piece p = next_piece(a, prefix, tb, pos, end);
+    const int row_tok = row / a.G, row_head = row - row_tok * a.G;
+    for (Piece p; ok && next(p);) {
       const int valid = p.ntok * a.G;
       const bool live_warp = 32 * qd < valid;
-      const int node = p.tok0 + row / a.G;
-      const int32_t* mask = a.tree_mask ? a.tree_mask + (int64_t)(p.q.q0 + min(node, p.q.n - 1)) * a.mask_words : nullptr;
+      const int node = p.tok0 + row_tok;
+      const int32_t* mask = a.tree_mask ? a.tree_mask + (int64_t)(p.row0 + min(row_tok, p.ntok - 1)) * a.mask_words
+                                        : nullptr;
       float mc = -INFINITY, l = 0.f;
       for (int j = 0; j < p.n; ++j, ++tiles) {
         const int b = tiles & 1;
         const uint32_t use = (uint32_t)(tiles >> 1);         // times that buffer b was used before
         const int key0 = (p.t0 + j) * kTile;
-        const bool special = key0 + kTile > p.q.ctx;
+        const bool special = key0 + kTile > p.ctx;
         bool any_odd = false;
         if (special) {
           // V rows past the last key, and nodes' rows that are not finite, become zeros (by halves of the head)
@@ -544,9 +595,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!wait(sm.full[item % NS], (uint32_t)(item / NS) & 1u)) break;
           const int key = key0 + row;
           uint4* v0 = reinterpret_cast<uint4*>(ring_ptr + (item % NS) * X::SLOT + w * kHalfBytes + row * 128);
-          bool zero = key >= p.q.kv, strange = false;
+          bool zero = key >= p.kv, strange = false;
           if (w < X::NH) {
-            if (!zero && key >= p.q.ctx) {
+            if (!zero && key >= p.ctx) {
               uint32_t hit = 0;
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
@@ -584,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (special) {
 #pragma unroll
             for (int cc = 0; cc < 2; ++cc) {
-              const int k0 = key0 + 64 * w + 32 * cc, j0 = k0 - p.q.ctx;   // first key of the word, as a node
+              const int k0 = key0 + 64 * w + 32 * cc, j0 = k0 - p.ctx;   // first key of the word, as a node
               auto low = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
               uint32_t bits;
               if (!mask) {
@@ -594,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int wi = j0 >> 5;
                 bits = j0 + 32 <= 0 ? 0xffffffffu : __funnelshift_r(word(wi), word(wi + 1), (uint32_t)(j0 & 31));
               }
-              bits &= low(p.q.kv - k0);
+              bits &= low(p.kv - k0);
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (!(bits >> i & 1u)) v[32 * cc + i] = -INFINITY;
@@ -672,15 +723,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait(sm.meet, meets & 1)) break;    // both halves' sums are there (and odd nodes are added)
       ++meets;
       tc_fence_after();
-      const bool whole = p.starts && p.ends;
-      const int slot = 2 * (int)blockIdx.x + (p.starts ? 1 : 0);
+      const bool whole = (p.flags & (kStarts | kEnds)) == (kStarts | kEnds);
+      const int slot = 2 * (int)blockIdx.x + (p.flags & kStarts ? 1 : 0);
       if (live_warp) {
         const float sum = sums[0][row] + sums[1][row];
         // a row without a visible key has sum 0 and O = 0 (never written if the piece has no tile)
         const float g = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
         const bool mine = row < valid;
-        const int64_t tok = p.q.q0 + p.tok0 + row / a.G;
-        const int head = p.h * a.G + row % a.G;
+        const int64_t tok = p.row0 + row_tok;
+        const int head = p.h * a.G + row_head;
         // group w writes half of the head's columns
 #pragma unroll
         for (int cc = 0; cc < DP / 64; ++cc) {
@@ -712,9 +763,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           else if (a.lse) a.lse[tok * a.H + head] = sum == 0.f ? -INFINITY : (mc + log2f(sum)) * 0.6931471805599453f;
         }
       }
-      if (p.starts && !p.ends && threadIdx.x == 0)
-        a.joins[blockIdx.x] = make_int4(owner(p.unit + p.parts - 1) - (int)blockIdx.x + 1, p.q.q0 + p.tok0, p.ntok, p.h);
-      joins = joins || (p.starts && !p.ends);
+      if (p.parts) {
+        if (threadIdx.x == 0) a.joins[blockIdx.x] = make_int4(p.parts, p.row0, p.ntok, p.h);
+        joins = true;
+      }
       if (p.n > 0) {
         tc_fence_before();
         arrive(sm.o_free);

@@ -225,7 +225,7 @@ moe_status_t moe_tree_attention(const moe_attn_config_t* cfg, int32_t R, int32_t
   CHECK(check_config(cfg));
   CHECK(check_cache(cfg));
   if (R < 0 || T < 0 || (tree_mask && mask_words < 1)) return MOE_ERR_INVALID_ARG;
-  const int64_t tiles = ((int64_t)cfg->max_pages * cfg->page_size + 127) / 128 + 1;
+  const int64_t tiles = ((int64_t)cfg->max_pages * cfg->page_size + 127) / 128 + 1 + kAttnPieceCost;
   if (R > kMaxRequests || T > kMaxRows || (int64_t)T * cfg->n_heads * 32 >= ((int64_t)1 << 31) ||
       ((int64_t)T + R) * cfg->n_kv_heads * tiles >= ((int64_t)1 << 31))
     return MOE_ERR_UNSUPPORTED;
