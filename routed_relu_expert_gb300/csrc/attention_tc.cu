@@ -84,7 +84,7 @@ constexpr int kStarts = 1, kEnds = 2, kLast = 4;
 struct Small {
   uint64_t full[10], empty[10];
   uint64_t piece_full[kQueue], piece_empty[kQueue];
-  uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done[2], o_free, meet, group, pair[4], drain;
+  uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done[2], o_free, meet, group, drain;
   float top[2][2][kAttnRows];                  // [tile parity][group][row] maxima of the halves
   float sum[2][2][kAttnRows];                  // [piece parity][group][row]
   uint32_t odd[2][2][4];                       // [tile parity][half of the head]: nodes whose V is not finite
@@ -110,6 +110,10 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+
+// the barrier of the two softmax warps that share rows (hardware barriers 1 .. 4)
+__device__ __forceinline__ void pair_sync(int q) { asm volatile("bar.sync %0, 64;" ::"r"(q + 1) : "memory"); }
+__device__ __forceinline__ void pair_arrive(int q) { asm volatile("bar.arrive %0, 64;" ::"r"(q + 1) : "memory"); }
 
 // one thread of a converged warp
 __device__ __forceinline__ bool elect_one() {
@@ -177,6 +181,28 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+// The warp's wait for a phase: a few tries that do not suspend the warp (the
+// hot waits end within them, and a suspended warp's wake-up is dearer than they
+// are), then the bounded wait of the other tensor-core kernels.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __noinline__ bool wait_slow(uint32_t b, uint32_t parity, volatile int* abort_flag, int32_t* err) {
+  return __all_sync(0xffffffffu, mbar_wait<false, true>(b, parity, abort_flag, err));
+}
+__device__ __forceinline__ bool wait_warp(uint32_t b, uint32_t parity, volatile int* abort_flag, int32_t* err) {
+#pragma unroll 1
+  for (int i = 0; i < 32; ++i)
+    if (__all_sync(0xffffffffu, mbar_test(b, parity))) return true;
+  return wait_slow(b, parity, abort_flag, err);
 }
 
 // shared-memory descriptor of V as the MN-major B operand: 64 values of a key
@@ -278,7 +304,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(sm.p_full[w]), kSoftWarps);
       mbar_init(bar(sm.pv_done[w]), 1);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(bar(sm.pair[i]), 2);
     mbar_init(bar(sm.group), kSoftWarps);
     mbar_init(bar(sm.o_free), kSoftWarps);
     mbar_init(bar(sm.meet), kSoftWarps);
@@ -334,8 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int taken = 0;
   auto next = [&](Piece& p) {
     const int e = taken % kQueue;
-    if (!__all_sync(0xffffffffu, mbar_wait(bar(sm.piece_full[e]), (uint32_t)(taken / kQueue) & 1u, abort_flag, err)))
-      return false;
+    if (!wait_warp(bar(sm.piece_full[e]), (uint32_t)(taken / kQueue) & 1u, abort_flag, err)) return false;
     p = sm.piece[e];
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(sm.piece_empty[e]));
@@ -384,9 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         p.n = max(t1 - t0, 0);
       }
       const int e = made % kQueue;
-      if (!__all_sync(0xffffffffu,
-                      mbar_wait(bar(sm.piece_empty[e]), ((uint32_t)(made / kQueue) & 1u) ^ 1u, abort_flag, err)))
-        break;
+      if (!wait_warp(bar(sm.piece_empty[e]), ((uint32_t)(made / kQueue) & 1u) ^ 1u, abort_flag, err)) break;
       if (lane == 0) {
         sm.piece[e] = p;
         mbar_arrive(bar(sm.piece_full[e]));
@@ -417,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       int id[3] = {page_of(0), page_of(1), -1};            // tiles j, j + 1, j + 2
       if (who == 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(sm.q_empty), (pieces & 1) ^ 1, abort_flag, err));
+        ok = wait_warp(bar(sm.q_empty), (pieces & 1) ^ 1, abort_flag, err);
         if (!ok) break;
         if (elect_one()) {
           mbar_expect_tx(bar(sm.q_full), (uint32_t)(X::NH * 128 * a.G * tb));
@@ -429,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++pieces;
       auto load = [&](const CUtensorMap* map, int j, int pid) {
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(sm.empty[slot]), phase ^ 1u, abort_flag, err));
+        ok = wait_warp(bar(sm.empty[slot]), phase ^ 1u, abort_flag, err);
         if (!ok) return;
         const int boxes = __popc(__ballot_sync(0xffffffffu, pid >= 0));   // lanes 0 .. boxes - 1
         const int off = ((p.t0 + j) * kTile) & (page - 1);                // pages larger than a tile
@@ -485,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int tiles = 0;                                       // of all pieces so far; buffer b = tile & 1
     bool ok = true, issued = false;
     auto wait = [&](uint64_t& b, uint32_t parity) {
-      ok = ok && __all_sync(0xffffffffu, mbar_wait<false, true>(bar(b), parity, abort_flag, err));
+      ok = ok && wait_warp(bar(b), parity, abort_flag, err);
       return ok;
     };
     auto advance = [&]() {
@@ -568,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int tiles = 0, items = 0, meets = 0, groups = 0, pairs = 0;
     bool ok = true, joins = false;
     auto wait = [&](uint64_t& b, uint32_t parity) {
-      ok = __all_sync(0xffffffffu, mbar_wait<false, true>(bar(b), parity, abort_flag, err));
+      ok = wait_warp(bar(b), parity, abort_flag, err);
       return ok;
     };
     auto arrive = [&](uint64_t& b) {
@@ -657,8 +679,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
           // the other half's maximum
           sm.top[pairs & 1][w][row] = top;
-          arrive(sm.pair[qd]);
-          if (!wait(sm.pair[qd], pairs & 1)) break;
+          ok = !*abort_flag;
+          if (!__all_sync(0xffffffffu, ok)) break;
+          pair_sync(qd);
           top = fmaxf(top, sm.top[pairs & 1][w ^ 1][row]) * c;
           ++pairs;
           const bool raise = top > mc + kRaise || (mc == -INFINITY && top > mc);
@@ -682,8 +705,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          // the P of two tiles ago has been multiplied
-          if (use > 0 && !wait(sm.pv_done[b], (use - 1) & 1u)) break;
+          // (P of two tiles ago has been multiplied: that product was issued before this tile's S, and the commit
+          // behind s_full covers all that was issued before it)
           const float base = mc == -INFINITY ? 0.f : mc;
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -772,6 +795,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         arrive(sm.o_free);
       }
     }
+    // a warp that gave up lets its partner through (which then sees the abort flag before it waits again)
+    if (*abort_flag) pair_arrive(qd);
     if (threadIdx.x == 0 && !joins) a.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
   }
   tc_fence_before();
