@@ -218,6 +218,26 @@ __device__ __forceinline__ uint64_t v_desc(uint32_t addr) {
   return d;
 }
 
+// lane l of four holds x[0..3]; after it, x[i] is what lane i of the four had in x[l]
+__device__ __forceinline__ void transpose4(uint4 (&x)[4], int lane) {
+  auto swap = [&](uint4& mine, int by) {
+    mine.x = __shfl_xor_sync(0xffffffffu, mine.x, by);
+    mine.y = __shfl_xor_sync(0xffffffffu, mine.y, by);
+    mine.z = __shfl_xor_sync(0xffffffffu, mine.z, by);
+    mine.w = __shfl_xor_sync(0xffffffffu, mine.w, by);
+  };
+  // two by two blocks, then the pairs inside them
+#pragma unroll
+  for (int by = 2; by > 0; by >>= 1)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & by) continue;
+      uint4 send = lane & by ? x[i] : x[i | by];
+      swap(send, by);
+      if (lane & by) x[i] = send; else x[i | by] = send;
+    }
+}
+
 // ---------------------------------------------------------------------------
 // nodes whose V is not finite (out of the hot path's registers)
 // ---------------------------------------------------------------------------
@@ -368,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp == 11) {
-    // ---------------- the run's pieces, worked out ahead of the other warps ----------------
+    // ---------------- the run's pieces, worked out ahead of the other warps, and their Q ----------------
     // a unit's cost is kAttnPieceCost, then a tile each
     auto owner = [&](int at) { return (int)((((int64_t)at + 1) * runs - 1) / total); };
     int r = 0;
@@ -376,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int mid = (r + hi) >> 1;
       if (prefix[mid] <= begin) r = mid; else hi = mid;
     }
-    int pos = begin, made = 0;
+    int pos = begin, made = 0, loads = 0;
     bool last = false;
     Req q;
     int have = -1;
@@ -415,14 +435,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       ++made;
+      if (last || p.n == 0) continue;
+      // Q, once the last S of the piece before is done; K and V of this piece are on their way meanwhile
+      if (!wait_warp(bar(sm.q_empty), (loads & 1) ^ 1, abort_flag, err)) break;
+      if (elect_one()) {
+        mbar_expect_tx(bar(sm.q_full), (uint32_t)(X::NH * 128 * a.G * tb));
+#pragma unroll
+        for (int hh = 0; hh < X::NH; ++hh)
+          tma_load_3d(q_smem + hh * kHalfBytes, &maps.q, 64 * hh, p.h * a.G, p.row0, bar(sm.q_full));
+      }
+      __syncwarp();
+      ++loads;
+    }
+    if (*abort_flag && loads > 0) {
+      // the copy in flight must land before the CTA leaves
+      const uint64_t t0 = globaltimer();
+      while (!mbar_try(bar(sm.q_full), (uint32_t)(loads - 1) & 1u) && globaltimer() - t0 < kWaitLimitNs) {
+      }
+      __syncwarp();
     }
   } else if (warp == 8 || warp == 10) {
-    // ---------------- K, V (and Q) into shared memory ----------------
+    // ---------------- K and V into shared memory ----------------
     // the boxes of a tile (page by page, half by half) are shared between the two loaders
     const int who = warp == 8 ? 0 : 1;
     const int page = 1 << a.page_shift, rows = min(page, kTile);
     const int per_tile = kTile / rows;                     // boxes of a half: lane l < per_tile has box l
-    int slot = 0, it = 0, pieces = 0;
+    int slot = 0, it = 0;
     uint32_t phase = 0;
     bool ok = true;
     for (Piece p; ok && next(p);) {
@@ -438,18 +476,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         return a.n_pages;                                  // past the last page: TMA fills zeros
       };
       int id[3] = {page_of(0), page_of(1), -1};            // tiles j, j + 1, j + 2
-      if (who == 0) {
-        ok = wait_warp(bar(sm.q_empty), (pieces & 1) ^ 1, abort_flag, err);
-        if (!ok) break;
-        if (elect_one()) {
-          mbar_expect_tx(bar(sm.q_full), (uint32_t)(X::NH * 128 * a.G * tb));
-#pragma unroll
-          for (int hh = 0; hh < X::NH; ++hh)
-            tma_load_3d(q_smem + hh * kHalfBytes, &maps.q, 64 * hh, p.h * a.G, p.row0, bar(sm.q_full));
-        }
-        __syncwarp();
-      }
-      ++pieces;
       auto load = [&](const CUtensorMap* map, int j, int pid) {
         ok = wait_warp(bar(sm.empty[slot]), phase ^ 1u, abort_flag, err);
         if (!ok) return;
@@ -492,7 +518,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int uses = (it - s + NS - 1) / NS;           // times that slot s was filled
         if (it > s) land(bar(sm.full[s]), (uint32_t)(uses - 1) & 1u);
       }
-      if (who == 0 && pieces > 0) land(bar(sm.q_full), (uint32_t)(pieces - 1) & 1u);
     }
     __syncwarp();
   } else if (warp == 9) {
@@ -604,47 +629,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int node = p.tok0 + row_tok;
       const int32_t* mask = a.tree_mask ? a.tree_mask + (int64_t)(p.row0 + min(row_tok, p.ntok - 1)) * a.mask_words
                                         : nullptr;
+      // the mask's first words, ahead of the tiles that need them
+      const uint32_t m0 = mask ? (uint32_t)mask[0] : 0u, m1 = mask && a.mask_words > 1 ? (uint32_t)mask[1] : 0u;
       float mc = -INFINITY, l = 0.f;
       for (int j = 0; j < p.n; ++j, ++tiles) {
         const int b = tiles & 1;
         const uint32_t use = (uint32_t)(tiles >> 1);         // times that buffer b was used before
         const int key0 = (p.t0 + j) * kTile;
         const bool special = key0 + kTile > p.ctx;
-        bool any_odd = false;
-        if (special) {
-          // V rows past the last key, and nodes' rows that are not finite, become zeros (by halves of the head)
-          const int item = items + v_item(j, p.n);
-          if (!wait(sm.full[item % NS], (uint32_t)(item / NS) & 1u)) break;
-          const int key = key0 + row;
-          uint4* v0 = reinterpret_cast<uint4*>(ring_ptr + (item % NS) * X::SLOT + w * kHalfBytes + row * 128);
-          bool zero = key >= p.kv, strange = false;
-          if (w < X::NH) {
-            if (!zero && key >= p.ctx) {
-              uint32_t hit = 0;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const uint4 x = v0[i];
-                const uint32_t ws[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  hit |= ((ws[e] & 0x7F80u) == 0x7F80u) | ((ws[e] & 0x7F800000u) == 0x7F800000u);
-              }
-              strange = hit != 0;
-            }
-            if (zero || strange) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) v0[i] = make_uint4(0, 0, 0, 0);
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          }
-          const uint32_t mine = __ballot_sync(0xffffffffu, strange);
-          if (lane == 0) sm.odd[b][w][qd] = mine;
-          arrive(sm.group);
-          if (!wait(sm.group, groups & 1)) break;
-          ++groups;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) any_odd |= sm.odd[b][w][i] != 0;
-        }
         if (!wait(sm.s_full[b], use & 1u)) break;
         if (live_warp) {
           tc_fence_after();
@@ -663,7 +655,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!mask) {
                 bits = low(node + 1 - j0);
               } else {
-                auto word = [&](int i) { return i < 0 ? 0xffffffffu : i < a.mask_words ? (uint32_t)mask[i] : 0u; };
+                auto word = [&](int i) {
+                  return i < 0 ? 0xffffffffu : i == 0 ? m0 : i == 1 ? m1 : i < a.mask_words ? (uint32_t)mask[i] : 0u;
+                };
                 const int wi = j0 >> 5;
                 bits = j0 + 32 <= 0 ? 0xffffffffu : __funnelshift_r(word(wi), word(wi + 1), (uint32_t)(j0 & 31));
               }
@@ -725,6 +719,41 @@ __global__ void __launch_bounds__(kThreads, 1)
           st_wait();
           tc_fence_before();
         }
+        bool any_odd = false;
+        if (special) {
+          // V rows past the last key, and nodes' rows that are not finite, become zeros (by halves of the head)
+          const int item = items + v_item(j, p.n);
+          if (!wait(sm.full[item % NS], (uint32_t)(item / NS) & 1u)) break;
+          const int key = key0 + row;
+          uint4* v0 = reinterpret_cast<uint4*>(ring_ptr + (item % NS) * X::SLOT + w * kHalfBytes + row * 128);
+          bool zero = key >= p.kv, strange = false;
+          if (w < X::NH) {
+            if (!zero && key >= p.ctx) {
+              uint32_t hit = 0;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const uint4 x = v0[i ^ (row & 7)];           // (eight lanes, eight bank groups)
+                const uint32_t ws[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  hit |= ((ws[e] & 0x7F80u) == 0x7F80u) | ((ws[e] & 0x7F800000u) == 0x7F800000u);
+              }
+              strange = hit != 0;
+            }
+            if (zero || strange) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v0[i ^ (row & 7)] = make_uint4(0, 0, 0, 0);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          }
+          const uint32_t mine = __ballot_sync(0xffffffffu, strange);
+          if (lane == 0) sm.odd[b][w][qd] = mine;
+          arrive(sm.group);
+          if (!wait(sm.group, groups & 1)) break;
+          ++groups;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) any_odd |= sm.odd[b][w][i] != 0;
+        }
         arrive(sm.p_full[b]);
         if (live_warp && any_odd) {
           // p v of the nodes whose V is not finite
@@ -766,19 +795,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = sum == 0.f ? 0.f : o[i] * g;
-          if (mine && whole) {
-            bf16* out = reinterpret_cast<bf16*>(a.out) + tok * a.out_ld + (int64_t)head * a.D + c0;
+          if (whole) {
+            // a row's 64 bytes of the chunk as one piece: four lanes exchange 16-byte quarters, so that a store of the
+            // warp touches 8 lines and not 32
+            uint4 x[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              if (c0 + 8 * i < a.D)
-                *reinterpret_cast<uint4*>(out + 8 * i) =
-                    make_uint4(pack_bf16(o[8 * i], o[8 * i + 1]), pack_bf16(o[8 * i + 2], o[8 * i + 3]),
-                               pack_bf16(o[8 * i + 4], o[8 * i + 5]), pack_bf16(o[8 * i + 6], o[8 * i + 7]));
+              x[i] = make_uint4(pack_bf16(o[8 * i], o[8 * i + 1]), pack_bf16(o[8 * i + 2], o[8 * i + 3]),
+                                pack_bf16(o[8 * i + 4], o[8 * i + 5]), pack_bf16(o[8 * i + 6], o[8 * i + 7]));
+            transpose4(x, lane);
+            bf16* out = reinterpret_cast<bf16*>(a.out) + (int64_t)p.row0 * a.out_ld + (int64_t)p.h * a.G * a.D + c0 +
+                        8 * (lane & 3);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r2 = (row & ~3) + i, t2 = r2 / a.G;
+              if (r2 < valid && c0 + 8 * (lane & 3) < a.D)
+                *reinterpret_cast<uint4*>(out + t2 * a.out_ld + (int64_t)(r2 - t2 * a.G) * a.D) = x[i];
+            }
           } else if (mine) {
-            float* out = a.part + ((int64_t)slot * kAttnRows + row) * kAttnPartDim + c0;
+            // partials: [four columns][row]
+            float* out = a.part + (int64_t)slot * kAttnRows * kAttnPartDim + ((c0 / 4) * kAttnRows + row) * 4;
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<float4*>(out + 4 * i) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+              *reinterpret_cast<float4*>(out + 4 * i * kAttnRows) =
+                  make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
           }
         }
         if (mine && w == 0) {
@@ -809,61 +849,62 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Units that a run's end cut: run c's unit that began but did not end in it has
 // its partials in slot 2c + 1 (its own) and 2 (c + 1), 2 (c + 2), ... of the runs
-// after it.  A warp a row, a lane four columns, parts in ascending order.
-constexpr int kJoinWarps = 8;
+// after it.  A lane a row, a warp four columns (the partials are laid out for it),
+// parts in ascending order, eight in flight; the block's 32 rows meet in shared
+// memory to be written whole.
+constexpr int kJoinWarps = kAttnPartDim / 4;
 __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const AttnArgs a) {
   pdl_wait();
   const int4 u = a.joins[blockIdx.x];
-  const int lane = threadIdx.x & 31, valid = u.z * a.G;
-  if (u.x < 2) return;
-  const int row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
-  if (row >= valid) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, valid = u.z * a.G;
+  const int row0 = blockIdx.y * 32;
+  if (u.x < 2 || row0 >= valid) return;
+  __shared__ uint2 s_out[32][kJoinWarps + 1];
+  const int row = min(row0 + lane, valid - 1);
   auto slot = [&](int p) { return 2 * ((int)blockIdx.x + p) + (p == 0 ? 1 : 0); };
-  float top = -INFINITY;
-  for (int p = lane; p < u.x; p += 32) {
-    const float2 ml = a.part_ml[slot(p) * kAttnRows + row];
-    if (ml.y != 0.f) top = fmaxf(top, ml.x);
-  }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-  float sum = 0.f;
+  const float* part = a.part + (warp * kAttnRows + row) * 4;
+  float top = -INFINITY, sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int p0 = 0; p0 < u.x; p0 += 32) {
-    const int np = min(32, u.x - p0);
-    float f = 0.f, l = 0.f;
-    if (lane < np) {
-      const float2 ml = a.part_ml[slot(p0 + lane) * kAttnRows + row];
-      l = ml.y;
-      f = l == 0.f ? 0.f : ex2(ml.x - top);
+  for (int p = 0; p < u.x; p += 8) {
+    float2 ml[8];
+    float4 v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const bool in = p + k < u.x;
+      ml[k] = in ? a.part_ml[slot(p + k) * kAttnRows + row] : make_float2(0.f, 0.f);
+      v[k] = in ? *reinterpret_cast<const float4*>(part + (int64_t)slot(p + k) * kAttnRows * kAttnPartDim)
+                : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    for (int p = 0; p < np; p += 16) {
-      float4 v[16];
+    float t = top;
 #pragma unroll
-      for (int k = 0; k < 16; ++k)
-        v[k] = p + k < np && 4 * lane < a.D
-                   ? *reinterpret_cast<const float4*>(a.part + ((int64_t)slot(p0 + p + k) * kAttnRows + row) *
-                                                                   kAttnPartDim + 4 * lane)
-                   : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < 8; ++k)
+      if (ml[k].y != 0.f) t = fmaxf(t, ml[k].x);
+    const float g = sum == 0.f ? 0.f : ex2(top - t);
+    top = t;
+    sum *= g;
+    acc = make_float4(acc.x * g, acc.y * g, acc.z * g, acc.w * g);
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const float fk = __shfl_sync(0xffffffffu, f, (p + k) & 31), lk = __shfl_sync(0xffffffffu, l, (p + k) & 31);
-        if (p + k >= np) continue;
-        sum = fmaf(lk, fk, sum);
-        acc.x = fmaf(v[k].x, fk, acc.x);
-        acc.y = fmaf(v[k].y, fk, acc.y);
-        acc.z = fmaf(v[k].z, fk, acc.z);
-        acc.w = fmaf(v[k].w, fk, acc.w);
-      }
+    for (int k = 0; k < 8; ++k) {
+      if (ml[k].y == 0.f) continue;            // no visible key in that part
+      const float f = ex2(ml[k].x - top);
+      sum = fmaf(ml[k].y, f, sum);
+      acc.x = fmaf(v[k].x, f, acc.x);
+      acc.y = fmaf(v[k].y, f, acc.y);
+      acc.z = fmaf(v[k].z, f, acc.z);
+      acc.w = fmaf(v[k].w, f, acc.w);
     }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int64_t tok = u.y + row / a.G;
-  const int head = u.w * a.G + row % a.G;
-  if (4 * lane < a.D)
-    *reinterpret_cast<uint2*>(reinterpret_cast<bf16*>(a.out) + tok * a.out_ld + (int64_t)head * a.D + 4 * lane) =
-        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-  if (a.lse && lane == 0)
-    a.lse[tok * a.H + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+  s_out[lane][warp] = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  if (a.lse && warp == 0 && row0 + lane < valid)
+    a.lse[(int64_t)(u.y + row / a.G) * a.H + u.w * a.G + row % a.G] =
+        sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+  __syncthreads();
+  const int per_row = a.D / 4;                 // warps of the block
+  const int r = threadIdx.x / per_row, r2 = row0 + r, c = threadIdx.x - r * per_row;
+  if (r2 < valid)
+    *reinterpret_cast<uint2*>(reinterpret_cast<bf16*>(a.out) + (int64_t)(u.y + r2 / a.G) * a.out_ld +
+                              (int64_t)(u.w * a.G + r2 % a.G) * a.D + 4 * c) = s_out[r][c];
 }
 
 // ---------------------------------------------------------------------------
@@ -912,8 +953,8 @@ cudaError_t launch_dp(const AttnArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   e = launch_k(attention_tc_kernel<DP>, dim3((unsigned)sms), dim3(kThreads), smem, s, maps, a, tb);
   if (e != cudaSuccess) return e;
-  return launch_k(attention_join_kernel, dim3((unsigned)sms, (unsigned)ceil_div(tb * a.G, kJoinWarps)),
-                  dim3(32 * kJoinWarps), 0, s, a);
+  return launch_k(attention_join_kernel, dim3((unsigned)sms, (unsigned)ceil_div(tb * a.G, 32)), dim3(32 * (a.D / 4)), 0,
+                  s, a);
 }
 
 }  // namespace

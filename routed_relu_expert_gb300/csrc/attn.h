@@ -19,11 +19,11 @@ struct AttnHeader {
 static_assert(sizeof(AttnHeader) == MOE_ATTN_HEADER_BYTES, "attention workspace header");
 
 // Split partials: kAttnMaxCtas blocks own two slots of 128 rows each: the rows'
-// FP32 output sums (pitch kAttnPartDim) and, after all of them, (max, sum).
+// FP32 output sums ([four columns][row]) and, after all of them, (max, sum).
 constexpr int kAttnMaxCtas = 160;
 constexpr int kAttnRows = 128;
 constexpr int kAttnPartDim = 128;
-constexpr int kAttnPieceCost = 2;              // a unit's fixed cost beside its key tiles, in tiles
+constexpr int kAttnPieceCost = 5;              // a unit's fixed cost beside its key tiles, in tiles
 constexpr size_t kAttnPartSlots = 2 * kAttnMaxCtas;
 constexpr size_t kAttnPartBytes = kAttnPartSlots * kAttnRows * (kAttnPartDim + 2) * 4;
 constexpr size_t kAttnJoinBytes = kAttnMaxCtas * 16;   // a record a run: what the join kernel adds
@@ -70,7 +70,7 @@ struct AttnArgs {
   void* out;
   float* lse;
   AttnHeader* hdr;
-  float* part;              // [slots][128 rows][kAttnPartDim]
+  float* part;              // [slots] of 128 x kAttnPartDim
   float2* part_ml;          // [slots][128 rows] (max, sum)
   int4* joins;              // [runs] (parts or 0, first row, nodes, KV head)
   int64_t q_ld, out_ld, page_stride, token_stride, head_stride;
