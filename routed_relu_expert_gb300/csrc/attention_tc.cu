@@ -35,6 +35,7 @@
 #include "tc_common.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace moe {
 
@@ -632,138 +633,169 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the mask's first words, ahead of the tiles that need them
       const uint32_t m0 = mask ? (uint32_t)mask[0] : 0u, m1 = mask && a.mask_words > 1 ? (uint32_t)mask[1] : 0u;
       float mc = -INFINITY, l = 0.f;
-      for (int j = 0; j < p.n; ++j, ++tiles) {
-        const int b = tiles & 1;
-        const uint32_t use = (uint32_t)(tiles >> 1);         // times that buffer b was used before
+
+      float v[64];                             // this thread's scores: half of its row's keys of a tile
+      auto ready = [&](int j) { return wait(sm.s_full[(tiles + j) & 1], (uint32_t)((tiles + j) >> 1) & 1u); };
+      auto scores_at = [&](int j) { return tmem + lane_addr + X::s_col((tiles + j) & 1) + 64u * w; };
+      // tile j's scores arrived and masked, their maximum told to the thread of the other half
+      auto look = [&](int j) {
+        ld32_wait<0>(v);
+        ld32_wait<32>(v);
         const int key0 = (p.t0 + j) * kTile;
-        const bool special = key0 + kTile > p.ctx;
-        if (!wait(sm.s_full[b], use & 1u)) break;
-        if (live_warp) {
-          tc_fence_after();
-          float v[64];
-          const uint32_t s_addr = tmem + lane_addr + X::s_col(b) + 64u * w;
-          ld32_async<0>(s_addr, v);
-          ld32_async<32>(s_addr + 32, v);
-          ld32_wait<0>(v);
-          ld32_wait<32>(v);
-          if (special) {
-#pragma unroll
-            for (int cc = 0; cc < 2; ++cc) {
-              const int k0 = key0 + 64 * w + 32 * cc, j0 = k0 - p.ctx;   // first key of the word, as a node
-              auto low = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
-              uint32_t bits;
-              if (!mask) {
-                bits = low(node + 1 - j0);
-              } else {
-                auto word = [&](int i) {
-                  return i < 0 ? 0xffffffffu : i == 0 ? m0 : i == 1 ? m1 : i < a.mask_words ? (uint32_t)mask[i] : 0u;
-                };
-                const int wi = j0 >> 5;
-                bits = j0 + 32 <= 0 ? 0xffffffffu : __funnelshift_r(word(wi), word(wi + 1), (uint32_t)(j0 & 31));
-              }
-              bits &= low(p.kv - k0);
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!(bits >> i & 1u)) v[32 * cc + i] = -INFINITY;
-            }
-          }
-          float t4[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-          for (int i = 4; i < 64; ++i) t4[i & 3] = fmaxf(t4[i & 3], v[i]);
-          float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-          // the other half's maximum
-          sm.top[pairs & 1][w][row] = top;
-          ok = !*abort_flag;
-          if (!__all_sync(0xffffffffu, ok)) break;
-          pair_sync(qd);
-          top = fmaxf(top, sm.top[pairs & 1][w ^ 1][row]) * c;
-          ++pairs;
-          const bool raise = top > mc + kRaise || (mc == -INFINITY && top > mc);
-          if (__any_sync(0xffffffffu, raise)) {
-            const float f = raise ? (mc == -INFINITY ? 0.f : ex2(mc - top)) : 1.f;
-            if (raise) mc = top;
-            l *= f;
-            if (j > 0) {
-              // O so far (this group's columns) scaled to the new reference
-              if (!wait(sm.pv_done[b ^ 1], (uint32_t)((tiles - 1) >> 1) & 1u)) break;
-              tc_fence_after();
-#pragma unroll
-              for (int c0 = 0; c0 < DP / 2; c0 += 32) {
-                float o[32];
-                const uint32_t addr = tmem + lane_addr + X::O + (uint32_t)(w * (DP / 2) + c0);
-                ld32_async<0>(addr, o);
-                ld32_wait<0>(o);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] *= f;
-                st32(addr, o);
-              }
-            }
-          }
-          // (P of two tiles ago has been multiplied: that product was issued before this tile's S, and the commit
-          // behind s_full covers all that was issued before it)
-          const float base = mc == -INFINITY ? 0.f : mc;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        if (key0 + kTile > p.ctx) {
 #pragma unroll
           for (int cc = 0; cc < 2; ++cc) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float x = ex2(fmaf(v[32 * cc + 2 * i], c, -base)), y = ex2(fmaf(v[32 * cc + 2 * i + 1], c, -base));
-              sum[(2 * i) & 3] += x;
-              sum[(2 * i + 1) & 3] += y;
-              pk[i] = pack_bf16(x, y);
+            const int k0 = key0 + 64 * w + 32 * cc, j0 = k0 - p.ctx;   // first key of the word, as a node
+            auto low = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
+            uint32_t bits;
+            if (!mask) {
+              bits = low(node + 1 - j0);
+            } else {
+              auto word = [&](int i) {
+                return i < 0 ? 0xffffffffu : i == 0 ? m0 : i == 1 ? m1 : i < a.mask_words ? (uint32_t)mask[i] : 0u;
+              };
+              const int wi = j0 >> 5;
+              bits = j0 + 32 <= 0 ? 0xffffffffu : __funnelshift_r(word(wi), word(wi + 1), (uint32_t)(j0 & 31));
             }
-            st16(tmem + lane_addr + X::p_col(b) + 32u * w + 16u * cc, pk);
+            bits &= low(p.kv - k0);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!(bits >> i & 1u)) v[32 * cc + i] = -INFINITY;
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        }
+        float t4[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+        for (int i = 4; i < 64; ++i) t4[i & 3] = fmaxf(t4[i & 3], v[i]);
+        const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+        sm.top[pairs & 1][w][row] = top;
+        return top;
+      };
+      // both halves' maxima: the reference for tile j, O scaled to it where it rose
+      auto agree = [&](int j, float top, int gone) {
+        if (__any_sync(0xffffffffu, gone)) {
+          ok = false;
+          return;
+        }
+        pair_sync(qd);
+        top = fmaxf(top, sm.top[pairs & 1][w ^ 1][row]) * c;
+        ++pairs;
+        const bool raise = top > mc + kRaise || (mc == -INFINITY && top > mc);
+        if (__any_sync(0xffffffffu, raise)) {
+          const float f = raise ? (mc == -INFINITY ? 0.f : ex2(mc - top)) : 1.f;
+          if (raise) mc = top;
+          l *= f;
+          if (j > 0) {
+            // this group's columns of O, after the tile before
+            const int last = tiles + j - 1;
+            if (!wait(sm.pv_done[last & 1], (uint32_t)(last >> 1) & 1u)) return;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c0 = 0; c0 < DP / 2; c0 += 32) {
+              float o[32];
+              const uint32_t addr = tmem + lane_addr + X::O + (uint32_t)(w * (DP / 2) + c0);
+              ld32_async<0>(addr, o);
+              ld32_wait<0>(o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] *= f;
+              st32(addr, o);
+            }
+            st_wait();
+          }
+        }
+      };
+      // 32 probabilities, from the CC'th half of the scores
+      auto exps = [&](auto CC, int b, float base) {
+        constexpr int cc = decltype(CC)::value;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float x = ex2(fmaf(v[32 * cc + 2 * i], c, -base)), y = ex2(fmaf(v[32 * cc + 2 * i + 1], c, -base));
+          sum[(2 * i) & 3] += x;
+          sum[(2 * i + 1) & 3] += y;
+          pk[i] = pack_bf16(x, y);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        st16(tmem + lane_addr + X::p_col(b) + 32u * w + 16u * cc, pk);
+      };
+      // V rows of tile j past the last key, and nodes' rows that are not finite, become zeros (by halves of the
+      // head); whether there is a node of the second kind
+      auto clean = [&](int j) {
+        const int b = (tiles + j) & 1, key0 = (p.t0 + j) * kTile;
+        const int item = items + v_item(j, p.n);
+        if (!wait(sm.full[item % NS], (uint32_t)(item / NS) & 1u)) return false;
+        const int key = key0 + row;
+        uint4* v0 = reinterpret_cast<uint4*>(ring_ptr + (item % NS) * X::SLOT + w * kHalfBytes + row * 128);
+        const bool zero = key >= p.kv;
+        bool strange = false;
+        if (w < X::NH) {
+          if (!zero && key >= p.ctx) {
+            uint32_t hit = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint4 x = v0[i ^ (row & 7)];               // (eight lanes, eight bank groups)
+              const uint32_t ws[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                hit |= ((ws[e] & 0x7F80u) == 0x7F80u) | ((ws[e] & 0x7F800000u) == 0x7F800000u);
+            }
+            strange = hit != 0;
+          }
+          if (zero || strange) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v0[i ^ (row & 7)] = make_uint4(0, 0, 0, 0);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        const uint32_t mine = __ballot_sync(0xffffffffu, strange);
+        if (lane == 0) sm.odd[b][w][qd] = mine;
+        arrive(sm.group);
+        if (!wait(sm.group, groups & 1)) return false;
+        ++groups;
+        return (sm.odd[b][w][0] | sm.odd[b][w][1] | sm.odd[b][w][2] | sm.odd[b][w][3]) != 0;
+      };
+      if (p.n > 0 && ready(0) && live_warp) {
+        tc_fence_after();
+        ld32_async<0>(scores_at(0), v);
+        ld32_async<32>(scores_at(0) + 32, v);
+        agree(0, look(0), *abort_flag);
+      }
+      for (int j = 0; j < p.n && ok; ++j) {
+        // tile j's scores are in v and its reference stands; the next tile's replace them half by half, so that
+        // their way from tensor memory runs beside the exponentials
+        const int b = (tiles + j) & 1, gone = *abort_flag;
+        const bool more = j + 1 < p.n;
+        const float base = mc == -INFINITY ? 0.f : mc;
+        // (P of two tiles ago has been multiplied: that product was issued before this tile's S, and the commit
+        // behind s_full covers all that was issued before it)
+        if (live_warp) exps(std::integral_constant<int, 0>(), b, base);
+        if (more && !ready(j + 1)) break;
+        if (live_warp) {
+          tc_fence_after();
+          if (more) ld32_async<0>(scores_at(j + 1), v);
+          exps(std::integral_constant<int, 1>(), b, base);
+          if (more) ld32_async<32>(scores_at(j + 1) + 32, v);
+        }
+        const bool any_odd = (p.t0 + j + 1) * kTile > p.ctx && clean(j);
+        if (!ok) break;
+        if (live_warp) {
           st_wait();
           tc_fence_before();
         }
-        bool any_odd = false;
-        if (special) {
-          // V rows past the last key, and nodes' rows that are not finite, become zeros (by halves of the head)
-          const int item = items + v_item(j, p.n);
-          if (!wait(sm.full[item % NS], (uint32_t)(item / NS) & 1u)) break;
-          const int key = key0 + row;
-          uint4* v0 = reinterpret_cast<uint4*>(ring_ptr + (item % NS) * X::SLOT + w * kHalfBytes + row * 128);
-          bool zero = key >= p.kv, strange = false;
-          if (w < X::NH) {
-            if (!zero && key >= p.ctx) {
-              uint32_t hit = 0;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const uint4 x = v0[i ^ (row & 7)];           // (eight lanes, eight bank groups)
-                const uint32_t ws[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  hit |= ((ws[e] & 0x7F80u) == 0x7F80u) | ((ws[e] & 0x7F800000u) == 0x7F800000u);
-              }
-              strange = hit != 0;
-            }
-            if (zero || strange) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) v0[i ^ (row & 7)] = make_uint4(0, 0, 0, 0);
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          }
-          const uint32_t mine = __ballot_sync(0xffffffffu, strange);
-          if (lane == 0) sm.odd[b][w][qd] = mine;
-          arrive(sm.group);
-          if (!wait(sm.group, groups & 1)) break;
-          ++groups;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) any_odd |= sm.odd[b][w][i] != 0;
-        }
         arrive(sm.p_full[b]);
-        if (live_warp && any_odd) {
+        if (!live_warp) continue;
+        if (any_odd) {
           // p v of the nodes whose V is not finite
-          if (!wait(sm.pv_done[b], use & 1u)) break;
+          if (!wait(sm.pv_done[b], (uint32_t)((tiles + j) >> 1) & 1u)) break;
           tc_fence_after();
-          add_odd(a, p.r, p.h, key0, sm.odd[b][w], 64 * w, tmem + lane_addr + X::p_col(b), tmem + lane_addr + X::O);
+          add_odd(a, p.r, p.h, (p.t0 + j) * kTile, sm.odd[b][w], 64 * w, tmem + lane_addr + X::p_col(b),
+                  tmem + lane_addr + X::O);
           tc_fence_before();
           __syncwarp();
         }
+        if (more) agree(j + 1, look(j + 1), gone);
       }
+      tiles += p.n;
       if (!ok) break;
 
       // ---- the piece's end: write the rows or their partials ----
