@@ -85,7 +85,7 @@ constexpr int kStarts = 1, kEnds = 2, kLast = 4;
 struct Small {
   uint64_t full[10], empty[10];
   uint64_t piece_full[kQueue], piece_empty[kQueue];
-  uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done[2], o_free, meet, group, drain;
+  uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done[2], o_free, s_free[2], meet, group, drain;
   float top[2][2][kAttnRows];                  // [tile parity][group][row] maxima of the halves
   float sum[2][2][kAttnRows];                  // [piece parity][group][row]
   uint32_t odd[2][2][4];                       // [tile parity][half of the head]: nodes whose V is not finite
@@ -288,8 +288,10 @@ __device__ __forceinline__ Req request(const AttnArgs& a, int r, int tb, int* ba
   return q;
 }
 
-// order of a piece's tiles in the ring: K0, [K1, V0], [K2, V1], ..., V(n-1)
-__device__ __forceinline__ int v_item(int j, int n) { return j == n - 1 ? 2 * n - 1 : 2 * j + 2; }
+// order of a piece's tiles in the ring: K0, K1, [K2, V0], [K3, V1], ..., V(n-2), V(n-1)
+__device__ __forceinline__ int v_item(int j, int n) {
+  return j >= n - 2 ? 2 * n - (n - j) : 2 * j + 3;
+}
 
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -327,6 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(bar(sm.group), kSoftWarps);
     mbar_init(bar(sm.o_free), kSoftWarps);
+    for (int b = 0; b < 2; ++b) mbar_init(bar(sm.s_free[b]), kSoftWarps);
     mbar_init(bar(sm.meet), kSoftWarps);
     mbar_init(bar(sm.drain), 1);
     sm.abort = 0;
@@ -476,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         set_error(err, MOE_DEVERR_CACHE);
         return a.n_pages;                                  // past the last page: TMA fills zeros
       };
-      int id[3] = {page_of(0), page_of(1), -1};            // tiles j, j + 1, j + 2
+      int id[4] = {page_of(0), page_of(1), page_of(2), -1};   // tiles j .. j + 3
       auto load = [&](const CUtensorMap* map, int j, int pid) {
         ok = wait_warp(bar(sm.empty[slot]), phase ^ 1u, abort_flag, err);
         if (!ok) return;
@@ -500,12 +503,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       load(&maps.k, 0, id[0]);
+      if (ok && p.n > 1) load(&maps.k, 1, id[1]);
       for (int j = 0; j < p.n && ok; ++j) {
-        id[2] = page_of(j + 2);
-        if (j + 1 < p.n) load(&maps.k, j + 1, id[1]);
+        id[3] = page_of(j + 3);
+        if (j + 2 < p.n) load(&maps.k, j + 2, id[2]);
         if (ok) load(&maps.v, j, id[0]);
         id[0] = id[1];
         id[1] = id[2];
+        id[2] = id[3];
       }
     }
     if (*abort_flag && lane == 0) {
@@ -547,8 +552,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait(sm.q_full, pieces & 1)) break;
       auto scores = [&](int j) {
         const int b = (tiles + j) & 1;
-        // the buffer is free: its last S was read before its P, which PV waited for
         if (!wait(sm.full[slot], phase)) return;
+        // the buffer's last S has been read
+        if (tiles + j >= 2 && !wait(sm.s_free[b], (uint32_t)(((tiles + j) >> 1) - 1) & 1u)) return;
         tc_fence_after();
         issued = true;
         if (elect_one()) {
@@ -568,9 +574,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         advance();
       };
+      // S runs two tiles ahead of P V
       scores(0);
+      if (p.n > 1) scores(1);
       for (int j = 0; j < p.n && ok; ++j) {
-        if (j + 1 < p.n) scores(j + 1);
+        if (j + 2 < p.n) scores(j + 2);
         const int b = (tiles + j) & 1;
         if (!wait(sm.full[slot], phase) || !wait(sm.p_full[b], (uint32_t)((tiles + j) >> 1) & 1u)) break;
         // O of the previous piece has been read
@@ -641,6 +649,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto look = [&](int j) {
         ld32_wait<0>(v);
         ld32_wait<32>(v);
+        tc_fence_before();
+        arrive(sm.s_free[(tiles + j) & 1]);
         const int key0 = (p.t0 + j) * kTile;
         if (key0 + kTile > p.ctx) {
 #pragma unroll
@@ -754,7 +764,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++groups;
         return (sm.odd[b][w][0] | sm.odd[b][w][1] | sm.odd[b][w][2] | sm.odd[b][w][3]) != 0;
       };
-      if (p.n > 0 && ready(0) && live_warp) {
+      if (p.n > 0 && ready(0) && !live_warp) arrive(sm.s_free[tiles & 1]);
+      if (p.n > 0 && ok && live_warp) {
         tc_fence_after();
         ld32_async<0>(scores_at(0), v);
         ld32_async<32>(scores_at(0) + 32, v);
@@ -766,12 +777,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int b = (tiles + j) & 1, gone = *abort_flag;
         const bool more = j + 1 < p.n;
         const float base = mc == -INFINITY ? 0.f : mc;
-        // (P of two tiles ago has been multiplied: that product was issued before this tile's S, and the commit
-        // behind s_full covers all that was issued before it)
-        if (live_warp) exps(std::integral_constant<int, 0>(), b, base);
+        // P of two tiles ago has been multiplied: that product was issued before the next tile's S, and the commit
+        // behind s_full covers all that was issued before it
         if (more && !ready(j + 1)) break;
+        if (!more && tiles + j >= 2 && !wait(sm.pv_done[b], (uint32_t)(((tiles + j) >> 1) - 1) & 1u)) break;
         if (live_warp) {
           tc_fence_after();
+          exps(std::integral_constant<int, 0>(), b, base);
           if (more) ld32_async<0>(scores_at(j + 1), v);
           exps(std::integral_constant<int, 1>(), b, base);
           if (more) ld32_async<32>(scores_at(j + 1) + 32, v);
@@ -783,7 +795,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_before();
         }
         arrive(sm.p_full[b]);
-        if (!live_warp) continue;
+        if (!live_warp) {
+          if (more) arrive(sm.s_free[b ^ 1]);
+          continue;
+        }
         if (any_odd) {
           // p v of the nodes whose V is not finite
           if (!wait(sm.pv_done[b], (uint32_t)((tiles + j) >> 1) & 1u)) break;
