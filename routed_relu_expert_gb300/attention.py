@@ -20,6 +20,9 @@ import torch
 from . import _native as N
 from .layer import _s
 
+# the current stream's handle of a device, without building a Stream object for it (3 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
 _TORCH = {N.MOE_DT_BF16: torch.bfloat16, N.MOE_DT_F32: torch.float32}
 _SCALING = {None: N.MOE_ROPE_PLAIN, "linear": N.MOE_ROPE_LINEAR, "yarn": N.MOE_ROPE_YARN}
 
@@ -37,6 +40,12 @@ def make_attn_config(n_heads: int, n_kv_heads: int, head_dim: int, *, page_size:
         softmax_scale = 1.0 / math.sqrt(head_dim) if head_dim > 0 else 1.0
     return N.MoeAttnConfig(n_heads, n_kv_heads, head_dim, page_size, n_pages, max_pages, rot_dim,
                            int(rope_interleaved), float(softmax_scale), dtype, *strides)
+
+
+def _stream(stream, t: torch.Tensor):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(t.get_device())
+    return _s(stream)
 
 
 def attn_workspace_bytes(cfg: N.MoeAttnConfig) -> int:
@@ -97,7 +106,7 @@ def moe_paged_plan(cfg, ctx_len, new_len, block_table, free_pages, free_head, q_
         _array(q_start, i32, R + 1, "q_start"), _array(kv_len, i32, R, "kv_len"),
         _array(positions, i32, T, "positions"), _array(slot_map, torch.int64, T, "slot_map"),
         _array(tree_mask, i32, T * words, "tree_mask"), words, _array(ws, torch.uint8, None, "ws"), ws.numel(),
-        _s(stream)), "moe_paged_plan")
+        _stream(stream, ws)), "moe_paged_plan")
 
 
 def rope_table(rot_dim: int, theta: float, *, scaling: Optional[str] = None, factor: float = 1.0,
@@ -127,7 +136,7 @@ def moe_rope(cfg, x, positions, table, out, rot_scale: float = 1.0, inverse: boo
     xp, x_ld = _rows(cfg, x, T, heads, "x")
     op, o_ld = _rows(cfg, out, T, heads, "out")
     N.check(N.load().moe_rope(ctypes.byref(cfg), T, heads, xp, x_ld, _array(positions, torch.int32, T, "positions"),
-                              _table(cfg, table), rot_scale, int(inverse), op, o_ld, _s(stream)), "moe_rope")
+                              _table(cfg, table), rot_scale, int(inverse), op, o_ld, _stream(stream, x)), "moe_rope")
 
 
 def moe_rope_append(cfg, q, k, v, positions, table, slot_map, k_cache, v_cache, q_out, ws, rot_scale: float = 1.0,
@@ -143,7 +152,8 @@ def moe_rope_append(cfg, q, k, v, positions, table, slot_map, k_cache, v_cache, 
                                      _array(positions, torch.int32, T, "positions"), _table(cfg, table), rot_scale,
                                      _array(slot_map, torch.int64, T, "slot_map"), op, o_ld,
                                      _cache(cfg, k_cache, "k_cache"), _cache(cfg, v_cache, "v_cache"),
-                                     _array(ws, torch.uint8, None, "ws"), ws.numel(), _s(stream)), "moe_rope_append")
+                                     _array(ws, torch.uint8, None, "ws"), ws.numel(), _stream(stream, ws)),
+            "moe_rope_append")
 
 
 def moe_tree_attention(cfg, q, q_start, kv_len, block_table, k_cache, v_cache, out, ws, tree_mask=None, lse=None,
@@ -158,7 +168,7 @@ def moe_tree_attention(cfg, q, q_start, kv_len, block_table, k_cache, v_cache, o
         _array(block_table, i32, R * cfg.max_pages, "block_table"), _cache(cfg, k_cache, "k_cache"),
         _cache(cfg, v_cache, "v_cache"), _array(tree_mask, i32, T * words, "tree_mask"), words, op, o_ld,
         _array(lse, torch.float32, T * cfg.n_heads, "lse"), _array(ws, torch.uint8, None, "ws"), ws.numel(),
-        _s(stream)), "moe_tree_attention")
+        _stream(stream, ws)), "moe_tree_attention")
 
 
 @dataclass

@@ -221,17 +221,30 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnArgs a, i
   for (int i = tid; i < nh * D; i += kThreads) {
     const int h = i / D, d = i - h * D;
     const int64_t first = (int64_t)unit * splits;
-    float top = -INFINITY;
-    for (int sp = 0; sp < splits; ++sp) {
-      const float x = __ldcg(&a.part_ml[(first + sp) * kHeads + h].x);
-      top = (x > top || x != x) ? x : top;
-    }
-    float sum = 0.f, acc = 0.f;
-    for (int sp = 0; sp < splits; ++sp) {
-      const float2 ml = __ldcg(&a.part_ml[(first + sp) * kHeads + h]);
-      const float f = factor(ml.x, top);
-      sum = fmaf(ml.y, f, sum);
-      acc = fmaf(__ldcg(&a.part[((first + sp) * kHeads + h) * kAttnPartDim + d]), f, acc);
+    float top = -INFINITY, sum = 0.f, acc = 0.f;
+    for (int s0 = 0; s0 < splits; s0 += 8) {                 // eight splits' loads in flight
+      float2 ml[8];
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const bool in = s0 + k < splits;
+        const int64_t at = (first + s0 + k) * kHeads + h;
+        ml[k] = in ? __ldcg(&a.part_ml[at]) : make_float2(-INFINITY, 0.f);
+        v[k] = in ? __ldcg(&a.part[at * kAttnPartDim + d]) : 0.f;
+      }
+      float m_new = top;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) m_new = (ml[k].x > m_new || ml[k].x != ml[k].x) ? ml[k].x : m_new;
+      const float g = factor(top, m_new);
+      top = m_new;
+      sum *= g;
+      acc *= g;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float f = factor(ml[k].x, top);
+        sum = fmaf(ml[k].y, f, sum);
+        acc = fmaf(v[k], f, acc);
+      }
     }
     T* out = reinterpret_cast<T*>(a.out) + (int64_t)t * a.out_ld + (int64_t)(h0 + h) * D + d;
     store1<T>(out, top == -INFINITY ? 0.f : acc / sum);
@@ -240,8 +253,9 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnArgs a, i
   if (tid == 0) a.hdr->counters[unit] = 0;
 }
 
-// the most splits whose counters and partials the workspace holds, of at most
-// 32, while the grid is under two blocks an SM
+// Splits: of at least 128 keys each if the tables' rows are full (a tile for each
+// of the four warps), at most 32, while the grid is under two blocks an SM and the
+// workspace holds their counters and partials.
 template <typename T>
 cudaError_t launch_t(const AttnArgs& a, cudaStream_t s) {
   const int groups = (a.G + kHeads - 1) / kHeads;
@@ -249,7 +263,8 @@ cudaError_t launch_t(const AttnArgs& a, cudaStream_t s) {
   int64_t splits = 1;
   if (units <= kAttnCounters / 4) {
     const int64_t room = (int64_t)kAttnPartSlots * kAttnRows / kHeads / units;
-    splits = std::max<int64_t>(1, std::min<int64_t>({32, 4 * kAttnMaxCtas / units, room}));
+    const int64_t keys = (int64_t)a.max_pages << a.page_shift;
+    splits = std::max<int64_t>(1, std::min<int64_t>({32, 4 * kAttnMaxCtas / units, room, ceil_div(keys, 128)}));
   }
   launch_k(attention_kernel<T>, dim3((unsigned)(units * splits)), kThreads, 0, s, a, groups, (int)splits);
   return cudaGetLastError();

@@ -23,7 +23,7 @@ static_assert(sizeof(AttnHeader) == MOE_ATTN_HEADER_BYTES, "attention workspace 
 constexpr int kAttnMaxCtas = 160;
 constexpr int kAttnRows = 128;
 constexpr int kAttnPartDim = 128;
-constexpr int kAttnPieceCost = 5;              // a unit's fixed cost beside its key tiles, in tiles
+constexpr int kAttnPieceCost = 4;              // a unit's fixed cost beside its key tiles, in tiles
 constexpr size_t kAttnPartSlots = 2 * kAttnMaxCtas;
 constexpr size_t kAttnPartBytes = kAttnPartSlots * kAttnRows * (kAttnPartDim + 2) * 4;
 constexpr size_t kAttnJoinBytes = kAttnMaxCtas * 16;   // a record a run: what the join kernel adds
