@@ -124,6 +124,7 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnArgs a, i
       float s[kHeads] = {0.f, 0.f, 0.f, 0.f};
       if (see && !zero) {
         const T* kp = reinterpret_cast<const T*>(a.k) + at;
+#pragma unroll 8
         for (int d = 0; d < D; d += 4) {
           const float4 kv4 = load4<T>(kp + d);
 #pragma unroll
@@ -159,18 +160,28 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnArgs a, i
         m[h] = m_new;
         o[h].x *= f; o[h].y *= f; o[h].z *= f; o[h].w *= f;
       }
-      for (uint32_t left = read; left; left &= left - 1) {
-        const int src = __ffs(left) - 1;
-        const int64_t va = __shfl_sync(0xffffffffu, at, src);
-        float4 v4 = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (dl < D) v4 = load4<T>(reinterpret_cast<const T*>(a.v) + va + dl);
+      // eight keys' V rows in flight at a time
 #pragma unroll
-        for (int h = 0; h < kHeads; ++h) {
-          const float w = __shfl_sync(0xffffffffu, p[h], src);
-          o[h].x = fmaf(w, v4.x, o[h].x);
-          o[h].y = fmaf(w, v4.y, o[h].y);
-          o[h].z = fmaf(w, v4.z, o[h].z);
-          o[h].w = fmaf(w, v4.w, o[h].w);
+      for (int k0 = 0; k0 < 32; k0 += 8) {
+        if (!(read >> k0 & 0xffu)) continue;
+        float4 v4[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int64_t va = __shfl_sync(0xffffffffu, at, k0 + k);
+          v4[k] = dl < D && (read >> (k0 + k) & 1u) ? load4<T>(reinterpret_cast<const T*>(a.v) + va + dl)
+                                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+#pragma unroll
+          for (int h = 0; h < kHeads; ++h) {
+            const float w = __shfl_sync(0xffffffffu, p[h], k0 + k);
+            if (!(read >> (k0 + k) & 1u)) continue;
+            o[h].x = fmaf(w, v4[k].x, o[h].x);
+            o[h].y = fmaf(w, v4[k].y, o[h].y);
+            o[h].z = fmaf(w, v4[k].z, o[h].z);
+            o[h].w = fmaf(w, v4[k].w, o[h].w);
+          }
         }
       }
     }

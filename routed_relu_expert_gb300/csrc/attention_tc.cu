@@ -178,6 +178,31 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// two FP32 values in one instruction (each rounded as by itself), and the larger
+// of three: the softmax groups are bound by the instructions that they issue
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -199,9 +224,10 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
 __device__ __noinline__ bool wait_slow(uint32_t b, uint32_t parity, volatile int* abort_flag, int32_t* err) {
   return __all_sync(0xffffffffu, mbar_wait<false, true>(b, parity, abort_flag, err));
 }
+template <int TRIES = 32>
 __device__ __forceinline__ bool wait_warp(uint32_t b, uint32_t parity, volatile int* abort_flag, int32_t* err) {
 #pragma unroll 1
-  for (int i = 0; i < 32; ++i)
+  for (int i = 0; i < TRIES; ++i)
     if (__all_sync(0xffffffffu, mbar_test(b, parity))) return true;
   return wait_slow(b, parity, abort_flag, err);
 }
@@ -335,6 +361,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     sm.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (warp == 8 && lane < 3) {
+    const CUtensorMap* map = lane == 0 ? &maps.q : lane == 1 ? &maps.k : &maps.v;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+  }
   if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem)),
                  "r"(kTmemCols)
@@ -361,10 +391,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     int run = x - local;
     for (int w = 0; w < warp; ++w) run += sm.scan[w];
-    for (int r = r0; r < r1; ++r) {
-      prefix[r] = run;
-      const Req q = request(a, r, tb, nullptr);
-      run += (q.tiles + kAttnPieceCost) * q.blocks * a.Hkv;
+    if (per == 1) {
+      if (r0 < r1) prefix[r0] = run;
+      run += local;
+    } else {
+      for (int r = r0; r < r1; ++r) {
+        prefix[r] = run;
+        const Req q = request(a, r, tb, nullptr);
+        run += (q.tiles + kAttnPieceCost) * q.blocks * a.Hkv;
+      }
     }
     if (threadIdx.x == kThreads - 1) prefix[a.R] = run;
     if (bad && blockIdx.x == 0) set_error(err, MOE_DEVERR_CACHE);
@@ -383,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int taken = 0;
   auto next = [&](Piece& p) {
     const int e = taken % kQueue;
-    if (!wait_warp(bar(sm.piece_full[e]), (uint32_t)(taken / kQueue) & 1u, abort_flag, err)) return false;
+    if (!wait_warp<4>(bar(sm.piece_full[e]), (uint32_t)(taken / kQueue) & 1u, abort_flag, err)) return false;
     p = sm.piece[e];
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(sm.piece_empty[e]));
@@ -432,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         p.n = max(t1 - t0, 0);
       }
       const int e = made % kQueue;
-      if (!wait_warp(bar(sm.piece_empty[e]), ((uint32_t)(made / kQueue) & 1u) ^ 1u, abort_flag, err)) break;
+      if (!wait_warp<1>(bar(sm.piece_empty[e]), ((uint32_t)(made / kQueue) & 1u) ^ 1u, abort_flag, err)) break;
       if (lane == 0) {
         sm.piece[e] = p;
         mbar_arrive(bar(sm.piece_full[e]));
@@ -441,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++made;
       if (last || p.n == 0) continue;
       // Q, once the last S of the piece before is done; K and V of this piece are on their way meanwhile
-      if (!wait_warp(bar(sm.q_empty), (loads & 1) ^ 1, abort_flag, err)) break;
+      if (!wait_warp<1>(bar(sm.q_empty), (loads & 1) ^ 1, abort_flag, err)) break;
       if (elect_one()) {
         mbar_expect_tx(bar(sm.q_full), (uint32_t)(X::NH * 128 * a.G * tb));
 #pragma unroll
@@ -481,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       int id[4] = {page_of(0), page_of(1), page_of(2), -1};   // tiles j .. j + 3
       auto load = [&](const CUtensorMap* map, int j, int pid) {
-        ok = wait_warp(bar(sm.empty[slot]), phase ^ 1u, abort_flag, err);
+        ok = wait_warp<1>(bar(sm.empty[slot]), phase ^ 1u, abort_flag, err);
         if (!ok) return;
         const int boxes = __popc(__ballot_sync(0xffffffffu, pid >= 0));   // lanes 0 .. boxes - 1
         const int off = ((p.t0 + j) * kTile) & (page - 1);                // pages larger than a tile
@@ -652,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         arrive(sm.s_free[(tiles + j) & 1]);
         const int key0 = (p.t0 + j) * kTile;
-        if (key0 + kTile > p.ctx) {
+        if (__builtin_expect(key0 + kTile > p.ctx, 0)) {
 #pragma unroll
           for (int cc = 0; cc < 2; ++cc) {
             const int k0 = key0 + 64 * w + 32 * cc, j0 = k0 - p.ctx;   // first key of the word, as a node
@@ -675,8 +710,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         float t4[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-        for (int i = 4; i < 64; ++i) t4[i & 3] = fmaxf(t4[i & 3], v[i]);
-        const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+        for (int i = 4; i < 60; i += 2) t4[(i >> 1) & 3] = max3(t4[(i >> 1) & 3], v[i], v[i + 1]);
+        const float top = max3(max3(t4[0], t4[1], v[60]), max3(t4[2], t4[3], v[61]), fmaxf(v[62], v[63]));
         sm.top[pairs & 1][w][row] = top;
         return top;
       };
@@ -690,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         top = fmaxf(top, sm.top[pairs & 1][w ^ 1][row]) * c;
         ++pairs;
         const bool raise = top > mc + kRaise || (mc == -INFINITY && top > mc);
-        if (__any_sync(0xffffffffu, raise)) {
+        if (__builtin_expect(__any_sync(0xffffffffu, raise), 0)) {
           const float f = raise ? (mc == -INFINITY ? 0.f : ex2(mc - top)) : 1.f;
           if (raise) mc = top;
           l *= f;
@@ -716,16 +751,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       // 32 probabilities, from the CC'th half of the scores
       auto exps = [&](auto CC, int b, float base) {
         constexpr int cc = decltype(CC)::value;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t c2 = pair(c, c), base2 = pair(-base, -base);
+        uint64_t sum[2] = {0, 0};
         uint32_t pk[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const float x = ex2(fmaf(v[32 * cc + 2 * i], c, -base)), y = ex2(fmaf(v[32 * cc + 2 * i + 1], c, -base));
-          sum[(2 * i) & 3] += x;
-          sum[(2 * i + 1) & 3] += y;
+          float x, y;
+          unpair(fma2(pair(v[32 * cc + 2 * i], v[32 * cc + 2 * i + 1]), c2, base2), x, y);
+          x = ex2(x);
+          y = ex2(y);
+          sum[i & 1] = add2(sum[i & 1], pair(x, y));
           pk[i] = pack_bf16(x, y);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        float s0, s1;
+        unpair(add2(sum[0], sum[1]), s0, s1);
+        l += s0 + s1;
         st16(tmem + lane_addr + X::p_col(b) + 32u * w + 16u * cc, pk);
       };
       // V rows of tile j past the last key, and nodes' rows that are not finite, become zeros (by halves of the
@@ -788,7 +828,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           exps(std::integral_constant<int, 1>(), b, base);
           if (more) ld32_async<32>(scores_at(j + 1) + 32, v);
         }
-        const bool any_odd = (p.t0 + j + 1) * kTile > p.ctx && clean(j);
+        bool any_odd = false;
+        if (__builtin_expect((p.t0 + j + 1) * kTile > p.ctx, 0)) any_odd = clean(j);
         if (!ok) break;
         if (live_warp) {
           st_wait();
@@ -799,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (more) arrive(sm.s_free[b ^ 1]);
           continue;
         }
-        if (any_odd) {
+        if (__builtin_expect(any_odd, 0)) {
           // p v of the nodes whose V is not finite
           if (!wait(sm.pv_done[b], (uint32_t)((tiles + j) >> 1) & 1u)) break;
           tc_fence_after();
