@@ -81,6 +81,10 @@ struct Piece {
 };
 constexpr int kStarts = 1, kEnds = 2, kLast = 4;
 
+struct Req {
+  int q0, n, kv, ctx, tiles, blocks;
+};
+
 // fixed shared-memory words after the tiles
 struct Small {
   uint64_t full[10], empty[10];
@@ -90,6 +94,8 @@ struct Small {
   float sum[2][2][kAttnRows];                  // [piece parity][group][row]
   uint32_t odd[2][2][4];                       // [tile parity][half of the head]: nodes whose V is not finite
   Piece piece[kQueue];
+  Req first;                                   // request that the run begins in
+  int first_r;
   uint32_t tmem;
   int abort;
   int scan[16];
@@ -296,9 +302,6 @@ __device__ __noinline__ void add_odd(const AttnArgs& a, int r, int h, int key0, 
 // ---------------------------------------------------------------------------
 // requests and units
 // ---------------------------------------------------------------------------
-struct Req {
-  int q0, n, kv, ctx, tiles, blocks;
-};
 __device__ __forceinline__ Req request(const AttnArgs& a, int r, int tb, int* bad) {
   Req q;
   q.q0 = min(max(a.q_start[r], 0), a.T);
@@ -372,14 +375,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   pdl_wait();
-  // cost before each request: its units' tiles and fixed costs
+  // cost before each request: its units' tiles and fixed costs; this CTA's run of the total, and the request that
+  // the run begins in (with what its thread has read of it)
+  int total, runs, share, extra;
+  // run c begins after c shares, the first `extra` of them one longer
+  auto run_start = [&](int c) { return c * share + min(c, extra); };
   {
     int bad = 0;
     const int per = (a.R + kThreads - 1) / kThreads, r0 = min((int)threadIdx.x * per, a.R), r1 = min(r0 + per, a.R);
+    auto cost = [&](const Req& q) { return (q.tiles + kAttnPieceCost) * q.blocks * a.Hkv; };
+    Req q;
     int local = 0;
     for (int r = r0; r < r1; ++r) {
-      const Req q = request(a, r, tb, &bad);
-      local += (q.tiles + kAttnPieceCost) * q.blocks * a.Hkv;
+      q = request(a, r, tb, &bad);
+      local += cost(q);
     }
     int x = local;
 #pragma unroll
@@ -390,27 +399,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 31) sm.scan[warp] = x;
     __syncthreads();
     int run = x - local;
-    for (int w = 0; w < warp; ++w) run += sm.scan[w];
-    if (per == 1) {
-      if (r0 < r1) prefix[r0] = run;
-      run += local;
-    } else {
-      for (int r = r0; r < r1; ++r) {
-        prefix[r] = run;
-        const Req q = request(a, r, tb, nullptr);
-        run += (q.tiles + kAttnPieceCost) * q.blocks * a.Hkv;
-      }
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      const int s = sm.scan[w];
+      if (w < warp) run += s;
+      total += s;
     }
-    if (threadIdx.x == kThreads - 1) prefix[a.R] = run;
+    runs = min((int)gridDim.x, max(total, 1));
+    share = total / runs;
+    extra = total - share * runs;
+    const int begin = run_start(blockIdx.x);
+    for (int r = r0; r < r1; ++r) {
+      if (per > 1) q = request(a, r, tb, nullptr);
+      prefix[r] = run;
+      const int next = run + cost(q);
+      if (run <= begin && begin < next) {
+        sm.first_r = r;
+        sm.first = q;
+      }
+      run = next;
+    }
+    if (threadIdx.x == 0) prefix[a.R] = total;
     if (bad && blockIdx.x == 0) set_error(err, MOE_DEVERR_CACHE);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
-  const int total = prefix[a.R];
-  const int runs = min((int)gridDim.x, max(total, 1));
-  auto run_start = [&](int c) { return (int)((int64_t)c * total / runs); };
   const bool idle = (int)blockIdx.x >= runs;
   const int begin = idle ? 0 : run_start(blockIdx.x), end = idle ? 0 : run_start(blockIdx.x + 1);
 
@@ -429,16 +445,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 11) {
     // ---------------- the run's pieces, worked out ahead of the other warps, and their Q ----------------
     // a unit's cost is kAttnPieceCost, then a tile each
-    auto owner = [&](int at) { return (int)((((int64_t)at + 1) * runs - 1) / total); };
-    int r = 0;
-    for (int hi = a.R; hi - r > 1;) {                      // prefix[r] <= begin < prefix[r + 1]
-      const int mid = (r + hi) >> 1;
-      if (prefix[mid] <= begin) r = mid; else hi = mid;
-    }
+    auto owner = [&](int at) {                             // the run that holds position `at`
+      const int longer = (share + 1) * extra;              // positions in the longer runs
+      return at < longer ? at / (share + 1) : extra + (at - longer) / share;
+    };
     int pos = begin, made = 0, loads = 0;
     bool last = false;
-    Req q;
-    int have = -1;
+    Req q = sm.first;                                      // (not read where the run is empty)
+    int r = sm.first_r, have = r;
     while (!last) {
       Piece p;
       last = pos >= end;
