@@ -11,11 +11,13 @@
 // [-1/2, 1/2), go to FP32 with a relative error of 2^-24.  Rows are turned in
 // FP32 and rounded once, on the store.
 //
-// Bound: every row is read once and written once.  A thread owns one piece of one
-// head (16 bytes, or the two 16-byte pieces that rotate into each other) and walks
-// a block's tokens with it: where the piece lies is worked out once, and the loads
-// of kRopeAhead tokens are in flight before the first is turned.  The angles of a
-// block's tokens are computed once for all of its pieces, into shared memory.
+// Bound: every row is read once and written once.  A thread owns one 16-byte piece
+// of one head and walks a block's tokens with it: where the piece lies is worked
+// out once, and the loads of kRopeAhead tokens are in flight before the first is
+// turned.  In the half layout the piece that a piece rotates with belongs to
+// another lane of the warp (a warp holds whole heads) and comes by shuffle, so
+// that every load and store is of whole lines.  The angles of a block's tokens are
+// computed once for all of its pieces, into shared memory.
 #include "attn.h"
 
 #include <algorithm>
@@ -57,62 +59,94 @@ template <> struct Vec16<bf16> {
   }
 };
 
+// threads of a head whose rotating part does not end on a piece: pairs, single elements, whole pieces
+__host__ __device__ __forceinline__ int pieces_of(int D, int rot, int n) {
+  const int edge = (rot + n - 1) / n * n;
+  return rot / 2 + (edge - rot) + (D - edge) / n;
+}
+
 __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(bf16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ void from_f(float v, float* p) { *p = v; }
 __device__ __forceinline__ void from_f(float v, bf16* p) { *p = __float2bfloat16_rn(v); }
 
-// VECTOR: pairs by 16-byte pieces (the pieces of a and of b are whole); else a
-// pair of elements at a time.  tb: tokens a block; blockIdx.y: kRopeThreads
-// pieces.
+// VECTOR: 16-byte pieces (the pieces that rotate are whole); else a thread has a
+// pair of elements, or one of the elements between the last pair and the next
+// 16-byte boundary, or a whole piece behind that.  tb: tokens a block; blockIdx.y: kRopeThreads pieces.
 template <typename T, bool INTER, bool VECTOR>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, int tb) {
   constexpr int N = Vec16<T>::N;
+  constexpr bool SHUFFLE = VECTOR && !INTER;
   pdl_wait();
   __shared__ __align__(16) float2 cs[kRopeMaxTokens * kRopeMaxPairs];
   __shared__ int64_t slot_at[kRopeMaxTokens];   // cache offset of the token's head 0, -1: not cached
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31;
   const int t0 = blockIdx.x * tb, nt = min(tb, a.T - t0);
   const int half = a.rot / 2;
-  // this thread's piece: part, head, and which of the head's pieces (the ones that rotate, then the others)
-  const int n_turn = VECTOR ? (INTER ? a.rot / N : a.rot / (2 * N)) : half;
-  int at = blockIdx.y * kRopeThreads + tid, part = 0, turns = 0, pieces = 0;
-  for (; part < a.n_parts; ++part) {
-    turns = a.part[part].rotate ? n_turn : 0;
-    const int rot = a.part[part].rotate ? a.rot : 0;
-    pieces = turns + (VECTOR ? (a.D - rot) / N : a.D - rot);
-    const int all = pieces * a.part[part].heads;
-    if (at < all) break;
-    at -= all;
+  // this thread's piece k of head h of a part (first the pieces that rotate)
+  int part = 0, h = 0, k = 0;
+  if (SHUFFLE) {
+    const int per = a.D / N, heads = 32 / per;             // a warp: whole heads
+    const int i = lane / per;
+    k = lane - i * per;
+    h = (blockIdx.y * (kRopeThreads / 32) + (tid >> 5)) * heads + i;
+    if (i >= heads) h = INT32_MAX;
+    for (; part < a.n_parts && h >= a.part[part].heads; ++part) h -= a.part[part].heads;
+  } else {
+    int at = blockIdx.y * kRopeThreads + tid;
+    for (; part < a.n_parts; ++part) {
+      const int rot = a.part[part].rotate ? a.rot : 0;
+      const int per = VECTOR ? a.D / N : pieces_of(a.D, rot, N), all = per * a.part[part].heads;
+      if (at < all) {
+        h = at / per;
+        k = at - h * per;
+        break;
+      }
+      at -= all;
+    }
   }
   const bool have = part < a.n_parts;
-  const int h = have ? at / pieces : 0, k = have ? at - h * pieces : 0;
   const RopeRows r = a.part[have ? part : 0];
-  const bool turn = k < turns;
-  // first and, where a piece rotates into another, second element
-  const int rest = (r.rotate ? a.rot : 0) + (VECTOR ? (k - turns) * N : k - turns);
-  const int e0 = !turn ? rest : VECTOR ? k * N : INTER ? 2 * k : k;
-  const int e1 = !turn ? e0 : VECTOR ? (INTER ? e0 : half + k * N) : INTER ? 2 * k + 1 : k + half;
-  const bool two = e1 != e0;
-  const T* src = reinterpret_cast<const T*>(r.src) + (int64_t)t0 * r.src_ld + (int64_t)h * a.D;
-  T* dst = reinterpret_cast<T*>(r.dst) + (r.to_cache ? (int64_t)h * a.head_stride
-                                                     : (int64_t)t0 * r.dst_ld + (int64_t)h * a.D);
+  const int rot = r.rotate ? a.rot : 0;
+  const bool turn = VECTOR ? k * N < rot : k < rot / 2;
+  const int edge = (rot + N - 1) / N * N;                  // first whole piece that does not rotate
+  const bool whole = VECTOR || k >= edge - rot / 2;
+  // the piece's first element; without VECTOR a pair's two
+  const int e0 = VECTOR  ? k * N
+                 : turn  ? (INTER ? 2 * k : k)
+                 : whole ? edge + (k - (edge - rot / 2)) * N
+                         : rot / 2 + k;
+  const int e1 = VECTOR || !turn ? e0 : INTER ? 2 * k + 1 : k + half;
+  // SHUFFLE: the lane of the other piece, which piece of the angles, and the sign of the sine
+  const int n_half = half / N;
+  const bool first = k < n_half;
+  const int other = lane + (first ? n_half : -n_half), piece = first ? k : k - n_half;
+  const float sign = first ? -1.f : 1.f;
+  const T* src = reinterpret_cast<const T*>(r.src) + (int64_t)t0 * r.src_ld + (int64_t)(have ? h : 0) * a.D;
+  T* dst = reinterpret_cast<T*>(r.dst) + (r.to_cache ? (int64_t)(have ? h : 0) * a.head_stride
+                                                     : (int64_t)t0 * r.dst_ld + (int64_t)(have ? h : 0) * a.D);
 
-  uint4 x[kRopeAhead], y[kRopeAhead];
+  uint4 x[kRopeAhead];
   auto fetch = [&](int t, int i) {
     if (!have || t >= nt) return;
     const T* s = src + t * r.src_ld;
-    if (VECTOR) {
+    if (whole) {
       x[i] = __ldcs(reinterpret_cast<const uint4*>(s + e0));
-      if (!INTER && two) y[i] = __ldcs(reinterpret_cast<const uint4*>(s + e1));
     } else {
       x[i].x = __float_as_uint(to_f(s[e0]));
-      if (two) y[i].x = __float_as_uint(to_f(s[e1]));
+      x[i].y = __float_as_uint(to_f(s[e1]));
     }
   };
 #pragma unroll
-  for (int i = 0; i < kRopeAhead; ++i) fetch(i, i);
+  for (int i = 0; i < kRopeAhead; ++i) {
+    x[i] = make_uint4(0, 0, 0, 0);
+    fetch(i, i);
+  }
 
+  // a token's angles lie so that the lanes of a warp, a piece each, read neighbours: [pair of the piece][piece]
+  constexpr int M = !VECTOR ? 1 : INTER ? N / 2 : N;         // pairs (or halves of pairs) a piece
+  const int n_piece = half / M;
+  auto place = [&](int p) { return p % M * n_piece + p / M; };
   for (int i = tid; i < nt * half; i += kRopeThreads) {
     const int t = i / half, p = i - t * half;
     const uint64_t turned = (uint64_t)(int64_t)a.positions[t0 + t] * a.table[p];
@@ -120,7 +154,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, in
     const int32_t frac = (int32_t)(uint32_t)((turned + 0x80000000ull) >> 32);
     float s, c;
     sincospif((float)frac * 4.656612873077393e-10f, &s, &c);   // 2^-31
-    cs[i] = make_float2(c * a.scale, (a.inverse ? -s : s) * a.scale);
+    cs[t * half + place(p)] = make_float2(c * a.scale, (a.inverse ? -s : s) * a.scale);
   }
   if (a.slot_map && tid < nt) {
     const int64_t slot = a.slot_map[t0 + tid];
@@ -132,15 +166,22 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, in
     slot_at[tid] = off;
   }
   __syncthreads();
-  if (!have) return;
 
   for (int tt = 0; tt < nt; tt += kRopeAhead) {
 #pragma unroll
     for (int i = 0; i < kRopeAhead; ++i) {
       const int t = tt + i;
       if (t >= nt) break;
-      const uint4 u = x[i], v = y[i];
+      const uint4 u = x[i];
       fetch(t + kRopeAhead, i);
+      uint4 v;
+      if (SHUFFLE) {
+        v.x = __shfl_sync(0xffffffffu, u.x, other & 31);
+        v.y = __shfl_sync(0xffffffffu, u.y, other & 31);
+        v.z = __shfl_sync(0xffffffffu, u.z, other & 31);
+        v.w = __shfl_sync(0xffffffffu, u.w, other & 31);
+      }
+      if (!have) continue;
       T* d = dst;
       if (r.to_cache) {
         if (slot_at[t] < 0) continue;
@@ -148,34 +189,32 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, in
       } else {
         d += t * r.dst_ld;
       }
-      if (VECTOR && !turn) {
+      if (whole && !turn) {
         *reinterpret_cast<uint4*>(d + e0) = u;
       } else if (VECTOR && INTER) {
         float f[N];
         Vec16<T>::load(&u, f);
 #pragma unroll
         for (int p = 0; p < N / 2; ++p) {
-          const float2 w = cs[t * half + k * (N / 2) + p];
+          const float2 w = cs[t * half + p * n_piece + k];
           const float fa = f[2 * p], fb = f[2 * p + 1];
           f[2 * p] = fa * w.x - fb * w.y;
           f[2 * p + 1] = fa * w.y + fb * w.x;
         }
         Vec16<T>::store(d + e0, f);
       } else if (VECTOR) {
+        // a cos - b sin, or b cos + a sin
         float f[N], g[N];
         Vec16<T>::load(&u, f);
         Vec16<T>::load(&v, g);
 #pragma unroll
         for (int p = 0; p < N; ++p) {
-          const float2 w = cs[t * half + k * N + p];
-          const float fa = f[p], fb = g[p];
-          f[p] = fa * w.x - fb * w.y;
-          g[p] = fa * w.y + fb * w.x;
+          const float2 w = cs[t * half + p * n_piece + piece];
+          f[p] = f[p] * w.x + sign * (g[p] * w.y);
         }
         Vec16<T>::store(d + e0, f);
-        Vec16<T>::store(d + e1, g);
       } else {
-        const float fa = __uint_as_float(u.x), fb = __uint_as_float(v.x);
+        const float fa = __uint_as_float(u.x), fb = __uint_as_float(u.y);
         if (turn) {
           const float2 w = cs[t * half + k];
           from_f(fa * w.x - fb * w.y, d + e0);
@@ -192,12 +231,11 @@ template <typename T>
 cudaError_t launch_t(const RopeArgs& a, int interleaved, cudaStream_t s) {
   constexpr int N = Vec16<T>::N;
   const bool vec = a.rot % (interleaved ? N : 2 * N) == 0;
-  int64_t pieces = 0;
-  for (int i = 0; i < a.n_parts; ++i) {
-    const int rot = a.part[i].rotate ? a.rot : 0;
-    pieces += (int64_t)a.part[i].heads * (vec ? (interleaved ? rot / N : rot / (2 * N)) + (a.D - rot) / N : a.D - rot / 2);
-  }
-  const int64_t chunks = ceil_div(pieces, kRopeThreads);
+  int64_t threads = 0;
+  for (int i = 0; i < a.n_parts; ++i)
+    threads += (int64_t)a.part[i].heads * (vec ? a.D / N : pieces_of(a.D, a.part[i].rotate ? a.rot : 0, N));
+  if (vec && !interleaved) threads = ceil_div(threads / (a.D / N), 32 / (a.D / N)) * 32;   // whole heads a warp
+  const int64_t chunks = ceil_div(threads, kRopeThreads);
   if (chunks > 65535) return cudaErrorInvalidValue;
   // tokens a block: what leaves about two waves of eight blocks an SM.  BF16, 16384 tokens, 48 heads of 128, half of
   // the head turned: 16 tokens 76 us, 8 78, 4 85, 2 102; loads 1, 2 and 4 tokens ahead 80, 76 and 88 us
