@@ -422,7 +422,7 @@ typedef struct moe_attn_config {
 moe_status_t moe_check_attn_config(const moe_attn_config_t* cfg);
 
 /* Bytes of the workspace of the entry points below (0 on an invalid
- * configuration).  It depends on head_dim alone, not on lengths or batch.    */
+ * configuration): one size, whatever the lengths and the batch.              */
 size_t moe_attn_workspace_bytes(const moe_attn_config_t* cfg);
 
 /* Block tables, slot maps, positions and tree masks of a step from its
@@ -443,6 +443,8 @@ size_t moe_attn_workspace_bytes(const moe_attn_config_t* cfg);
  *   slot_map   [T] int64 out: page * page_size + offset, or -1
  *   tree_mask  [T, mask_words] int32 out (with parents), bit j % 32 of word
  *              j / 32: node j is the row's node or one of its ancestors
+ * Pages come back by writing them before free_pages[*free_head] and lowering
+ * *free_head (a finished request's, or those of a draft's rejected end).
  * Rows past the last node get position 0, slot -1 and an empty mask, so that a
  * captured graph may run at a fixed T.  Out of free pages (or of the table's
  * row): MOE_DEVERR_PAGES, entries and slots -1.  Bad lengths, parents and page
@@ -474,7 +476,8 @@ moe_status_t moe_rope_table(int32_t rot_dim, double theta, int32_t scaling, doub
  * rot_dim dims becomes rot_scale * (a cos - b sin, a sin + b cos), the other dims
  * are copied.  inverse: the transposed map, which is its backward (the gradient
  * of the input from the gradient of the output).  FP32, rounded once.
- *   x, out [T, heads, D] with row strides; out may be x;  positions [T] int32 >= 0
+ *   x, out [T, heads, D] with row strides; out may be x (same
+ *   stride), and overlap it in no other way;  positions [T] int32 >= 0
  *   table  [rot_dim / 2] of moe_rope_table, on the device (NULL if rot_dim is 0) */
 moe_status_t moe_rope(const moe_attn_config_t* cfg, int32_t T, int32_t heads, const void* x, int64_t x_ld,
                       const int32_t* positions, const uint64_t* table, float rot_scale, int32_t inverse, void* out,

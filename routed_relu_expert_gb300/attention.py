@@ -225,3 +225,22 @@ class PagedKVCache:
         moe_tree_attention(self.cfg, q, step.q_start, step.kv_len, self.block_table, self.k_cache, self.v_cache, out,
                            self.ws, tree_mask=step.tree_mask, lse=lse, stream=stream)
         return out
+
+    def release(self, kv_len: torch.Tensor, ctx_len: torch.Tensor) -> None:
+        """Gives the pages back that a request holds for its first kv_len tokens but not
+        for its first ctx_len (a rejected part of a draft; 0: a finished request).  They
+        go before the list's head, which the next plan takes pages from.  kv_len, ctx_len
+        [R]; torch operations on the current stream, nothing on the host."""
+        shift = self.cfg.page_size.bit_length() - 1
+        mask = self.cfg.page_size - 1
+        held = lambda n: ((n.long() + mask) >> shift)[:, None]
+        col = torch.arange(self.block_table.shape[1], device=self.block_table.device)
+        back = ((col >= held(ctx_len)) & (col < held(kv_len)) & (self.block_table >= 0)).view(-1)
+        # the returned pages first, in table order
+        pages = self.block_table.view(-1)[torch.argsort((~back).to(torch.uint8), stable=True)]
+        head = self.free_head - back.sum(dtype=torch.int32)
+        at = torch.arange(self.free_pages.numel(), device=head.device) - head
+        inside = (at >= 0) & (at < self.free_head - head)
+        self.free_pages.copy_(torch.where(inside, pages[at.clamp(0, pages.numel() - 1)], self.free_pages))
+        self.block_table.masked_fill_(back.view(self.block_table.shape), -1)
+        self.free_head.copy_(head)

@@ -26,23 +26,7 @@ constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kHeads = 4;                      // query heads a block
 
-template <typename T>
-__device__ __forceinline__ float4 load4(const T* p);
-template <>
-__device__ __forceinline__ float4 load4<float>(const float* p) {
-  return *reinterpret_cast<const float4*>(p);
-}
-template <>
-__device__ __forceinline__ float4 load4<bf16>(const bf16* p) {
-  const uint2 q = *reinterpret_cast<const uint2*>(p);
-  return make_float4(bf16_lo(q.x), bf16_hi(q.x), bf16_lo(q.y), bf16_hi(q.y));
-}
-template <typename T>
-__device__ __forceinline__ void store1(T* p, float v);
-template <>
-__device__ __forceinline__ void store1<float>(float* p, float v) { *p = v; }
-template <>
-__device__ __forceinline__ void store1<bf16>(bf16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
 // request of row t: the last r with q_start[r] <= t (rows past q_start[R]: R)
 __device__ __forceinline__ int request_of(const int32_t* q_start, int R, int t) {
@@ -55,8 +39,7 @@ __device__ __forceinline__ int request_of(const int32_t* q_start, int R, int t) 
   return lo;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) attention_kernel(const AttnArgs a, int groups, int splits) {
+__global__ void __launch_bounds__(kThreads) attention_f32_kernel(const AttnArgs a, int groups, int splits) {
   pdl_wait();
   __shared__ __align__(16) float s_q[kHeads][kAttnPartDim];
   __shared__ __align__(16) float s_o[kWarps][kHeads][kAttnPartDim];
@@ -74,8 +57,7 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnArgs a, i
     const int h = i / D, d = i - h * D;
     float v = 0.f;
     if (h < nh) {
-      const T* q = reinterpret_cast<const T*>(a.q) + (int64_t)t * a.q_ld + (int64_t)(h0 + h) * D + d;
-      v = sizeof(T) == 4 ? *reinterpret_cast<const float*>(q) : __bfloat162float(*reinterpret_cast<const bf16*>(q));
+      v = reinterpret_cast<const float*>(a.q)[(int64_t)t * a.q_ld + (int64_t)(h0 + h) * D + d];
     }
     s_q[h][d] = v;
   }
@@ -123,10 +105,10 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnArgs a, i
       }
       float s[kHeads] = {0.f, 0.f, 0.f, 0.f};
       if (see && !zero) {
-        const T* kp = reinterpret_cast<const T*>(a.k) + at;
+        const float* kp = reinterpret_cast<const float*>(a.k) + at;
 #pragma unroll 8
         for (int d = 0; d < D; d += 4) {
-          const float4 kv4 = load4<T>(kp + d);
+          const float4 kv4 = load4(kp + d);
 #pragma unroll
           for (int h = 0; h < kHeads; ++h) {
             const float4 q4 = *reinterpret_cast<const float4*>(&s_q[h][d]);
@@ -168,7 +150,7 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnArgs a, i
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const int64_t va = __shfl_sync(0xffffffffu, at, k0 + k);
-          v4[k] = dl < D && (read >> (k0 + k) & 1u) ? load4<T>(reinterpret_cast<const T*>(a.v) + va + dl)
+          v4[k] = dl < D && (read >> (k0 + k) & 1u) ? load4(reinterpret_cast<const float*>(a.v) + va + dl)
                                                     : make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll
@@ -213,8 +195,8 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnArgs a, i
       acc = fmaf(s_o[w][h][d], f, acc);
     }
     if (splits == 1) {
-      T* out = reinterpret_cast<T*>(a.out) + (int64_t)t * a.out_ld + (int64_t)(h0 + h) * D + d;
-      store1<T>(out, top == -INFINITY ? 0.f : acc / sum);
+      reinterpret_cast<float*>(a.out)[(int64_t)t * a.out_ld + (int64_t)(h0 + h) * D + d] =
+          top == -INFINITY ? 0.f : acc / sum;
       if (a.lse && d == 0) a.lse[(int64_t)t * a.H + h0 + h] = top == -INFINITY ? -INFINITY : top + logf(sum);
     } else {
       a.part[(slot * kHeads + h) * kAttnPartDim + d] = acc;
@@ -257,18 +239,20 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttnArgs a, i
         acc = fmaf(v[k], f, acc);
       }
     }
-    T* out = reinterpret_cast<T*>(a.out) + (int64_t)t * a.out_ld + (int64_t)(h0 + h) * D + d;
-    store1<T>(out, top == -INFINITY ? 0.f : acc / sum);
+    reinterpret_cast<float*>(a.out)[(int64_t)t * a.out_ld + (int64_t)(h0 + h) * D + d] =
+        top == -INFINITY ? 0.f : acc / sum;
     if (a.lse && d == 0) a.lse[(int64_t)t * a.H + h0 + h] = top == -INFINITY ? -INFINITY : top + logf(sum);
   }
   if (tid == 0) a.hdr->counters[unit] = 0;
 }
 
+}  // namespace
+
 // Splits: of at least 128 keys each if the tables' rows are full (a tile for each
 // of the four warps), at most 32, while the grid is under two blocks an SM and the
 // workspace holds their counters and partials.
-template <typename T>
-cudaError_t launch_t(const AttnArgs& a, cudaStream_t s) {
+cudaError_t launch_attention_f32(const AttnArgs& a, cudaStream_t s) {
+  if (a.T <= 0) return cudaSuccess;
   const int groups = (a.G + kHeads - 1) / kHeads;
   const int64_t units = (int64_t)a.T * a.Hkv * groups;
   int64_t splits = 1;
@@ -277,14 +261,8 @@ cudaError_t launch_t(const AttnArgs& a, cudaStream_t s) {
     const int64_t keys = (int64_t)a.max_pages << a.page_shift;
     splits = std::max<int64_t>(1, std::min<int64_t>({32, 4 * kAttnMaxCtas / units, room, ceil_div(keys, 128)}));
   }
-  launch_k(attention_kernel<T>, dim3((unsigned)(units * splits)), kThreads, 0, s, a, groups, (int)splits);
+  launch_k(attention_f32_kernel, dim3((unsigned)(units * splits)), kThreads, 0, s, a, groups, (int)splits);
   return cudaGetLastError();
-}
-
-}  // namespace
-
-cudaError_t launch_attention_f32(const AttnArgs& a, cudaStream_t s) {
-  return a.T > 0 ? launch_t<float>(a, s) : cudaSuccess;
 }
 
 }  // namespace moe

@@ -679,3 +679,65 @@ def test_steps_of_a_decoded_sequence_in_one_graph():
     # both are FP32 evaluations of the same sums in another order
     # (weights sum to one, |v| < 6: scores within 200 U of each other, sums within 200 U)
     assert float((got - want).abs().max()) <= 2 * 6 * 400 * U
+
+
+def test_released_pages_are_taken_again():
+    """Pages of a draft's rejected end go back to the free list and come out of it again,
+    each to one request at a time."""
+    M = _m()
+    R, page = 4, 8
+    cfg = M.make_attn_config(2, 1, 16, page_size=page, n_pages=R * 6, max_pages=6, dtype=M.MOE_DT_F32)
+    c = M.PagedKVCache(cfg, R)
+    rng = np.random.default_rng(3)
+    ctx = np.array([0, 3, 8, 15])
+    c.plan(_i32([0] * R), _i32(ctx.tolist()), int(ctx.sum()))
+    for _ in range(12):
+        new = rng.integers(0, 17, R)
+        new = np.minimum(new, 6 * page - ctx)
+        step = c.plan(_i32(ctx.tolist()), _i32(new.tolist()), int(new.sum()) + 2)
+        after = ctx + rng.integers(0, new + 1)
+        c.release(step.kv_len, _i32(after.tolist()))
+        table = c.block_table.cpu().numpy()
+        held = [table[r, :-(-int(after[r]) // page)] for r in range(R)]
+        used = np.concatenate(held)
+        free = c.free_pages.cpu().numpy()[int(c.free_head):]
+        assert sorted(np.concatenate([used, free]).tolist()) == list(range(R * 6))
+        assert all((table[r, len(held[r]):] == -1).all() for r in range(R))
+        ctx = after
+    assert _err(c.ws) == 0
+
+
+def test_nodes_past_the_rows_are_dropped():
+    M = _m()
+    cfg = M.make_attn_config(4, 2, 64, page_size=16, n_pages=8, max_pages=2)
+    ws = M.new_attn_workspace(cfg)
+    q_start, kv, pos = _i32([9] * 4), _i32([9] * 3), _i32([9] * 5)
+    slot = torch.zeros(5, dtype=torch.int64, device="cuda")
+    M.moe_paged_plan(cfg, _i32([3, 2, 1]), _i32([4, 3, 2]), _i32([[6, -1], [7, -1], [5, -1]]), _i32([0, 1]), _i32([0]),
+                     q_start, kv, pos, slot, ws, free_head_out=_i32([0]))
+    assert _err(ws) == M.MOE_DEVERR_CACHE
+    assert q_start.tolist() == [0, 4, 5, 5] and kv.tolist() == [7, 3, 1]
+    assert pos.tolist() == [3, 4, 5, 6, 2] and slot.tolist() == [99, 100, 101, 102, 114]
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+def test_attention_without_requests(dt):
+    M = _m()
+    s = Step([20], [3], 8, 2, 64, 16, dt, T=5)
+    out, lse = torch.full((5, 8, 64), 7.0, dtype=dt, device="cuda"), torch.full((5, 8), 7.0, device="cuda")
+    M.moe_tree_attention(s.cfg, s.q, _i32([0]), _i32([]), s.table_d[:0], s.k, s.v, out, s.ws, lse=lse)
+    assert bool((out == 0).all()) and bool((lse == -math.inf).all()) and _err(s.ws) == 0
+
+
+def test_verify_step_example():
+    """plan, append, attend and the MoE block over drafted trees, the accepted path kept:
+    its rows are those of decoding the same tokens one at a time.  The two differ by BF16
+    roundings of attention and projections (2^-8 of values of a few units, through an
+    expert choice that a rounding may flip at a tie: one percent of the output's size)."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "verify_step.py")
+    spec = importlib.util.spec_from_file_location("verify_step", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    assert ex.main() <= 0.25
