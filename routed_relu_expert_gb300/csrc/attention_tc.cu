@@ -276,10 +276,11 @@ __device__ __forceinline__ void transpose4(uint4 (&x)[4], int lane) {
 // ---------------------------------------------------------------------------
 // O += p V, columns c0 .. c0 + 63 of the head, for the rows that see them (p, read
 // back from tensor memory, is 0 where a row does not)
-__device__ __noinline__ void add_odd(const AttnArgs& a, int r, int h, int key0, const uint32_t* odd, int c0,
-                                     uint32_t p_addr, uint32_t o_addr) {
+__device__ __noinline__ void add_odd(const AttnArgs& a, int r, int h, int key0, uint4 odd, int c0, uint32_t p_addr,
+                                     uint32_t o_addr) {
   for (int i = 0; i < kTile; ++i) {
-    if (!(odd[i >> 5] >> (i & 31) & 1u)) continue;
+    const uint32_t word = i < 64 ? (i < 32 ? odd.x : odd.y) : (i < 96 ? odd.z : odd.w);
+    if (!(word >> (i & 31) & 1u)) continue;
     const int key = key0 + i;
     const int pg = a.block_table[(int64_t)r * a.max_pages + (key >> a.page_shift)];
     if (pg < 0 || pg >= a.n_pages) continue;
@@ -783,11 +784,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         st16(tmem + lane_addr + X::p_col(b) + 32u * w + 16u * cc, pk);
       };
       // V rows of tile j past the last key, and nodes' rows that are not finite, become zeros (by halves of the
-      // head); whether there is a node of the second kind
+      // head); the nodes of the second kind (read before P is announced: two tiles on, the words are others)
       auto clean = [&](int j) {
         const int b = (tiles + j) & 1, key0 = (p.t0 + j) * kTile;
         const int item = items + v_item(j, p.n);
-        if (!wait(sm.full[item % NS], (uint32_t)(item / NS) & 1u)) return false;
+        const uint4 none = make_uint4(0, 0, 0, 0);
+        if (!wait(sm.full[item % NS], (uint32_t)(item / NS) & 1u)) return none;
         const int key = key0 + row;
         uint4* v0 = reinterpret_cast<uint4*>(ring_ptr + (item % NS) * X::SLOT + w * kHalfBytes + row * 128);
         const bool zero = key >= p.kv;
@@ -814,9 +816,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t mine = __ballot_sync(0xffffffffu, strange);
         if (lane == 0) sm.odd[b][w][qd] = mine;
         arrive(sm.group);
-        if (!wait(sm.group, groups & 1)) return false;
+        if (!wait(sm.group, groups & 1)) return none;
         ++groups;
-        return (sm.odd[b][w][0] | sm.odd[b][w][1] | sm.odd[b][w][2] | sm.odd[b][w][3]) != 0;
+        return make_uint4(sm.odd[b][w][0], sm.odd[b][w][1], sm.odd[b][w][2], sm.odd[b][w][3]);
       };
       if (p.n > 0 && ready(0) && !live_warp) arrive(sm.s_free[tiles & 1]);
       if (p.n > 0 && ok && live_warp) {
@@ -842,8 +844,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           exps(std::integral_constant<int, 1>(), b, base);
           if (more) ld32_async<32>(scores_at(j + 1) + 32, v);
         }
-        bool any_odd = false;
-        if (__builtin_expect((p.t0 + j + 1) * kTile > p.ctx, 0)) any_odd = clean(j);
+        uint4 odd = make_uint4(0, 0, 0, 0);
+        if (__builtin_expect((p.t0 + j + 1) * kTile > p.ctx, 0)) odd = clean(j);
         if (!ok) break;
         if (live_warp) {
           st_wait();
@@ -854,11 +856,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (more) arrive(sm.s_free[b ^ 1]);
           continue;
         }
-        if (__builtin_expect(any_odd, 0)) {
+        if (__builtin_expect((odd.x | odd.y | odd.z | odd.w) != 0, 0)) {
           // p v of the nodes whose V is not finite
           if (!wait(sm.pv_done[b], (uint32_t)((tiles + j) >> 1) & 1u)) break;
           tc_fence_after();
-          add_odd(a, p.r, p.h, (p.t0 + j) * kTile, sm.odd[b][w], 64 * w, tmem + lane_addr + X::p_col(b),
+          add_odd(a, p.r, p.h, (p.t0 + j) * kTile, odd, 64 * w, tmem + lane_addr + X::p_col(b),
                   tmem + lane_addr + X::O);
           tc_fence_before();
           __syncwarp();

@@ -547,6 +547,23 @@ def test_a_nodes_values_reach_only_the_rows_that_see_it(dt, bad):
 
 
 @pytest.mark.parametrize("dt", [BF, FP])
+def test_nodes_that_are_not_finite_in_tile_after_tile(dt):
+    """A chain of 400 nodes over several key tiles with NaN in V of some: a row is not
+    finite from the first such node on that it sees, and as it was before."""
+    s = Step([100], [400], 8, 2, 128, 16, dt, tree=False, seed=4)
+    clean, lse = s.run()
+    s.check(clean, lse)
+    for node in (390, 275, 150, 148):
+        tok = 100 + node
+        s.v[int(s.table[0, tok // 16]), tok % 16, :, 64:] = float("nan")
+        out, lse2 = s.run()
+        assert torch.equal(lse2, lse)
+        assert torch.equal(out[:node], clean[:node])
+        assert torch.equal(out[:, :, :64], clean[:, :, :64])
+        assert bool(torch.isnan(out[node:, :, 64:].float()).all())
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
 def test_large_scores(dt):
     """Scores in the hundreds: the running maximum moves by far more than FP32's exponent range."""
     s = Step([3000], [4], 8, 2, 128, 16, dt, q_gain=60.0, seed=8)
