@@ -954,10 +954,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Units that a run's end cut: run c's unit that began but did not end in it has
 // its partials in slot 2c + 1 (its own) and 2 (c + 1), 2 (c + 2), ... of the runs
 // after it.  A lane a row, a warp four columns (the partials are laid out for it),
-// parts in ascending order, eight in flight; the block's 32 rows meet in shared
+// parts in ascending order; the block's 32 rows meet in shared
 // memory to be written whole.
 constexpr int kJoinWarps = kAttnPartDim / 4;
-__global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const AttnArgs a) {
+constexpr int kJoinAhead = 4;                  // parts in flight (32 registers: two blocks an SM)
+__global__ void __launch_bounds__(32 * kJoinWarps, 2) attention_join_kernel(const AttnArgs a) {
   pdl_wait();
   const int4 u = a.joins[blockIdx.x];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, valid = u.z * a.G;
@@ -969,11 +970,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const A
   const float* part = a.part + (warp * kAttnRows + row) * 4;
   float top = -INFINITY, sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int p = 0; p < u.x; p += 8) {
-    float2 ml[8];
-    float4 v[8];
+  for (int p = 0; p < u.x; p += kJoinAhead) {
+    float2 ml[kJoinAhead];
+    float4 v[kJoinAhead];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < kJoinAhead; ++k) {
       const bool in = p + k < u.x;
       ml[k] = in ? a.part_ml[slot(p + k) * kAttnRows + row] : make_float2(0.f, 0.f);
       v[k] = in ? *reinterpret_cast<const float4*>(part + (int64_t)slot(p + k) * kAttnRows * kAttnPartDim)
@@ -981,14 +982,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const A
     }
     float t = top;
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
+    for (int k = 0; k < kJoinAhead; ++k)
       if (ml[k].y != 0.f) t = fmaxf(t, ml[k].x);
     const float g = sum == 0.f ? 0.f : ex2(top - t);
     top = t;
     sum *= g;
     acc = make_float4(acc.x * g, acc.y * g, acc.z * g, acc.w * g);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < kJoinAhead; ++k) {
       if (ml[k].y == 0.f) continue;            // no visible key in that part
       const float f = ex2(ml[k].x - top);
       sum = fmaf(ml[k].y, f, sum);
