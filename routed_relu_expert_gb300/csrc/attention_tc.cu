@@ -1067,7 +1067,7 @@ cudaError_t launch_dp(const AttnArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   e = launch_k(attention_tc_kernel<DP>, dim3((unsigned)sms), dim3(kThreads), smem, s, maps, a, tb);
   if (e != cudaSuccess) return e;
-  return launch_k(attention_join_kernel, dim3((unsigned)sms, (unsigned)ceil_div(tb * a.G, 32)), dim3(32 * (a.D / 4)), 0,
+  return launch_k(attention_join_kernel, dim3((unsigned)sms, (unsigned)ceil_div(std::min(tb, a.T) * a.G, 32)), dim3(32 * (a.D / 4)), 0,
                   s, a);
 }
 

@@ -239,10 +239,10 @@ cudaError_t launch_t(const RopeArgs& a, int interleaved, cudaStream_t s) {
   if (vec && !interleaved) threads = ceil_div(threads / (a.D / N), 32 / (a.D / N)) * 32;   // whole heads a warp
   const int64_t chunks = ceil_div(threads, kRopeThreads);
   if (chunks > 65535) return cudaErrorInvalidValue;
-  // tokens a block: what leaves about two waves of eight blocks an SM.  BF16, 16384 tokens, 48 heads of 128, half of
+  // tokens a block: what leaves about eight blocks an SM.  BF16, 16384 tokens, 48 heads of 128, half of
   // the head turned: 16 tokens 76 us, 8 78, 4 85, 2 102; loads 1, 2 and 4 tokens ahead 80, 76 and 88 us
-  const int64_t waves = 2 * 8 * 152;
-  const int tb = (int)std::min<int64_t>(std::max<int64_t>((int64_t)a.T * chunks / waves, 1), kRopeMaxTokens);
+  const int64_t blocks = 8 * 152;
+  const int tb = (int)std::min<int64_t>(std::max<int64_t>((int64_t)a.T * chunks / blocks, 1), kRopeMaxTokens);
   const dim3 grid((unsigned)ceil_div(a.T, tb), (unsigned)chunks);
   if (interleaved) {
     if (vec) launch_k(rope_kernel<T, true, true>, grid, kRopeThreads, 0, s, a, tb);

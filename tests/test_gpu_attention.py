@@ -441,7 +441,8 @@ class Step:
                 gl = got_l[a:a + n, h]
                 dead = np.isinf(wl)
                 assert np.all(gl[dead] == -np.inf) and np.all(got[a:a + n, h][dead] == 0)
-                assert np.all(np.abs(gl - wl)[~dead] <= (ep[:, 0] + add + 4 * U * (1 + np.abs(wl)))[~dead])
+                live = ~dead
+                assert np.all(np.abs(gl[live] - wl[live]) <= (ep[:, 0] + add)[live] + 4 * U * (1 + np.abs(wl[live])))
             a += n
 
 
@@ -485,6 +486,14 @@ def test_attention_over_a_long_cache_is_split_and_joined(dt):
 def test_attention_of_many_short_requests(dt):
     n = 200 if dt is BF else 40
     s = Step([(i * 37) % 300 for i in range(n)], [1 + i % 9 for i in range(n)], 16, 4, 128, 16, dt, seed=5)
+    s.check(*s.run())
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+def test_attention_of_more_requests_than_a_block_has_threads(dt):
+    """Every block sums all requests' lengths, several a thread from 385 requests on."""
+    n = 901
+    s = Step([(i * 7) % 150 for i in range(n)], [(i * 5) % 4 for i in range(n)], 4, 2, 64, 16, dt, seed=13)
     s.check(*s.run())
 
 
