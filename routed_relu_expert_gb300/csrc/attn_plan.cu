@@ -14,9 +14,9 @@
 //
 // A warp (or, for long requests, all eight warps of a block and several blocks)
 // takes a request's nodes, a lane a node.  The bound is the latency of the
-// dependent steps (lengths, table entry, slot; for trees of over 32 nodes the walk
-// to the root), not bytes: 3.5 us for one request, 4.4 us for 64 with trees of up
-// to 16, 9.7 us for 2048 with trees of up to 64 (1.6 MB).
+// dependent steps (lengths, table entry, slot), not bytes: 3.5 us
+// for one request, 4.5 us for 64 with trees of up to 16, 7.7 us for 2048 with trees
+// of up to 64 (1.6 MB; 9.7 us with a walk to the root for each node).
 #include "attn.h"
 
 #include <algorithm>
@@ -61,16 +61,23 @@ __device__ __forceinline__ ReqLen clamp_len(const PlanArgs& a, int ctx, int n, i
   return q;
 }
 
-__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* tmp) {
+// the block's sums of four values, in every thread
+__device__ __forceinline__ void block_sums(int64_t (&v)[4], int64_t (*tmp)[4]) {
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) tmp[threadIdx.x >> 5] = v;
-  __syncthreads();
-  int64_t s = 0;
+  for (int off = 16; off > 0; off >>= 1)
 #pragma unroll
-  for (int w = 0; w < kPlanWarps; ++w) s += tmp[w];
-  return s;
+    for (int i = 0; i < 4; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
+  if ((threadIdx.x & 31) == 0)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) tmp[threadIdx.x >> 5][i] = v[i];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    int64_t s = 0;
+#pragma unroll
+    for (int w = 0; w < kPlanWarps; ++w) s += tmp[w][i];
+    v[i] = s;
+  }
 }
 
 // parent of node i, -1 where it is not an earlier node
@@ -88,21 +95,21 @@ template <int WPR>
 __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs a) {
   constexpr int RB = kPlanWarps / WPR;         // requests a block
   pdl_wait();
-  __shared__ int64_t tmp[kPlanWarps];
+  __shared__ int64_t tmp[kPlanWarps][4];
   __shared__ int s_ctx[RB], s_n[RB];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r_base = blockIdx.x * RB;
   int bad = 0;
 
   // totals before this block's requests and over all of them
-  int64_t rows_before = 0, more_before = 0, rows_all = 0, more_all = 0;
+  int64_t sums[4] = {0, 0, 0, 0};
   for (int r = tid; r < a.R; r += kPlanThreads) {
     const ReqLen q = clamp_len(a, a.ctx_len[r], a.new_len[r], bad);
-    rows_all += q.n;
-    more_all += q.more;
+    sums[0] += q.n;
+    sums[1] += q.more;
     if (r < r_base) {
-      rows_before += q.n;
-      more_before += q.more;
+      sums[2] += q.n;
+      sums[3] += q.more;
     }
     if (r >= r_base && r < r_base + RB) {
       s_ctx[r - r_base] = q.ctx;
@@ -111,10 +118,8 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
   }
   const int head = max(*a.free_head, 0);
   if (*a.free_head < 0) bad |= MOE_DEVERR_CACHE;
-  rows_before = block_sum(rows_before, tmp);
-  more_before = block_sum(more_before, tmp);
-  rows_all = block_sum(rows_all, tmp);
-  more_all = block_sum(more_all, tmp);
+  block_sums(sums, tmp);
+  const int64_t rows_all = sums[0], more_all = sums[1], rows_before = sums[2], more_before = sums[3];
   if (rows_all > a.T) bad |= MOE_DEVERR_CACHE;
   if (more_all > (int64_t)a.n_free - head) bad |= more_all > 0 ? MOE_DEVERR_PAGES : 0;
 
@@ -153,6 +158,8 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
 
     const int32_t* par = a.parents ? a.parents + start : nullptr;
     const int step = lanes * (int)gridDim.y;
+    constexpr int max_doubled = WPR == 1 ? 2 : 1;
+    uint32_t first_set = 0;                    // of the request's first 32 nodes
     // every lane of a warp runs every round: the shuffles below need them all
     for (int i0 = lanes * (int)blockIdx.y + (warp % WPR) * 32; i0 < n; i0 += step) {
       const int i = i0 + lane;
@@ -176,22 +183,35 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
       }
       if (!par) continue;
       int depth = 0;
-      if (n <= 32 && a.mask_words == 1) {
-        // trees of up to 32 nodes: ancestor sets by pointer doubling, five
-        // rounds of two shuffles whatever the depth
-        int jump = live ? parent_of(par, i, bad) : -1;
+      if (n <= 32 * max_doubled && a.mask_words <= 2 && (a.mask_words != 1 || n <= 32)) {
+        // trees of up to 32 nodes (64 where one warp has them all): ancestor sets by pointer doubling, five rounds
+        // of shuffles a 32 whatever the depth.  Ancestors come before a node, so the first 32 need no others; a node
+        // of the second 32 joins its ancestors there with the set of the one of the first that its chain leaves to
+        const bool second = i0 > 0;
+        const int up = live ? parent_of(par, i, bad) : -1;
+        int jump = second ? (up >= 32 ? up - 32 : -1) : up;
+        int leave = second && up < 32 ? up : -1;
         uint32_t set = 1u << lane;
 #pragma unroll
         for (int round = 0; round < 5; ++round) {
           const uint32_t up_set = __shfl_sync(0xffffffffu, set, jump & 31);
           const int up_jump = __shfl_sync(0xffffffffu, jump, jump & 31);
+          const int up_leave = __shfl_sync(0xffffffffu, leave, jump & 31);
           if (jump >= 0) {
             set |= up_set;
             jump = up_jump;
+            leave = up_leave;
           }
         }
-        depth = __popc(set) - 1;
-        if (live && a.tree_mask) a.tree_mask[start + i] = (int32_t)set;
+        const uint32_t below = __shfl_sync(0xffffffffu, first_set, leave & 31);
+        const uint32_t low = second ? (leave >= 0 ? below : 0u) : set, high = second ? set : 0u;
+        if (!second) first_set = set;
+        depth = __popc(low) + __popc(high) - 1;
+        if (live && a.tree_mask) {
+          int32_t* out = a.tree_mask + (int64_t)(start + i) * a.mask_words;
+          out[0] = (int32_t)low;
+          if (a.mask_words == 2) out[1] = (int32_t)high;
+        }
       } else if (live) {
         // any size: walk to the root; ancestors descend, so the words of the
         // mask are finished from the last to the first
@@ -236,7 +256,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
       for (int w = 0; w < a.mask_words; ++w) a.tree_mask[i * a.mask_words + w] = 0;
   }
   if (bad) set_error(&a.hdr->err, bad);
-  // block_sum's barriers put every thread's read of *free_head before this
+  // block_sums' barrier puts every thread's read of *free_head before this
   if (tid == 0) {
     const int blocks = (int)(gridDim.x * gridDim.y);
     __threadfence();

@@ -133,6 +133,8 @@ def run_plan(ctx, new, page, *, kind=None, words=None, T=None, free_short=0, in_
     ([33, 2, 0], [16, 1, 32], 16, "tree"),
     ([33, 2, 0], [16, 1, 32], 16, "path"),                  # depth 31: every doubling round counts
     ([10, 4], [33, 64], 32, "tree"), ([10, 4], [64, 33], 32, "path"), ([3], [130], 16, "roots"),
+    ([1, 2, 3, 0], [64, 5, 33, 32], 16, "tree"), ([1, 2, 3, 0], [64, 5, 33, 32], 16, "path"),    # two words for all
+    ([6, 7], [64, 64], 16, "path"),                          # 64 rows each: a block's warps a request
     ([9] * 300, [i % 17 for i in range(300)], 16, "tree"),
     (list(range(2500)), [i % 3 for i in range(2500)], 16, "roots"),
 ])
@@ -148,6 +150,7 @@ def test_plan_without_requests():
 def test_plan_pads_rows_past_the_last_node():
     assert run_plan([4, 20], [3, 2], 16, kind="tree", T=40) == 0
     assert run_plan([4, 20], [3, 2], 16, T=700) == 0
+    assert run_plan([4, 20], [30, 12], 16, kind="path", T=700) == 0
 
 
 @pytest.mark.parametrize("short", [1, 3, 100])
