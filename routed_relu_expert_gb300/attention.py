@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 from dataclasses import dataclass
 from typing import Optional, Tuple
 
@@ -24,6 +25,8 @@ from .layer import _s
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 _TORCH = {N.MOE_DT_BF16: torch.bfloat16, N.MOE_DT_F32: torch.float32}
+# all fields of a moe_attn_config_t at once (reading them one by one costs as much as the launch)
+_FIELDS = struct.Struct("@8ifi3q")
 _SCALING = {None: N.MOE_ROPE_PLAIN, "linear": N.MOE_ROPE_LINEAR, "yarn": N.MOE_ROPE_YARN}
 
 
@@ -71,22 +74,20 @@ def _array(t: Optional[torch.Tensor], dtype, n: Optional[int], name: str):
     return t.data_ptr()
 
 
-def _rows(cfg, t: torch.Tensor, T: int, heads: int, name: str) -> Tuple[int, int]:
-    """(pointer, row stride) of rows [T, heads, head_dim]."""
-    D = cfg.head_dim
-    if not t.is_cuda or t.dtype is not _TORCH.get(cfg.dtype) or t.shape != (T, heads, D):
-        raise ValueError(f"{name} must be a {_TORCH.get(cfg.dtype)} CUDA tensor of shape {(T, heads, D)}")
+def _rows(t: torch.Tensor, T: int, heads: int, D: int, dt, name: str) -> Tuple[int, int]:
+    """(pointer, row stride) of rows [T, heads, D]."""
+    if not t.is_cuda or t.dtype is not dt or t.shape != (T, heads, D):
+        raise ValueError(f"{name} must be a {dt} CUDA tensor of shape {(T, heads, D)}")
     ld, step, one = t.stride()
     if (one != 1 and D > 1) or (heads > 1 and step != D):
         raise ValueError(f"the heads of a row of {name} must be contiguous")
     return t.data_ptr(), (ld if T > 1 else heads * D)
 
 
-def _cache(cfg, t: torch.Tensor, name: str) -> int:
-    shape = (cfg.n_pages, cfg.page_size, cfg.n_kv_heads, cfg.head_dim)
-    if not t.is_cuda or t.dtype is not _TORCH.get(cfg.dtype) or t.shape != shape:
-        raise ValueError(f"{name} must be a {_TORCH.get(cfg.dtype)} CUDA tensor of shape {shape}")
-    if t.stride() != (cfg.page_stride, cfg.token_stride, cfg.head_stride, 1):
+def _cache(t: torch.Tensor, shape, strides, dt, name: str) -> int:
+    if not t.is_cuda or t.dtype is not dt or t.shape != shape:
+        raise ValueError(f"{name} must be a {dt} CUDA tensor of shape {shape}")
+    if t.stride() != strides:
         raise ValueError(f"{name} does not have the configuration's strides")
     return t.data_ptr()
 
@@ -121,22 +122,24 @@ def rope_table(rot_dim: int, theta: float, *, scaling: Optional[str] = None, fac
     return host.to(device), float(scale.value)
 
 
-def _table(cfg, table):
-    if cfg.rot_dim == 0:
+def _table(rot: int, table):
+    if rot == 0:
         return None
     if table is None:
         raise ValueError("table is missing")
-    return _array(table, torch.int64, cfg.rot_dim // 2, "table")
+    return _array(table, torch.int64, rot // 2, "table")
 
 
 def moe_rope(cfg, x, positions, table, out, rot_scale: float = 1.0, inverse: bool = False, stream=None):
     """Rows x [T, heads, head_dim] turned by their positions into ``out`` (which
     may be x); ``inverse`` is the backward."""
     T, heads = x.shape[0], x.shape[1]
-    xp, x_ld = _rows(cfg, x, T, heads, "x")
-    op, o_ld = _rows(cfg, out, T, heads, "out")
+    _, _, D, _, _, _, rot, _, _, dtype, _, _, _ = _FIELDS.unpack_from(cfg)
+    dt = _TORCH.get(dtype)
+    xp, x_ld = _rows(x, T, heads, D, dt, "x")
+    op, o_ld = _rows(out, T, heads, D, dt, "out")
     N.check(N.load().moe_rope(ctypes.byref(cfg), T, heads, xp, x_ld, _array(positions, torch.int32, T, "positions"),
-                              _table(cfg, table), rot_scale, int(inverse), op, o_ld, _stream(stream, x)), "moe_rope")
+                              _table(rot, table), rot_scale, int(inverse), op, o_ld, _stream(stream, x)), "moe_rope")
 
 
 def moe_rope_append(cfg, q, k, v, positions, table, slot_map, k_cache, v_cache, q_out, ws, rot_scale: float = 1.0,
@@ -144,14 +147,18 @@ def moe_rope_append(cfg, q, k, v, positions, table, slot_map, k_cache, v_cache, 
     """q turned into q_out (which may be q); k turned and v as it is into the
     caches at slot_map."""
     T = q.shape[0]
-    qp, q_ld = _rows(cfg, q, T, cfg.n_heads, "q")
-    kp, k_ld = _rows(cfg, k, T, cfg.n_kv_heads, "k")
-    vp, v_ld = _rows(cfg, v, T, cfg.n_kv_heads, "v")
-    op, o_ld = _rows(cfg, q_out, T, cfg.n_heads, "q_out")
+    H, Hkv, D, page, pages, _, rot, _, _, dtype, sp, st, sh = _FIELDS.unpack_from(cfg)
+    dt = _TORCH.get(dtype)
+    qp, q_ld = _rows(q, T, H, D, dt, "q")
+    kp, k_ld = _rows(k, T, Hkv, D, dt, "k")
+    vp, v_ld = _rows(v, T, Hkv, D, dt, "v")
+    op, o_ld = _rows(q_out, T, H, D, dt, "q_out")
+    shape, strides = (pages, page, Hkv, D), (sp, st, sh, 1)
     N.check(N.load().moe_rope_append(ctypes.byref(cfg), T, qp, q_ld, kp, k_ld, vp, v_ld,
-                                     _array(positions, torch.int32, T, "positions"), _table(cfg, table), rot_scale,
+                                     _array(positions, torch.int32, T, "positions"), _table(rot, table), rot_scale,
                                      _array(slot_map, torch.int64, T, "slot_map"), op, o_ld,
-                                     _cache(cfg, k_cache, "k_cache"), _cache(cfg, v_cache, "v_cache"),
+                                     _cache(k_cache, shape, strides, dt, "k_cache"),
+                                     _cache(v_cache, shape, strides, dt, "v_cache"),
                                      _array(ws, torch.uint8, None, "ws"), ws.numel(), _stream(stream, ws)),
             "moe_rope_append")
 
@@ -160,14 +167,17 @@ def moe_tree_attention(cfg, q, q_start, kv_len, block_table, k_cache, v_cache, o
                        stream=None):
     """out [T, n_heads, head_dim] (and lse [T, n_heads] FP32) of the rows q over the cache."""
     T, R, i32 = q.shape[0], kv_len.shape[0], torch.int32
+    H, Hkv, D, page, pages, max_pages, _, _, _, dtype, sp, st, sh = _FIELDS.unpack_from(cfg)
+    dt = _TORCH.get(dtype)
     words = 0 if tree_mask is None else tree_mask.shape[1]
-    qp, q_ld = _rows(cfg, q, T, cfg.n_heads, "q")
-    op, o_ld = _rows(cfg, out, T, cfg.n_heads, "out")
+    qp, q_ld = _rows(q, T, H, D, dt, "q")
+    op, o_ld = _rows(out, T, H, D, dt, "out")
+    shape, strides = (pages, page, Hkv, D), (sp, st, sh, 1)
     N.check(N.load().moe_tree_attention(
         ctypes.byref(cfg), R, T, qp, q_ld, _array(q_start, i32, R + 1, "q_start"), _array(kv_len, i32, R, "kv_len"),
-        _array(block_table, i32, R * cfg.max_pages, "block_table"), _cache(cfg, k_cache, "k_cache"),
-        _cache(cfg, v_cache, "v_cache"), _array(tree_mask, i32, T * words, "tree_mask"), words, op, o_ld,
-        _array(lse, torch.float32, T * cfg.n_heads, "lse"), _array(ws, torch.uint8, None, "ws"), ws.numel(),
+        _array(block_table, i32, R * max_pages, "block_table"), _cache(k_cache, shape, strides, dt, "k_cache"),
+        _cache(v_cache, shape, strides, dt, "v_cache"), _array(tree_mask, i32, T * words, "tree_mask"), words, op, o_ld,
+        _array(lse, torch.float32, T * H, "lse"), _array(ws, torch.uint8, None, "ws"), ws.numel(),
         _stream(stream, ws)), "moe_tree_attention")
 
 

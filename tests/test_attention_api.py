@@ -34,6 +34,11 @@ def test_struct_layout(lib):
     from routed_relu_expert_gb300 import MoeAttnConfig
     assert ctypes.sizeof(MoeAttnConfig) == 10 * 4 + 3 * 8
     assert MoeAttnConfig.page_stride.offset == 40
+    # the binding reads all fields at once
+    from routed_relu_expert_gb300.attention import _FIELDS
+    c = _cfg(rope_interleaved=True, softmax_scale=0.5)
+    assert _FIELDS.size == ctypes.sizeof(c)
+    assert _FIELDS.unpack_from(c) == tuple(getattr(c, f) for f, _ in MoeAttnConfig._fields_)
 
 
 def test_config_validation(lib):
