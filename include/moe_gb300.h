@@ -509,8 +509,9 @@ moe_status_t moe_rope_append(const moe_attn_config_t* cfg, int32_t T, const void
  * V enter the rows that do not see that node.  FP32 scores and softmax; BF16:
  * the probabilities enter the second product in BF16.  Lengths outside the block
  * table's row are clamped and pages outside the cache read as zeros, both with
- * MOE_DEVERR_CACHE.  T * Hkv * (key tiles of a full block-table row) must stay
- * below 2^31 (MOE_ERR_UNSUPPORTED).                                          */
+ * MOE_DEVERR_CACHE.  (T + R) * Hkv * (ceil(max_pages * page_size / 128) + 5) and
+ * 32 * T * H must stay below 2^31 (MOE_ERR_UNSUPPORTED).  FP32 runs on the CUDA
+ * cores and is made for the sizes of FP32 layers.                             */
 moe_status_t moe_tree_attention(const moe_attn_config_t* cfg, int32_t R, int32_t T, const void* q, int64_t q_ld,
                                 const int32_t* q_start, const int32_t* kv_len, const int32_t* block_table,
                                 const void* k_cache, const void* v_cache, const int32_t* tree_mask,

@@ -14,14 +14,15 @@
 // of keys whatever the batch.  A unit cut by a run's end leaves FP32 partials (at
 // most two a CTA) and a second small kernel adds them in run order.
 //
-// Inside a CTA: warp 8 brings K and V tiles into a ring by TMA, a box per page
-// and 64-wide half (any page size from 8 on; the table's entries are fetched a
-// tile ahead); warp 9 issues the MMAs; warps 0-3 and 4-7 are two softmax groups,
-// a thread a row and half of the tile's keys.  S and P have two buffers each in
-// tensor memory (with O they fill it), so the products of the next tile's S and
-// of the last tile's P V run beside the exponentials of this one.  P goes back
-// to tensor memory as the A operand of P V; V is the MN-major B operand as it
-// lies.  A row's two threads exchange their maxima through shared memory.
+// Inside a CTA: warps 8 and 10 bring K and V tiles into a ring by TMA, a box per
+// page and 64-wide half (any page size from 8 on; the table's entries are fetched
+// two tiles ahead); warp 9 issues the MMAs; warp 11 works the run's pieces out
+// ahead and loads their Q; warps 0-3 and 4-7 are two softmax groups, a thread a row
+// and half of the tile's keys.  S and P have two buffers each in tensor memory (with
+// O they fill it): S runs two tiles ahead, so that the next tile's scores come to a
+// thread's registers beside this one's exponentials.  P goes back to tensor memory
+// as the A operand of P V; V is the MN-major B operand as it lies.  A row's two
+// threads exchange their maxima through shared memory.
 //
 // The reference m of a row follows its maximum only when that rose by more than
 // 2^8: below that p and the sums just grow by at most 2^8, exactly undone by the
@@ -33,8 +34,9 @@
 // 177 us = 5.9 TB/s (the mean CTA streams at 6.8).  With 128 rows a tile's chain
 // (scores ready, exponentials, P stored, maxima exchanged), about 1700 cycles where
 // its products need 1024: 32 requests with trees of up to 64 and 16 query heads a KV
-// head 89 us = 755 TFLOP/s.  128 keys a tile and not 64: 89 against 143 us there, and
-// 165 against 203 us for the long request (a tile's fixed waits count twice).
+// head 89 us = 755 TFLOP/s.  The other split measured, tiles of 64 keys that the two
+// groups take in turn, each with its own reference and O and no exchange, doubles a
+// tile's fixed waits: 143 us there, 203 us for the long request.
 //
 // Masked places.  Only the tiles that hold nodes or end past the last key look
 // at masks; there, V rows past the last key are zeroed in shared memory (P is 0,
@@ -317,9 +319,9 @@ __device__ __forceinline__ Req request(const AttnArgs& a, int r, int tb, int* ba
   q.q0 = min(max(a.q_start[r], 0), a.T);
   const int q1 = min(max(a.q_start[r + 1], q.q0), a.T);
   q.n = q1 - q.q0;
-  const int64_t cap = (int64_t)a.max_pages << a.page_shift;
+  const int cap = a.max_pages << a.page_shift;             // at most 2^30
   const int kv = a.kv_len[r];
-  q.kv = (int)min((int64_t)max(kv, q.n), cap);
+  q.kv = min(max(kv, q.n), cap);
   if (bad && (q.kv != kv || q.q0 != a.q_start[r])) *bad = 1;
   q.ctx = max(q.kv - q.n, 0);
   q.tiles = max((q.kv + kTile - 1) / kTile, 1);
@@ -491,7 +493,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         p.n = max(t1 - t0, 0);
       }
       const int e = made % kQueue;
-      if (!wait_warp<1>(bar(sm.piece_empty[e]), ((uint32_t)(made / kQueue) & 1u) ^ 1u, abort_flag, err)) break;
+      if (made >= kQueue &&
+          !wait_warp<1>(bar(sm.piece_empty[e]), ((uint32_t)(made / kQueue) & 1u) ^ 1u, abort_flag, err))
+        break;
       if (lane == 0) {
         sm.piece[e] = p;
         mbar_arrive(bar(sm.piece_full[e]));
@@ -500,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++made;
       if (last || p.n == 0) continue;
       // Q, once the last S of the piece before is done; K and V of this piece are on their way meanwhile
-      if (!wait_warp<1>(bar(sm.q_empty), (loads & 1) ^ 1, abort_flag, err)) break;
+      if (loads > 0 && !wait_warp<1>(bar(sm.q_empty), (loads & 1) ^ 1, abort_flag, err)) break;
       if (elect_one()) {
         mbar_expect_tx(bar(sm.q_full), (uint32_t)(X::NH * 128 * a.G * tb));
 #pragma unroll
@@ -540,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       int id[4] = {page_of(0), page_of(1), page_of(2), -1};   // tiles j .. j + 3
       auto load = [&](const CUtensorMap* map, int j, int pid) {
-        ok = wait_warp<1>(bar(sm.empty[slot]), phase ^ 1u, abort_flag, err);
+        if (it >= NS) ok = wait_warp<1>(bar(sm.empty[slot]), phase ^ 1u, abort_flag, err);
         if (!ok) return;
         const int boxes = __popc(__ballot_sync(0xffffffffu, pid >= 0));   // lanes 0 .. boxes - 1
         const int off = ((p.t0 + j) * kTile) & (page - 1);                // pages larger than a tile
