@@ -109,7 +109,7 @@ struct Small {
   int first_r;
   uint32_t tmem;
   int abort;
-  int scan[16];
+  int64_t scan[kThreads / 32];
 };
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
@@ -397,27 +397,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int per = (a.R + kThreads - 1) / kThreads, r0 = min((int)threadIdx.x * per, a.R), r1 = min(r0 + per, a.R);
     auto cost = [&](const Req& q) { return (q.tiles + kAttnPieceCost) * q.blocks * a.Hkv; };
     Req q;
-    int local = 0;
-    for (int r = r0; r < r1; ++r) {
+    int64_t local = 0;                                     // (one request's cost fits 31 bits; row starts that are no
+    for (int r = r0; r < r1; ++r) {                        // prefix sums may not add up to so few)
       q = request(a, r, tb, &bad);
       local += cost(q);
     }
-    int x = local;
+    int64_t x = local;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, off);
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, off);
       if (lane >= off) x += y;
     }
     if (lane == 31) sm.scan[warp] = x;
     __syncthreads();
-    int run = x - local;
-    total = 0;
+    int64_t before = x - local, all = 0;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
-      const int s = sm.scan[w];
-      if (w < warp) run += s;
-      total += s;
+      const int64_t s = sm.scan[w];
+      if (w < warp) before += s;
+      all += s;
     }
+    if (all > INT32_MAX) {
+      bad = 1;
+      all = 0;                                             // nothing is computed
+    }
+    total = (int)all;
+    int run = (int)before;
     runs = min((int)gridDim.x, max(total, 1));
     share = total / runs;
     extra = total - share * runs;

@@ -602,6 +602,10 @@ def test_bad_pages_and_lengths_are_flagged(dt):
     out, _ = s.run()
     assert _err(s.ws) == M.MOE_DEVERR_CACHE and torch.equal(out[2:], good[2:])
     s = Step([200, 30], [2, 2], 8, 2, 64, 16, dt, seed=9)
+    s.q_start[2] = 9                                         # past the rows
+    out, _ = s.run()
+    assert torch.equal(out[:2], good[:2])
+    s = Step([200, 30], [2, 2], 8, 2, 64, 16, dt, seed=9)
     s.kv_len[0] = 1                                          # fewer tokens than nodes
     out, _ = s.run()
     assert _err(s.ws) == M.MOE_DEVERR_CACHE and torch.equal(out[2:], good[2:])
