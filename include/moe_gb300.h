@@ -507,8 +507,10 @@ moe_status_t moe_rope_append(const moe_attn_config_t* cfg, int32_t T, const void
  * lse = -inf.  Keys that no row sees (stale or unwritten cache memory) do not
  * enter, whatever they hold, NaN and infinities included; nor do a node's K and
  * V enter the rows that do not see that node.  FP32 scores and softmax; BF16:
- * the probabilities enter the second product in BF16.  Lengths outside the block
- * table's row are clamped and pages outside the cache read as zeros, both with
+ * the probabilities enter the second product in BF16.  Where kv_len ends past the
+ * block table's row, the tokens past it (nodes among them) are seen by no row and
+ * the others stay where they are; a kv_len below the number of nodes counts as
+ * that number; pages outside the cache read as zeros; all with
  * MOE_DEVERR_CACHE.  (T + R) * Hkv * (ceil(max_pages * page_size / 128) + 5) and
  * 32 * T * H must stay below 2^31 (MOE_ERR_UNSUPPORTED).  FP32 runs on the CUDA
  * cores and is made for the sizes of FP32 layers.                             */

@@ -79,12 +79,11 @@ __global__ void __launch_bounds__(kThreads) attention_f32_kernel(const AttnArgs 
   if (r < a.R) {
     const int q0 = a.q_start[r], n = a.q_start[r + 1] - q0, node = t - q0;
     const int64_t cap = (int64_t)a.max_pages << a.page_shift;
-    int kv = a.kv_len[r];
-    if (kv < n || kv > cap) {
-      bad = MOE_DEVERR_CACHE;
-      kv = (int)min((int64_t)max(kv, n), cap);
-    }
-    const int ctx = max(kv - n, 0);
+    // a length past the table's row is cut there: its tokens before that stay where they are, nodes among them or not
+    const int len = a.kv_len[r];
+    if (len < n || len > cap) bad = MOE_DEVERR_CACHE;
+    const int ctx = (int)min((int64_t)max(len, n) - n, cap);
+    const int kv = (int)min((int64_t)ctx + n, cap);
     const int32_t* table = a.block_table + (int64_t)r * a.max_pages;
     const int32_t* mask = a.tree_mask ? a.tree_mask + (int64_t)t * a.mask_words : nullptr;
     const int tiles = (kv + 31) / 32;

@@ -85,7 +85,7 @@ struct Maps {
 struct Piece {
   int r, h;                // request, KV head
   int row0, tok0, ntok;    // first row of the block in q; its first node and its nodes
-  int ctx, kv;             // tokens before the nodes; all tokens
+  int ctx, kv;             // tokens before the nodes; all tokens of the table's row (at most ctx + nodes)
   int t0, n;               // first tile and number of tiles (those that a chain's block can see)
   int flags;               // kStarts, kEnds, kLast
   int parts;               // of a unit that starts here and ends in a later run: its runs
@@ -319,11 +319,12 @@ __device__ __forceinline__ Req request(const AttnArgs& a, int r, int tb, int* ba
   q.q0 = min(max(a.q_start[r], 0), a.T);
   const int q1 = min(max(a.q_start[r + 1], q.q0), a.T);
   q.n = q1 - q.q0;
+  // a length past the table's row is cut there: its tokens before that stay where they are, nodes among them or not
   const int cap = a.max_pages << a.page_shift;             // at most 2^30
   const int kv = a.kv_len[r];
-  q.kv = min(max(kv, q.n), cap);
-  if (bad && (q.kv != kv || q.q0 != a.q_start[r])) *bad = 1;
-  q.ctx = max(q.kv - q.n, 0);
+  q.ctx = min(max(kv, q.n) - q.n, cap);
+  q.kv = min(q.ctx + q.n, cap);
+  if (bad && (kv < q.n || kv > cap || q.q0 != a.q_start[r])) *bad = 1;
   q.tiles = max((q.kv + kTile - 1) / kTile, 1);
   q.blocks = (q.n + tb - 1) / tb;
   return q;

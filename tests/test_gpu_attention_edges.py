@@ -1,0 +1,83 @@
+"""Paged attention where a step leaves its ranges: requests that outgrow their
+block-table row, against plain NumPy evaluations in 64 bits with the tolerances
+derived in ``test_gpu_attention``."""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_attention import BF, FP, Step, _err, _i32, _m, random_parents
+
+pytestmark = pytest.mark.gpu
+
+
+class Overrun(Step):
+    """A step whose requests may be longer than their block-table row: tokens past its
+    last entry are in no page, so no row sees them; every other token stays where it is."""
+
+    def __init__(self, *args, max_pages, **kw):
+        super().__init__(*args, **kw)
+        self.cap = max_pages * self.page
+        self.cfg.max_pages = max_pages
+        self.table_d = self.table_d[:, :max_pages].contiguous()
+
+    def seen(self, r):
+        see = super().seen(r)
+        see[:, self.cap:] = False
+        return see
+
+    def check_flagged(self, out, lse):
+        M = _m()
+        assert _err(self.ws) == M.MOE_DEVERR_CACHE
+        M.moe_clear_device_error(self.ws)
+        self.check(out, lse)
+
+
+OVERRUN = [
+    # ctx, new, page, max_pages: the first request ends past its row, the second does not
+    ([31, 20], [3, 2], 16, 2),             # the first node is still in a page
+    ([32, 20], [2, 2], 16, 2),             # none is
+    ([250, 7], [40, 5], 16, 17),           # nodes past a tile's edge, some in pages
+    ([100, 3], [200, 4], 16, 9),           # several row blocks, the row ends inside the nodes
+    ([256, 9], [30, 1], 128, 2),           # the row ends with a tile
+]
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("ctx,new,page,max_pages", OVERRUN)
+def test_nodes_keep_their_tokens_where_a_request_outgrows_its_row(ctx, new, page, max_pages, tree, dt):
+    s = Overrun(ctx, new, 8, 2, 64, page, dt, tree=tree, max_pages=max_pages, seed=21)
+    s.check_flagged(*s.run())
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("ctx,new,page,max_pages", OVERRUN)
+def test_a_step_that_outgrows_its_row(ctx, new, page, max_pages, tree, dt):
+    """plan -> append -> attend of the same: the plan keeps all rows and names the full
+    length, the nodes that have a slot are attended at their tokens."""
+    M = _m()
+    H, Hkv, D, R = 8, 2, 64, len(ctx)
+    s = Overrun(ctx, new, H, Hkv, D, page, dt, tree=False, max_pages=max_pages, seed=22)
+    cfg = M.make_attn_config(H, Hkv, D, page_size=page, n_pages=R * max_pages, max_pages=max_pages, dtype=s.cfg.dtype)
+    c = M.PagedKVCache(cfg, R)
+
+    def rows(store, first, count):         # tokens first .. first + count - 1 of every request
+        t = [np.arange(a, a + b) for a, b in zip(first, count)]
+        return torch.cat([store[torch.from_numpy(s.table[r][x // page]).long().cuda(), torch.from_numpy(x % page).cuda()]
+                          for r, x in enumerate(t)])
+
+    zero, total = [0] * R, sum(ctx)
+    prompt = torch.zeros((total, H, D), dtype=dt, device="cuda")
+    c.append(c.plan(_i32(zero), _i32(ctx), total), prompt, rows(s.k, zero, ctx), rows(s.v, zero, ctx))
+    assert _err(c.ws) == 0
+    par = _i32(random_parents(np.random.default_rng(5), new, "tree")) if tree else None
+    step = c.plan(_i32(ctx), _i32(new), s.T, parents=par, max_nodes=max(new))
+    assert step.kv_len.tolist() == [a + b for a, b in zip(ctx, new)] and step.q_start.tolist() == s.q_start.tolist()
+    q = c.append(step, s.q, rows(s.k, ctx, new), rows(s.v, ctx, new))
+    lse = torch.empty((s.T, H), device="cuda")
+    out = c.attend(step, q, lse=lse)
+    assert _err(c.ws) == M.MOE_DEVERR_PAGES | M.MOE_DEVERR_CACHE
+    s.mask = step.tree_mask
+    s.words = 0 if s.mask is None else s.mask.shape[1]
+    s.check(out, lse)
