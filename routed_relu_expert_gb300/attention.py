@@ -208,10 +208,17 @@ class PagedKVCache:
         self.ws = new_attn_workspace(cfg, device)
         self.table, self.rot_scale = rope_table(cfg.rot_dim, theta, device=device, **scaling)
 
-    def plan(self, ctx_len, new_len, T: int, parents=None, max_nodes: int = 32, stream=None) -> PagedStep:
+    def plan(self, ctx_len, new_len, T: int, parents=None, max_nodes: Optional[int] = None, stream=None) -> PagedStep:
         """ctx_len, new_len [R] (R = max_requests; idle requests bring 0 tokens);
-        T rows; parents [T]: trees of up to max_nodes nodes."""
+        T rows; parents [T]: trees of up to max_nodes nodes (nodes past that are seen by
+        nobody, with MOE_DEVERR_CACHE in the workspace's error word).  By default the mask
+        has room for any tree that T rows and a block-table row can hold; a server with
+        many rows passes its largest tree, for T * ceil(max_nodes / 32) words of mask."""
         R, dev = self.block_table.shape[0], self.block_table.device
+        if max_nodes is None:
+            max_nodes = max(1, min(T, self.cfg.max_pages * self.cfg.page_size))
+        elif max_nodes < 1:
+            raise ValueError(f"max_nodes must be at least 1, got {max_nodes}")
 
         def new(*shape, dtype=torch.int32):
             return torch.empty(shape, dtype=dtype, device=dev)

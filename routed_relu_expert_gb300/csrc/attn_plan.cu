@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
       }
       if (!par) continue;
       int depth = 0;
-      if (n <= 32 * max_doubled && a.mask_words <= 2 && (a.mask_words != 1 || n <= 32)) {
+      if (n <= 32 * max_doubled && (a.mask_words != 1 || n <= 32)) {
         // trees of up to 32 nodes (64 where one warp has them all): ancestor sets by pointer doubling, five rounds
         // of shuffles a 32 whatever the depth.  Ancestors come before a node, so the first 32 need no others; a node
         // of the second 32 joins its ancestors there with the set of the one of the first that its chain leaves to
@@ -210,8 +210,14 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
         if (live && a.tree_mask) {
           int32_t* out = a.tree_mask + (int64_t)(start + i) * a.mask_words;
           out[0] = (int32_t)low;
-          if (a.mask_words == 2) out[1] = (int32_t)high;
+          if (a.mask_words > 1) out[1] = (int32_t)high;
         }
+        // a mask wider than the tree: the warp clears the rest, row by row
+        if (a.mask_words > 2)
+          for (int j = i0; j < min(i0 + 32, n); ++j) {
+            int32_t* out = a.tree_mask + (int64_t)(start + j) * a.mask_words;
+            for (int w = 2 + lane; w < a.mask_words; w += 32) out[w] = 0;
+          }
       } else if (live) {
         // any size: walk to the root; ancestors descend, so the words of the
         // mask are finished from the last to the first

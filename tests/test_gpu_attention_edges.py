@@ -1,11 +1,11 @@
-"""Paged attention where a step leaves its ranges: requests that outgrow their
-block-table row, against plain NumPy evaluations in 64 bits with the tolerances
-derived in ``test_gpu_attention``."""
+"""Paged attention where a step leaves the usual ranges: requests that outgrow their
+block-table row, trees of many nodes.  Against plain NumPy evaluations in 64 bits, with
+the tolerances derived in ``test_gpu_attention``."""
 import numpy as np
 import pytest
 import torch
 
-from test_gpu_attention import BF, FP, Step, _err, _i32, _m, random_parents
+from test_gpu_attention import BF, FP, Step, _err, _i32, _m, plan_reference, random_parents, run_plan
 
 pytestmark = pytest.mark.gpu
 
@@ -81,3 +81,30 @@ def test_a_step_that_outgrows_its_row(ctx, new, page, max_pages, tree, dt):
     s.mask = step.tree_mask
     s.words = 0 if s.mask is None else s.mask.shape[1]
     s.check(out, lse)
+
+
+@pytest.mark.parametrize("new,T", [([40], 40), ([33, 1, 64, 0], 98), ([100, 7], 110), ([5] * 60, 300)])
+def test_no_node_is_lost_from_a_step_of_trees(new, T):
+    """The mask of PagedKVCache.plan has room for every tree that the rows can hold."""
+    M = _m()
+    R, page, most = len(new), 16, 10
+    cfg = M.make_attn_config(2, 1, 16, page_size=page, n_pages=R * most, max_pages=most)
+    c = M.PagedKVCache(cfg, R)
+    par = random_parents(np.random.default_rng(6), new, "path")
+    step = c.plan(_i32([0] * R), _i32(new), T, parents=_i32(par + [-1] * (T - len(par))))
+    assert _err(c.ws) == 0
+    words = step.tree_mask.shape[1]
+    want = plan_reference([0] * R, new, par, np.full((R, most), -1), np.arange(R * most), 0, page, T, words, R * most)
+    assert np.array_equal(step.tree_mask.cpu().numpy().view(np.uint32), want["tree_mask"].astype(np.uint32))
+    assert step.positions.tolist() == want["positions"].tolist()
+    own, at = np.concatenate([np.arange(n) for n in new]), np.arange(sum(new))      # a node is among its row's
+    assert np.all(want["tree_mask"][at, own // 32] >> (own % 32) & 1)
+
+
+@pytest.mark.parametrize("ctx,new,kind", [([33, 2, 0], [16, 1, 32], "tree"), ([10, 4], [64, 33], "path"),
+                                          ([6, 7], [64, 64], "path"), ([9] * 40, [i % 17 for i in range(40)], "roots"),
+                                          ([3], [130], "roots")])
+@pytest.mark.parametrize("words", [3, 9])
+def test_plan_writes_masks_wider_than_the_trees(ctx, new, kind, words):
+    words = max(words, -(-max(new) // 32))
+    assert run_plan(ctx, new, 16, kind=kind, words=words, T=sum(new) + 3, seed=7) == 0
