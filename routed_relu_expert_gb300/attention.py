@@ -3,10 +3,11 @@ moe_rope, moe_rope_append and moe_tree_attention, and a holder of one layer's
 paged KV cache.
 
 As in ``layer``: each function checks tensor placement, types and shapes, takes
-data pointers and the current CUDA stream, and calls the library.  Rows
-([T, heads, head_dim]) may be parts of a wider row, such as one projection's
-q, k and v; caches are views [n_pages, page_size, n_kv_heads, head_dim] of any
-layout whose head_dim is contiguous.
+data pointers and the current CUDA stream, and calls the library, which launches
+on the current device: the operands, and a stream that is given, have to be that
+device's.  Rows ([T, heads, head_dim]) may be parts of a wider row, such as one
+projection's q, k and v; caches are views [n_pages, page_size, n_kv_heads,
+head_dim] of any layout whose head_dim is contiguous.
 """
 from __future__ import annotations
 
@@ -23,6 +24,7 @@ from .layer import _s
 
 # the current stream's handle of a device, without building a Stream object for it (3 us a call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 _TORCH = {N.MOE_DT_BF16: torch.bfloat16, N.MOE_DT_F32: torch.float32}
 # all fields of a moe_attn_config_t at once (reading them one by one costs as much as the launch)
@@ -45,9 +47,21 @@ def make_attn_config(n_heads: int, n_kv_heads: int, head_dim: int, *, page_size:
                            int(rope_interleaved), float(softmax_scale), dtype, *strides)
 
 
-def _stream(stream, t: torch.Tensor):
+def _device(t: torch.Tensor, name: str) -> int:
+    """The device that all of a call's tensors have to be on: that of ``t``, which is current."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dev != _current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{_current_device()}")
+    return dev
+
+
+def _stream(stream, dev: int):
     if stream is None and _raw_stream is not None:
-        return _raw_stream(t.get_device())
+        return _raw_stream(dev)
+    if getattr(stream, "device_index", dev) != dev:
+        raise ValueError(f"the stream is one of cuda:{stream.device_index}, the tensors are on cuda:{dev}")
     return _s(stream)
 
 
@@ -64,29 +78,29 @@ def new_attn_workspace(cfg: N.MoeAttnConfig, device="cuda") -> torch.Tensor:
     return ws
 
 
-def _array(t: Optional[torch.Tensor], dtype, n: Optional[int], name: str):
-    """Pointer of a contiguous device array of n values (None: any number)."""
+def _array(t: Optional[torch.Tensor], dtype, n: Optional[int], name: str, dev: int):
+    """Pointer of a contiguous array of n values (None: any number) on the device."""
     if t is None:
         return None
-    if not t.is_cuda or t.dtype is not dtype or not t.is_contiguous() or (n is not None and t.numel() != n):
-        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor"
+    if t.get_device() != dev or t.dtype is not dtype or not t.is_contiguous() or (n is not None and t.numel() != n):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on cuda:{dev}"
                          + ("" if n is None else f" of {n} values"))
     return t.data_ptr()
 
 
-def _rows(t: torch.Tensor, T: int, heads: int, D: int, dt, name: str) -> Tuple[int, int]:
+def _rows(t: torch.Tensor, T: int, heads: int, D: int, dt, name: str, dev: int) -> Tuple[int, int]:
     """(pointer, row stride) of rows [T, heads, D]."""
-    if not t.is_cuda or t.dtype is not dt or t.shape != (T, heads, D):
-        raise ValueError(f"{name} must be a {dt} CUDA tensor of shape {(T, heads, D)}")
+    if t.get_device() != dev or t.dtype is not dt or t.shape != (T, heads, D):
+        raise ValueError(f"{name} must be a {dt} tensor on cuda:{dev} of shape {(T, heads, D)}")
     ld, step, one = t.stride()
     if (one != 1 and D > 1) or (heads > 1 and step != D):
         raise ValueError(f"the heads of a row of {name} must be contiguous")
     return t.data_ptr(), (ld if T > 1 else heads * D)
 
 
-def _cache(t: torch.Tensor, shape, strides, dt, name: str) -> int:
-    if not t.is_cuda or t.dtype is not dt or t.shape != shape:
-        raise ValueError(f"{name} must be a {dt} CUDA tensor of shape {shape}")
+def _cache(t: torch.Tensor, shape, strides, dt, name: str, dev: int) -> int:
+    if t.get_device() != dev or t.dtype is not dt or t.shape != shape:
+        raise ValueError(f"{name} must be a {dt} tensor on cuda:{dev} of shape {shape}")
     if t.stride() != strides:
         raise ValueError(f"{name} does not have the configuration's strides")
     return t.data_ptr()
@@ -97,17 +111,18 @@ def moe_paged_plan(cfg, ctx_len, new_len, block_table, free_pages, free_head, q_
     """Block tables, slots, positions and tree masks of a step, written into
     block_table, q_start, kv_len, positions, slot_map, tree_mask and
     free_head_out (default: free_head, in place)."""
-    R, T, i32 = ctx_len.shape[0], positions.shape[0], torch.int32
+    dev, R, T, i32 = _device(ws, "ws"), ctx_len.shape[0], positions.shape[0], torch.int32
     words = 0 if tree_mask is None else tree_mask.shape[1]
     N.check(N.load().moe_paged_plan(
-        ctypes.byref(cfg), R, T, _array(ctx_len, i32, R, "ctx_len"), _array(new_len, i32, R, "new_len"),
-        _array(parents, i32, T, "parents"), _array(block_table, i32, R * cfg.max_pages, "block_table"),
-        _array(free_pages, i32, None, "free_pages"), free_pages.numel(), _array(free_head, i32, 1, "free_head"),
-        _array(free_head if free_head_out is None else free_head_out, i32, 1, "free_head_out"),
-        _array(q_start, i32, R + 1, "q_start"), _array(kv_len, i32, R, "kv_len"),
-        _array(positions, i32, T, "positions"), _array(slot_map, torch.int64, T, "slot_map"),
-        _array(tree_mask, i32, T * words, "tree_mask"), words, _array(ws, torch.uint8, None, "ws"), ws.numel(),
-        _stream(stream, ws)), "moe_paged_plan")
+        ctypes.byref(cfg), R, T, _array(ctx_len, i32, R, "ctx_len", dev), _array(new_len, i32, R, "new_len", dev),
+        _array(parents, i32, T, "parents", dev), _array(block_table, i32, R * cfg.max_pages, "block_table", dev),
+        _array(free_pages, i32, None, "free_pages", dev), free_pages.numel(),
+        _array(free_head, i32, 1, "free_head", dev),
+        _array(free_head if free_head_out is None else free_head_out, i32, 1, "free_head_out", dev),
+        _array(q_start, i32, R + 1, "q_start", dev), _array(kv_len, i32, R, "kv_len", dev),
+        _array(positions, i32, T, "positions", dev), _array(slot_map, torch.int64, T, "slot_map", dev),
+        _array(tree_mask, i32, T * words, "tree_mask", dev), words,
+        _array(ws, torch.uint8, None, "ws", dev), ws.numel(), _stream(stream, dev)), "moe_paged_plan")
 
 
 def rope_table(rot_dim: int, theta: float, *, scaling: Optional[str] = None, factor: float = 1.0,
@@ -122,63 +137,65 @@ def rope_table(rot_dim: int, theta: float, *, scaling: Optional[str] = None, fac
     return host.to(device), float(scale.value)
 
 
-def _table(rot: int, table):
+def _table(rot: int, table, dev: int):
     if rot == 0:
         return None
     if table is None:
         raise ValueError("table is missing")
-    return _array(table, torch.int64, rot // 2, "table")
+    return _array(table, torch.int64, rot // 2, "table", dev)
 
 
 def moe_rope(cfg, x, positions, table, out, rot_scale: float = 1.0, inverse: bool = False, stream=None):
     """Rows x [T, heads, head_dim] turned by their positions into ``out`` (which
     may be x); ``inverse`` is the backward."""
-    T, heads = x.shape[0], x.shape[1]
+    dev, T, heads = _device(x, "x"), x.shape[0], x.shape[1]
     _, _, D, _, _, _, rot, _, _, dtype, _, _, _ = _FIELDS.unpack_from(cfg)
     dt = _TORCH.get(dtype)
-    xp, x_ld = _rows(x, T, heads, D, dt, "x")
-    op, o_ld = _rows(out, T, heads, D, dt, "out")
-    N.check(N.load().moe_rope(ctypes.byref(cfg), T, heads, xp, x_ld, _array(positions, torch.int32, T, "positions"),
-                              _table(rot, table), rot_scale, int(inverse), op, o_ld, _stream(stream, x)), "moe_rope")
+    xp, x_ld = _rows(x, T, heads, D, dt, "x", dev)
+    op, o_ld = _rows(out, T, heads, D, dt, "out", dev)
+    N.check(N.load().moe_rope(ctypes.byref(cfg), T, heads, xp, x_ld,
+                              _array(positions, torch.int32, T, "positions", dev), _table(rot, table, dev), rot_scale,
+                              int(inverse), op, o_ld, _stream(stream, dev)), "moe_rope")
 
 
 def moe_rope_append(cfg, q, k, v, positions, table, slot_map, k_cache, v_cache, q_out, ws, rot_scale: float = 1.0,
                     stream=None):
     """q turned into q_out (which may be q); k turned and v as it is into the
     caches at slot_map."""
-    T = q.shape[0]
+    dev, T = _device(ws, "ws"), q.shape[0]
     H, Hkv, D, page, pages, _, rot, _, _, dtype, sp, st, sh = _FIELDS.unpack_from(cfg)
     dt = _TORCH.get(dtype)
-    qp, q_ld = _rows(q, T, H, D, dt, "q")
-    kp, k_ld = _rows(k, T, Hkv, D, dt, "k")
-    vp, v_ld = _rows(v, T, Hkv, D, dt, "v")
-    op, o_ld = _rows(q_out, T, H, D, dt, "q_out")
+    qp, q_ld = _rows(q, T, H, D, dt, "q", dev)
+    kp, k_ld = _rows(k, T, Hkv, D, dt, "k", dev)
+    vp, v_ld = _rows(v, T, Hkv, D, dt, "v", dev)
+    op, o_ld = _rows(q_out, T, H, D, dt, "q_out", dev)
     shape, strides = (pages, page, Hkv, D), (sp, st, sh, 1)
     N.check(N.load().moe_rope_append(ctypes.byref(cfg), T, qp, q_ld, kp, k_ld, vp, v_ld,
-                                     _array(positions, torch.int32, T, "positions"), _table(rot, table), rot_scale,
-                                     _array(slot_map, torch.int64, T, "slot_map"), op, o_ld,
-                                     _cache(k_cache, shape, strides, dt, "k_cache"),
-                                     _cache(v_cache, shape, strides, dt, "v_cache"),
-                                     _array(ws, torch.uint8, None, "ws"), ws.numel(), _stream(stream, ws)),
+                                     _array(positions, torch.int32, T, "positions", dev), _table(rot, table, dev),
+                                     rot_scale, _array(slot_map, torch.int64, T, "slot_map", dev), op, o_ld,
+                                     _cache(k_cache, shape, strides, dt, "k_cache", dev),
+                                     _cache(v_cache, shape, strides, dt, "v_cache", dev),
+                                     _array(ws, torch.uint8, None, "ws", dev), ws.numel(), _stream(stream, dev)),
             "moe_rope_append")
 
 
 def moe_tree_attention(cfg, q, q_start, kv_len, block_table, k_cache, v_cache, out, ws, tree_mask=None, lse=None,
                        stream=None):
     """out [T, n_heads, head_dim] (and lse [T, n_heads] FP32) of the rows q over the cache."""
-    T, R, i32 = q.shape[0], kv_len.shape[0], torch.int32
+    dev, T, R, i32 = _device(ws, "ws"), q.shape[0], kv_len.shape[0], torch.int32
     H, Hkv, D, page, pages, max_pages, _, _, _, dtype, sp, st, sh = _FIELDS.unpack_from(cfg)
     dt = _TORCH.get(dtype)
     words = 0 if tree_mask is None else tree_mask.shape[1]
-    qp, q_ld = _rows(q, T, H, D, dt, "q")
-    op, o_ld = _rows(out, T, H, D, dt, "out")
+    qp, q_ld = _rows(q, T, H, D, dt, "q", dev)
+    op, o_ld = _rows(out, T, H, D, dt, "out", dev)
     shape, strides = (pages, page, Hkv, D), (sp, st, sh, 1)
     N.check(N.load().moe_tree_attention(
-        ctypes.byref(cfg), R, T, qp, q_ld, _array(q_start, i32, R + 1, "q_start"), _array(kv_len, i32, R, "kv_len"),
-        _array(block_table, i32, R * max_pages, "block_table"), _cache(k_cache, shape, strides, dt, "k_cache"),
-        _cache(v_cache, shape, strides, dt, "v_cache"), _array(tree_mask, i32, T * words, "tree_mask"), words, op, o_ld,
-        _array(lse, torch.float32, T * H, "lse"), _array(ws, torch.uint8, None, "ws"), ws.numel(),
-        _stream(stream, ws)), "moe_tree_attention")
+        ctypes.byref(cfg), R, T, qp, q_ld, _array(q_start, i32, R + 1, "q_start", dev),
+        _array(kv_len, i32, R, "kv_len", dev), _array(block_table, i32, R * max_pages, "block_table", dev),
+        _cache(k_cache, shape, strides, dt, "k_cache", dev), _cache(v_cache, shape, strides, dt, "v_cache", dev),
+        _array(tree_mask, i32, T * words, "tree_mask", dev), words, op, o_ld,
+        _array(lse, torch.float32, T * H, "lse", dev), _array(ws, torch.uint8, None, "ws", dev), ws.numel(),
+        _stream(stream, dev)), "moe_tree_attention")
 
 
 @dataclass
