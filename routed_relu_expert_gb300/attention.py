@@ -106,13 +106,23 @@ def _cache(t: torch.Tensor, shape, strides, dt, name: str, dev: int) -> int:
     return t.data_ptr()
 
 
+def _words(tree_mask: Optional[torch.Tensor], T: int) -> int:
+    """Words a row of the mask (0: no mask, chains)."""
+    if tree_mask is None:
+        return 0
+    shape = tree_mask.shape
+    if len(shape) != 2 or shape[0] != T or shape[1] < 1:
+        raise ValueError(f"tree_mask must be of shape ({T}, words)")
+    return shape[1]
+
+
 def moe_paged_plan(cfg, ctx_len, new_len, block_table, free_pages, free_head, q_start, kv_len, positions, slot_map,
                    ws, free_head_out=None, parents=None, tree_mask=None, stream=None):
     """Block tables, slots, positions and tree masks of a step, written into
     block_table, q_start, kv_len, positions, slot_map, tree_mask and
     free_head_out (default: free_head, in place)."""
     dev, R, T, i32 = _device(ws, "ws"), ctx_len.shape[0], positions.shape[0], torch.int32
-    words = 0 if tree_mask is None else tree_mask.shape[1]
+    words = _words(tree_mask, T)
     N.check(N.load().moe_paged_plan(
         ctypes.byref(cfg), R, T, _array(ctx_len, i32, R, "ctx_len", dev), _array(new_len, i32, R, "new_len", dev),
         _array(parents, i32, T, "parents", dev), _array(block_table, i32, R * cfg.max_pages, "block_table", dev),
@@ -185,7 +195,7 @@ def moe_tree_attention(cfg, q, q_start, kv_len, block_table, k_cache, v_cache, o
     dev, T, R, i32 = _device(ws, "ws"), q.shape[0], kv_len.shape[0], torch.int32
     H, Hkv, D, page, pages, max_pages, _, _, _, dtype, sp, st, sh = _FIELDS.unpack_from(cfg)
     dt = _TORCH.get(dtype)
-    words = 0 if tree_mask is None else tree_mask.shape[1]
+    words = _words(tree_mask, T)
     qp, q_ld = _rows(q, T, H, D, dt, "q", dev)
     op, o_ld = _rows(out, T, H, D, dt, "out", dev)
     shape, strides = (pages, page, Hkv, D), (sp, st, sh, 1)

@@ -108,3 +108,14 @@ def test_a_stream_of_another_device_is_refused(lib, op):
     CALLS[op](CFG, **operands()[op], stream=Stream())
     CALLS[op](CFG, **operands()[op], stream=78)
     assert [getattr(args[-1], "value", args[-1]) for _, args in lib.calls] == [77, 78]
+
+
+@pytest.mark.parametrize("op", ["plan", "attention"])
+@pytest.mark.parametrize("shape", [(T, 0), (T,), (T - 1, 1), (1, T), (1, T, 1)])
+def test_a_mask_that_is_no_mask_of_the_rows_is_refused(lib, op, shape):
+    """A mask without words would reach the library as none at all: a chain."""
+    a = operands()[op]
+    a["tree_mask"] = Tensor(I32, *shape)
+    with pytest.raises(ValueError, match="tree_mask"):
+        CALLS[op](CFG, **a)
+    assert not lib.calls
