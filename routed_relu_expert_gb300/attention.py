@@ -11,6 +11,7 @@ head_dim] of any layout whose head_dim is contiguous.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import struct
@@ -208,6 +209,15 @@ def moe_tree_attention(cfg, q, q_start, kv_len, block_table, k_cache, v_cache, o
         _stream(stream, dev)), "moe_tree_attention")
 
 
+def _memory_of(stream, device):
+    """Within it, new tensors are the memory of the stream that a call is given (None: the current one)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device) if int(stream) else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
 @dataclass
 class PagedStep:
     """What PagedKVCache.plan leaves for the other calls of a step."""
@@ -221,7 +231,9 @@ class PagedStep:
 class PagedKVCache:
     """One attention layer's paged KV cache: the pages, the requests' block
     tables, the free pages and the workspace.  A step is plan -> append -> attend,
-    all on the current stream, nothing on the host."""
+    all on the current stream, nothing on the host.  A call that is given another
+    stream makes its tensors from that stream's memory; they are used on a third one
+    as any tensor is (after an event, with ``record_stream``)."""
 
     def __init__(self, cfg: N.MoeAttnConfig, max_requests: int, device="cuda", theta: float = 10000.0, **scaling):
         self.cfg = cfg
@@ -250,8 +262,9 @@ class PagedKVCache:
         def new(*shape, dtype=torch.int32):
             return torch.empty(shape, dtype=dtype, device=dev)
 
-        step = PagedStep(new(R + 1), new(R), new(T), new(T, dtype=torch.int64),
-                         None if parents is None else new(T, -(-max_nodes // 32)))
+        with _memory_of(stream, dev):
+            step = PagedStep(new(R + 1), new(R), new(T), new(T, dtype=torch.int64),
+                             None if parents is None else new(T, -(-max_nodes // 32)))
         moe_paged_plan(self.cfg, ctx_len, new_len, self.block_table, self.free_pages, self.free_head, step.q_start,
                        step.kv_len, step.positions, step.slot_map, self.ws, parents=parents,
                        tree_mask=step.tree_mask, stream=stream)
@@ -259,13 +272,17 @@ class PagedKVCache:
 
     def append(self, step: PagedStep, q, k, v, q_out=None, stream=None) -> torch.Tensor:
         """Rotated queries; the keys and values of the step are in the cache after it."""
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+        if q_out is None:
+            with _memory_of(stream, q.device):
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         moe_rope_append(self.cfg, q, k, v, step.positions, self.table, step.slot_map, self.k_cache, self.v_cache,
                         q_out, self.ws, rot_scale=self.rot_scale, stream=stream)
         return q_out
 
     def attend(self, step: PagedStep, q, out=None, lse=None, stream=None) -> torch.Tensor:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else out
+        if out is None:
+            with _memory_of(stream, q.device):
+                out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         moe_tree_attention(self.cfg, q, step.q_start, step.kv_len, self.block_table, self.k_cache, self.v_cache, out,
                            self.ws, tree_mask=step.tree_mask, lse=lse, stream=stream)
         return out

@@ -108,3 +108,33 @@ def test_no_node_is_lost_from_a_step_of_trees(new, T):
 def test_plan_writes_masks_wider_than_the_trees(ctx, new, kind, words):
     words = max(words, -(-max(new) // 32))
     assert run_plan(ctx, new, 16, kind=kind, words=words, T=sum(new) + 3, seed=7) == 0
+
+
+def test_steps_on_another_stream_take_memory_of_that_stream():
+    """Tensors that PagedKVCache makes for a call on a stream belong to it: memory of the
+    current stream may still be in use there, and may be given out again before the call ran."""
+    M = _m()
+    cfg = M.make_attn_config(2, 1, 16, page_size=16, n_pages=8, max_pages=4, dtype=M.MOE_DT_F32)
+    c = M.PagedKVCache(cfg, 1)
+    q, k, v = (torch.randn((40, h, 16), device="cuda") for h in (2, 1, 1))
+    ctx, new = _i32([0]), _i32([40])
+    want = c.attend(*(lambda s: (s, c.append(s, q, k, v)))(c.plan(ctx, new, 40)))
+    c.free_head.zero_()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+
+    def owner(t):                          # the stream that a tensor's memory was taken for
+        at = t.data_ptr()
+        return [s["stream"] for s in torch.cuda.memory_snapshot()
+                if s["address"] <= at < s["address"] + s["total_size"]]
+
+    for stream in (side, side.cuda_stream):
+        step = c.plan(ctx, new, 40, parents=_i32([-1] + list(range(39))), stream=stream)
+        rows = c.append(step, q, k, v, stream=stream)
+        out = c.attend(step, rows, stream=stream)
+        side.synchronize()
+        assert torch.equal(out, want) and _err(c.ws) == 0
+        c.free_head.zero_()
+        torch.cuda.synchronize()
+        for t in (step.q_start, step.kv_len, step.positions, step.slot_map, step.tree_mask, rows, out):
+            assert owner(t) == [side.cuda_stream]
