@@ -12,10 +12,11 @@ of T synthetic tokens.  Weights come in several seeded replicas that the steps
 rotate through, so no step finds the previous step's weights in L2.  Prints
 one JSON line (rank 0): the headline workload (Nano decode, T = 64) with its
 dominant kernel's roofline, the end-to-end figure through the host-buffer
-entry point and the oracle on the host cores, plus ``per_workload``: every
-workload at every token count it is defined for.  Multi-GPU (torchrun): every
-rank runs its own layer replica on its own tokens (no collective on the data
-path; weak scaling).
+entry point and the oracle on the host cores.  ``per_workload``, every workload
+at every token count it is defined for, is a JSON line of its own on stderr: at
+18 KB it made the line too long to be read from a log's tail.  Multi-GPU
+(torchrun): every rank runs its own layer replica on its own tokens (no
+collective on the data path; weak scaling).
 """
 from __future__ import annotations
 
@@ -58,7 +59,7 @@ def parse(argv=None):
     ap.add_argument("--replicas", type=int, default=0, help="weight replicas (0 = enough to defeat L2)")
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--points", default="all",
-                    help="per_workload entries: all, none, or one workload name")
+                    help="per_workload entries (on stderr): all, none, or one workload name")
     ap.add_argument("--eager", action="store_true", help="time eager calls instead of CUDA-graph replays")
     ap.add_argument("--no-backward", dest="backward", action="store_false",
                     help="skip the backward timings")
@@ -898,6 +899,13 @@ def roofline_entry(r, shape, T, pk):
 
 
 # ---------------------------------------------------------------------------
+def emit(line, detail=None):
+    """The one line on stdout; before it, what else was measured on stderr."""
+    if detail is not None:
+        print(json.dumps(detail), file=sys.stderr, flush=True)
+    print(json.dumps(line), flush=True)
+
+
 def main():
     args = parse()
     world = int(os.environ.get("WORLD_SIZE", "1"))
@@ -906,7 +914,7 @@ def main():
     if args.impl == "reference":
         line = run_reference(args, rank, world)
         if line is not None:
-            print(json.dumps(line), flush=True)
+            emit(line)
         return
     import torch
     if world > 1:
@@ -962,13 +970,13 @@ def main():
                     "api": "moe_layer_forward_host (pinned host x and y)"},
             "cpu_baseline": cpu,
         }
+        detail = None
         if r["per_workload"]:
-            line["per_workload"] = r["per_workload"]
-            line["per_workload_clocks"] = r["per_workload_clocks"]
-            line["per_workload_note"] = ("graph replays; bound = the larger ideal time (bytes at the measured copy "
-                                         "bandwidth, FLOPs at the burst bf16 peak); tensor fractions against both "
-                                         "the burst and the sustained measured bf16 peaks")
-        print(json.dumps(line), flush=True)
+            detail = {"per_workload": r["per_workload"], "per_workload_clocks": r["per_workload_clocks"],
+                      "per_workload_note": ("graph replays; bound = the larger ideal time (bytes at the measured copy "
+                                            "bandwidth, FLOPs at the burst bf16 peak); tensor fractions against both "
+                                            "the burst and the sustained measured bf16 peaks")}
+        emit(line, detail)
     if world > 1:
         torch.distributed.destroy_process_group()
 
