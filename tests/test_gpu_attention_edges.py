@@ -1,6 +1,7 @@
 """Paged attention where a step leaves the usual ranges: requests that outgrow their
-block-table row, trees of many nodes.  Against plain NumPy evaluations in 64 bits, with
-the tolerances derived in ``test_gpu_attention``."""
+block-table row, trees of many nodes, prompts of thousands of rows; steps on another
+stream and in a graph.  Against plain NumPy evaluations in 64 bits, with the tolerances
+derived in ``test_gpu_attention``."""
 import numpy as np
 import pytest
 import torch
@@ -138,3 +139,54 @@ def test_steps_on_another_stream_take_memory_of_that_stream():
         torch.cuda.synchronize()
         for t in (step.q_start, step.kv_len, step.positions, step.slot_map, step.tree_mask, rows, out):
             assert owner(t) == [side.cuda_stream]
+
+
+@pytest.mark.parametrize("ctx,new", [([0], [3000]), ([900, 0, 5], [1700, 1300, 400])])
+@pytest.mark.parametrize("D,G", [(128, 4), (64, 16)])
+def test_prompts_of_thousands_of_rows(ctx, new, D, G):
+    """Chains whose first row blocks see few of their request's keys: runs that see nothing
+    of a unit leave it as it is."""
+    s = Step(ctx, new, G, 1, D, 64, BF, tree=False, seed=23)
+    out, lse = s.run()
+    s.check(out, lse)
+    again, lse2 = s.run()
+    assert torch.equal(again, out) and torch.equal(lse2, lse)
+
+
+@pytest.mark.parametrize("tree", [False, True])
+def test_bf16_steps_in_one_graph(tree):
+    """plan -> append -> attend (both of its launches) captured at a fixed number of rows and
+    replayed over growing requests give what the calls give, bit for bit."""
+    M = _m()
+    H, Hkv, D, page, R, T = 8, 2, 128, 16, 3, 24
+    cfg = M.make_attn_config(H, Hkv, D, page_size=page, n_pages=120, max_pages=40, rot_dim=64)
+    g = torch.Generator("cuda").manual_seed(9)
+    parents = _i32([-1, 0, 0, 1, 3, 1] * 4) if tree else None
+    ctx, new = _i32([0, 130, 255]), _i32([6, 6, 6])
+    bufs = [torch.zeros((T, h, D), device="cuda", dtype=BF) for h in (H, Hkv, Hkv)]
+    lse = torch.empty((T, H), device="cuda")
+    caches = [M.PagedKVCache(cfg, R) for _ in range(2)]
+    rows = [torch.randn((385, h, D), generator=g, device="cuda").to(BF) for h in (H, Hkv, Hkv)]
+    for c in caches:                                         # what is cached before: 0, 130 and 255 tokens
+        c.append(c.plan(_i32([0] * R), ctx, 385), *rows)
+
+    def body(c):
+        step = c.plan(ctx, new, T, parents=parents)
+        return c.attend(step, c.append(step, *bufs), lse=lse)
+
+    graph = torch.cuda.CUDAGraph()
+    body(caches[0])                                          # warm-up; its pages go back
+    caches[0].release(ctx + new, ctx)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        out = body(caches[0])
+    for _ in range(6):
+        for b in bufs:
+            b.copy_(torch.randn(b.shape, generator=g, device="cuda"))
+        graph.replay()
+        got, got_l = out.clone(), lse.clone()
+        want = body(caches[1])
+        assert torch.equal(got, want) and torch.equal(got_l, lse)
+        assert bool((got[18:] == 0).all()) and bool(torch.isfinite(got.float()).all())
+        ctx.add_(6)
+    assert [_err(c.ws) for c in caches] == [0, 0]
