@@ -111,6 +111,12 @@ def test_plan_writes_masks_wider_than_the_trees(ctx, new, kind, words):
     assert run_plan(ctx, new, 16, kind=kind, words=words, T=sum(new) + 3, seed=7) == 0
 
 
+@pytest.mark.parametrize("R,rows,kind", [(16384, 3, "tree"), (16384, 2, None), (1200, 130, None)])
+def test_plan_of_the_most_requests(R, rows, kind):
+    """Every block sums the lengths of all requests: up to the most that a plan takes."""
+    assert run_plan([i % 50 for i in range(R)], [i % rows for i in range(R)], 16, kind=kind, seed=8) == 0
+
+
 def test_steps_on_another_stream_take_memory_of_that_stream():
     """Tensors that PagedKVCache makes for a call on a stream belong to it: memory of the
     current stream may still be in use there, and may be given out again before the call ran."""
