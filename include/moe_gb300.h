@@ -458,16 +458,21 @@ moe_status_t moe_paged_plan(const moe_attn_config_t* cfg, int32_t R, int32_t T, 
                             void* stream);
 
 /* Rotary frequencies as turns: entry i < rot_dim / 2 of the HOST table is
- * f_i / (2 pi) * 2^64, rounded, with f_i = theta^(-2i / rot_dim) radians a
- * position, so that position * entry mod 2^64 is the angle's fraction of a turn
- * exactly, however far the position.  Host arithmetic only; the caller copies
- * the table to the device once.
+ * f_i / (2 pi) * 2^64, made in FP64 (relative error 2^-51 at most), with
+ * f_i = theta^(-2i / rot_dim) radians a position.  position * entry mod 2^64 is
+ * the angle's fraction of a turn without further rounding, however far the
+ * position: the angle is off by at most 2^-51 position f_i radians from the table
+ * and, in the kernels, by 2^-33 turns and an FP32 rounding.  Host arithmetic only;
+ * the caller copies the table to the device once.
  *   scaling  MOE_ROPE_PLAIN; MOE_ROPE_LINEAR: f_i / factor; MOE_ROPE_YARN: the
  *            method of "YaRN: Efficient Context Window Extension of Large
  *            Language Models" (Peng et al., 2023): f_i / factor where a pair
  *            turns fewer than 1 time over original_context tokens, f_i where it
  *            turns more than 32 times, a ramp between, and *rot_scale =
- *            0.1 ln(factor) + 1 (otherwise 1)                                  */
+ *            0.1 ln(factor) + 1 (otherwise 1).  The ramp is linear in the pair's
+ *            index i, from low = max(floor(i32), 0) to high = min(ceil(i1),
+ *            rot_dim - 1) (at least 0.001 apart), where i32 and i1 are the indexes
+ *            at which a pair turns 32 times and once, as models are trained with */
 enum { MOE_ROPE_PLAIN = 0, MOE_ROPE_LINEAR = 1, MOE_ROPE_YARN = 2 };
 moe_status_t moe_rope_table(int32_t rot_dim, double theta, int32_t scaling, double factor,
                             int64_t original_context, uint64_t* table_host, float* rot_scale);

@@ -230,8 +230,9 @@ class PagedStep:
 
 class PagedKVCache:
     """One attention layer's paged KV cache: the pages, the requests' block
-    tables, the free pages and the workspace.  A step is plan -> append -> attend,
-    all on the current stream, nothing on the host.  A call that is given another
+    tables, the free pages and the workspace (``ws``, with the error word that
+    moe_get_device_error reads).  A step is plan -> append -> attend, all on the
+    current stream, nothing on the host.  A call that is given another
     stream makes its tensors from that stream's memory; they are used on a third one
     as any tensor is (after an event, with ``record_stream``)."""
 

@@ -10,9 +10,12 @@
 //
 // Work.  A unit's keys are tiles of 128.  The tiles of all units, in order, are
 // cut into equal runs, one per CTA (one CTA an SM): the lengths are read on the
-// device, no call needs them on the host, and every SM streams the same number
-// of keys whatever the batch.  A unit cut by a run's end leaves FP32 partials (at
-// most two a CTA) and a second small kernel adds them in run order.
+// device, no call needs them on the host, and with one row block a KV head (single
+// tokens, small trees) every SM streams the same number of keys whatever the batch.
+// A chain of several blocks (a prompt) is charged all of its request's tiles for each
+// of them, though a block sees only those up to its last node: runs over the first
+// blocks end early (figures below).  A unit cut by a run's end leaves FP32 partials
+// (at most two a CTA) and a second small kernel adds them in run order.
 //
 // Inside a CTA: warps 8 and 10 bring K and V tiles into a ring by TMA, a box per
 // page and 64-wide half (any page size from 8 on; the table's entries are fetched
@@ -24,19 +27,29 @@
 // as the A operand of P V; V is the MN-major B operand as it lies.  A row's two
 // threads exchange their maxima through shared memory.
 //
-// The reference m of a row follows its maximum only when that rose by more than
-// 2^8: below that p and the sums just grow by at most 2^8, exactly undone by the
-// division, and O is left alone.
+// The running maximum and sum are the online softmax of Milakov and Gimelshein
+// ("Online normalizer calculation for softmax", 2018), but the reference m of a row
+// follows its maximum only when that rose by more than 2^8: below that p and the sums
+// just grow by at most 2^8, which the division undoes, and O is left alone.
+//
+// P is rounded to BF16 for the second product (the tensor cores take one 16-bit type
+// for both operands, and V is BF16), at most half a step, 2^-8, of each p; l sums p
+// before it.  Against 64 bits the outputs are off by 1.7 to 2.3e-3 of their norm where
+// P in FP32 gives 1.5 to 1.7e-3, nearly all of that the store's own rounding.
 //
 // Bound and measures (GB300, 32 heads over 8 KV heads of 128 unless said): HBM
 // while a KV head's rows are few: one request of 262,001 tokens with 16 nodes
-// 165 us = 6.5 TB/s, 64 ragged requests of up to 8,000 tokens and trees of up to 8
-// 177 us = 5.9 TB/s (the mean CTA streams at 6.8).  With 128 rows a tile's chain
-// (scores ready, exponentials, P stored, maxima exchanged), about 1700 cycles where
-// its products need 1024: 32 requests with trees of up to 64 and 16 query heads a KV
-// head 89 us = 755 TFLOP/s.  The other split measured, tiles of 64 keys that the two
-// groups take in turn, each with its own reference and O and no exchange, doubles a
-// tile's fixed waits: 143 us there, 203 us for the long request.
+// 164 to 167 us = 6.4 to 6.6 TB/s, 64 ragged requests of up to 8,000 tokens and trees of
+// up to 8 176 to 185 us = 5.7 to 6.0 TB/s (the mean CTA streams at 6.8), of up to 16,000
+// tokens with heads of 64 253 us = 4.2 TB/s (a tile's bytes halve, its chain does not).
+// With 128 rows a tile's chain (scores ready, exponentials, P stored, maxima exchanged),
+// about 1700 cycles where its products need 1024: 32 requests with trees of up to 64 and
+// 16 query heads a KV head 88 to 94 us = 715 to 765 TFLOP/s, 2048 rows behind 8192 cached
+// tokens 355 us = 870.  Prompts: one of 8192 rows 1672 us = 329 TFLOP/s, four of 2048
+// 437 us = 315 (the busiest run has nearly twice the mean work).  The other split
+// measured, tiles of 64 keys that the two groups take in turn, each with its own
+// reference and O and no exchange, doubles a tile's fixed waits: 143 us for the large
+// trees, 203 us for the long request.
 //
 // Masked places.  Only the tiles that hold nodes or end past the last key look
 // at masks; there, V rows past the last key are zeroed in shared memory (P is 0,
@@ -62,7 +75,7 @@ constexpr int kLoaders = 2;                    // warps that issue the TMA copie
 constexpr int kQueue = 4;                      // pieces worked out ahead
 
 constexpr uint32_t kTmemCols = 512;
-constexpr float kRaise = 8.f;                  // log2 units by which a maximum may pass its reference
+constexpr float kRaise = 8.f;                  // log2 units by which a maximum may pass its reference (above)
 constexpr int kMaxSmem = 232448;
 
 template <int DP>
@@ -782,7 +795,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       };
-      // 32 probabilities, from the CC'th half of the scores
+      // 32 probabilities, from the CC'th half of the scores; summed before they are rounded to BF16 (above)
       auto exps = [&](auto CC, int b, float base) {
         constexpr int cc = decltype(CC)::value;
         const uint64_t c2 = pair(c, c), base2 = pair(-base, -base);

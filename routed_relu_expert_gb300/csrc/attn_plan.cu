@@ -7,8 +7,9 @@
 //   base_r = *free_head + sum_{s < r} more_s;  q_start_r = sum_{s < r} n_s
 //
 // One launch without a grid-wide wait: every block sums all R lengths itself
-// (8 R bytes, out of L2 after the first block) and so knows the prefix of its
-// own requests; nothing it needs is written by another block.  The one value
+// (8 R bytes, out of L2 after the first block) and so knows the prefix of its own
+// requests; nothing it needs is written by another block.  That cost grows with R
+// squared: a token for each of 2048 requests 5 us, 4096 11 us, 16384 95 us.  The one value
 // that all blocks read and one writes, *free_head (it may be updated in place),
 // is written by the block whose ticket says that every block has read it.
 //
@@ -16,7 +17,8 @@
 // takes a request's nodes, a lane a node.  The bound is the latency of the
 // dependent steps (lengths, table entry, slot), not bytes: 3.5 us
 // for one request, 4.5 us for 64 with trees of up to 16, 7.7 us for 2048 with trees
-// of up to 64 (1.6 MB; 9.7 us with a walk to the root for each node).
+// of up to 64 (1.6 MB; 9.7 us with a walk to the root for each node).  Trees of more
+// than 64 nodes do walk to the root, a dependent load a level.
 #include "attn.h"
 
 #include <algorithm>
@@ -277,7 +279,8 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
 
 cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t s) {
   // long requests (64 rows each on average): a block a request and, past 1024
-  // rows a request, several; else a warp a request
+  // rows a request, several; else a warp a request.  The mean is what the host
+  // knows: one long prompt among many single tokens is walked by one warp
   const int64_t per = a.R > 0 ? a.T / a.R : 0;
   if (per >= 64) {
     const unsigned y = (unsigned)std::min<int64_t>(std::max<int64_t>(per / 1024, 1), 32);

@@ -4,12 +4,14 @@
 //   angle = 2 pi frac(pos * F_i / 2^64),  F_i = round(f_i / (2 pi) * 2^64)
 //   (a, b) -> (a cos - b sin, a sin + b cos) * rot_scale
 //
-// The product pos * F_i mod 2^64 is the fraction of a turn exactly, in one
-// 64-bit integer multiply, however far the position (an FP32 product of a
-// position near 2^20 and a frequency near 1 is off by a twentieth of a
-// radian); its upper 32 bits, taken as a signed fraction of a turn in
-// [-1/2, 1/2), go to FP32 with a relative error of 2^-24.  Rows are turned in
-// FP32 and rounded once, on the store.
+// The product pos * F_i mod 2^64 is the fraction of a turn in one 64-bit integer
+// multiply that rounds nothing, however far the position (an FP32 product of a
+// position near 2^20 and a frequency near 1 is off by a twentieth of a radian).  What
+// the angle is off by: the table's entry, made in FP64, 2^-51 of pos * f / (2 pi) turns
+// at most; the cut to the upper 32 bits, a signed fraction of a turn in [-1/2, 1/2),
+// 2^-33 turns; their FP32 value, 2^-24 of it.  The cut is absolute: a sine of 1e-7 keeps
+// two digits, an error of 1e-9 beside the cosine's of 6e-8.  Rows are turned in FP32 and
+// rounded once, on the store.
 //
 // Bound: every row is read once and written once.  A thread owns one 16-byte piece
 // of one head and walks a block's tokens with it: where the piece lies is worked
@@ -19,7 +21,9 @@
 // that every load and store is of whole lines.  The angles of a block's tokens are
 // computed once for all of its pieces, into shared memory.  16384 BF16 tokens of
 // 32 + 2 x 8 heads of 128 (403 MB): 73 us with half of the head turned = 5.5 TB/s, 76
-// with all of it, 69 interleaved, 122 where 22 of 128 turn (pairs of single elements).
+// with all of it, 66 with none (a plain cache write), 69 interleaved, 122 where 22 of
+// 128 turn: a rotating part that is no whole number of pieces (of pairs of pieces in the
+// half layout) goes by single elements, 2-byte loads and stores.
 #include "attn.h"
 
 #include <algorithm>
