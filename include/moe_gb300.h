@@ -525,6 +525,130 @@ moe_status_t moe_tree_attention(const moe_attn_config_t* cfg, int32_t R, int32_t
                                 int32_t mask_words, void* out, int64_t out_ld, float* lse, void* ws, size_t ws_bytes,
                                 void* stream);
 
+/* ---- requests that share pages ---------------------------------------------
+ * Several requests may hold one page in their rows of the block table (samples
+ * of one prompt, a system prompt, beams).  page_shares[p] counts the holders of
+ * page p beyond its first: 0 for a page that one request holds and for a free one,
+ * so that moe_paged_plan, whose pages have one holder, need not know of it.  Only
+ * whole pages are shared; what a request writes next lies in a page of its own.
+ * That is the caller's to keep: cut a request (release) inside a page that others
+ * hold, and its next tokens would be theirs; fork it onto another row instead.   */
+
+/* Continues requests by others: fork i makes row dst_rows[i] of dst_table hold the
+ * first lengths[i] tokens of row src_rows[i] of src_table.  Its whole pages are
+ * shared (page_shares + 1 each, any number of forks of one row); the tokens of a
+ * partly filled last one are copied, K and V, into a page taken from the list of
+ * free ones, the forks' pages in ascending i.
+ *   n          forks, 0..4096;  src_rows, dst_rows, lengths [n] int32
+ *   src_table, dst_table [R, max_pages] int32, R 0..16384: one table, or two that
+ *              do not overlap (beams: the new step's rows from the old ones)
+ *   page_shares [n_pages] int32, in and out
+ *   free_pages [n_free], free_head, free_head_out: as in moe_paged_plan
+ * Written: entries 0 .. ceil(lengths[i] / page_size) - 1 of row dst_rows[i] (pages that
+ * it held before are not given back), the counts, the copied tokens.  A row is
+ * the destination of one fork and, within one table, no source: of forks that meet
+ * in a destination the first is done, one whose source is another's destination, or
+ * whose row or length is out of range, is not, with MOE_DEVERR_CACHE.  Such a fork
+ * still takes its page if its rows and length are in range.  Page ids outside the cache
+ * become -1 entries (MOE_DEVERR_CACHE); out of free pages: entry -1, MOE_DEVERR_PAGES.
+ * 2 * n_kv_heads * head_dim * page_size elements in pieces of 16 bytes must be below
+ * 2^31 (MOE_ERR_UNSUPPORTED).                                                     */
+moe_status_t moe_paged_fork(const moe_attn_config_t* cfg, int32_t n, const int32_t* src_rows, const int32_t* dst_rows,
+                            const int32_t* lengths, int32_t R, const int32_t* src_table, int32_t* dst_table,
+                            int32_t* page_shares, const int32_t* free_pages, int32_t n_free, const int32_t* free_head,
+                            int32_t* free_head_out, void* k_cache, void* v_cache, void* ws, size_t ws_bytes,
+                            void* stream);
+
+/* Moves the kept tokens of each request to the front, K and V, in place: of the
+ * tokens from first[r] on (the nodes of a step, say), number keep[keep_start[r] + i]
+ * goes to token first[r] + i.  The accepted path of a drafted tree (its nodes
+ * ascend), or what an eviction leaves of a context (first 0).
+ *   R          requests, 0..16384;  N: entries of keep
+ *   first [R], keep_start [R+1], keep [N] int32: ascending numbers, from 0, a request
+ *   page_shares [n_pages] int32 or NULL: where given, a shared page is not written to
+ *   len_out    [R] int32 out or NULL: first + number of kept tokens
+ * Kept numbers that do not ascend, tokens past the table's row, pages outside the
+ * cache and shared pages that would be written: the token is not moved, with
+ * MOE_DEVERR_CACHE (so is a request whose keep_start or first is out of range left
+ * as it is, with len_out = max(first, 0)).  The pages stay the request's; the ones behind the
+ * kept tokens go back with moe_paged_release.                                      */
+moe_status_t moe_paged_compact(const moe_attn_config_t* cfg, int32_t R, int32_t N, const int32_t* first,
+                               const int32_t* keep_start, const int32_t* keep, const int32_t* block_table,
+                               const int32_t* page_shares, int32_t* len_out, void* k_cache, void* v_cache, void* ws,
+                               size_t ws_bytes, void* stream);
+
+/* Gives pages back: those that request r holds for its first held_len[r] tokens but
+ * not for its first keep_len[r] (a rejected part of a draft; 0: a finished request).
+ * A page that others hold loses a holder; one that is left without any goes back to
+ * the list, before free_pages[*free_head], in the table's order (where several
+ * rows give one up in this call, at the last of them).
+ *   R          requests, 0..16384, R * max_pages < 2^31
+ *   held_len, keep_len [R] int32;  block_table [R, max_pages] int32: entries given
+ *              back become -1
+ *   page_shares [n_pages] int32, in and out, or NULL: no page is shared
+ *   free_pages [n_free] int32, free_head [1] int32, in and out
+ * Entries -1 are passed over.  Negative lengths (count as 0), page ids outside the
+ * cache, a page given back more often than it is held, and more pages than the list
+ * gave out (the first ones are dropped): MOE_DEVERR_CACHE.                          */
+moe_status_t moe_paged_release(const moe_attn_config_t* cfg, int32_t R, const int32_t* held_len,
+                               const int32_t* keep_len, int32_t* block_table, int32_t* page_shares,
+                               int32_t* free_pages, int32_t n_free, int32_t* free_head, void* ws, size_t ws_bytes,
+                               void* stream);
+
+/* moe_tree_attention for requests in groups with a common prefix: its pages are
+ * attended once for all rows of the group, the requests' other tokens by themselves,
+ * and a row's two parts joined (FP32 partial sums, maxima and exponential sums).
+ *   n_groups   groups, 0..R (R 0..2048);  group_start [n_groups+1] int32, ascending:
+ *              group g is requests group_start[g] .. group_start[g+1] - 1; requests
+ *              before the first and behind the last group share nothing
+ *   prefix_row [n_groups] int32: the block-table row (any of the R) that the prefix
+ *              is read through
+ *   prefix_len [n_groups] int32: the common tokens.  Their whole pages are
+ *              attended once; a partly filled last one through each request's own row
+ *   ws         moe_prefix_workspace_bytes(cfg, T)
+ * The others as in moe_tree_attention; a request's tokens are counted from its
+ * context's start as there, prefix included.  A request whose context (kv_len
+ * without its nodes) is shorter than the prefix's whole pages, and a group of fewer
+ * than two requests, are attended through their own rows alone.  Bad groups (bounds
+ * or rows out of range, not ascending, a prefix past the table's row):
+ * MOE_DEVERR_CACHE, and they share nothing.  (2 T + R + n_groups) * Hkv *
+ * (ceil(max_pages * page_size / 128) + 5) and 32 * T * H must stay below 2^31.
+ * FP32 reads the prefix through prefix_row for each row by itself.                  */
+size_t moe_prefix_workspace_bytes(const moe_attn_config_t* cfg, int32_t T);
+moe_status_t moe_prefix_attention(const moe_attn_config_t* cfg, int32_t R, int32_t T, const void* q, int64_t q_ld,
+                                  const int32_t* q_start, const int32_t* kv_len, const int32_t* block_table,
+                                  int32_t n_groups, const int32_t* group_start, const int32_t* prefix_row,
+                                  const int32_t* prefix_len, const void* k_cache, const void* v_cache,
+                                  const int32_t* tree_mask, int32_t mask_words, void* out, int64_t out_ld, float* lse,
+                                  void* ws, size_t ws_bytes, void* stream);
+
+/* ---- rotary positions with several axes -------------------------------------
+ * A token of an image or a video has a position on each of a few axes (time,
+ * height, width); every rotating pair turns by the position of one of them, text
+ * tokens having the same position on all.  moe_rope_axes_table makes the pairs' axes
+ * and frequencies on the HOST: sections[a] pairs belong to axis a (their sum is
+ * rot_dim / 2), in one piece after another, or (interleaved) dealt out one
+ * at a time to the axes that have pairs left.  One ladder of frequencies,
+ * theta^(-2i / rot_dim) for pair i, or (own_ladders) one for each axis,
+ * theta^(-j / sections[a]) for its j-th pair; scaling as in moe_rope_table.
+ *   table_host [rot_dim / 2] uint64, axis_host [rot_dim / 2] uint8 out
+ * moe_rope_axes and moe_rope_append_axes are moe_rope and moe_rope_append with
+ *   n_axes     1..4;  positions [n_axes, T] int32
+ *   axis       [rot_dim / 2] uint8 on the device (NULL if rot_dim is 0); a number
+ *              past the last axis counts as the last                                */
+#define MOE_ROPE_MAX_AXES 4
+moe_status_t moe_rope_axes_table(int32_t n_axes, const int32_t* sections, int32_t interleaved, int32_t own_ladders,
+                                 double theta, int32_t scaling, double factor, int64_t original_context,
+                                 uint64_t* table_host, uint8_t* axis_host, float* rot_scale);
+moe_status_t moe_rope_axes(const moe_attn_config_t* cfg, int32_t T, int32_t heads, const void* x, int64_t x_ld,
+                           int32_t n_axes, const int32_t* positions, const uint8_t* axis, const uint64_t* table,
+                           float rot_scale, int32_t inverse, void* out, int64_t out_ld, void* stream);
+moe_status_t moe_rope_append_axes(const moe_attn_config_t* cfg, int32_t T, const void* q, int64_t q_ld,
+                                  const void* k, int64_t k_ld, const void* v, int64_t v_ld, int32_t n_axes,
+                                  const int32_t* positions, const uint8_t* axis, const uint64_t* table,
+                                  float rot_scale, const int64_t* slot_map, void* q_out, int64_t q_out_ld,
+                                  void* k_cache, void* v_cache, void* ws, size_t ws_bytes, void* stream);
+
 /* Synchronises `stream`, copies the device error word of `ws` to *code (host
  * pointer) and returns MOE_ERR_DEVICE if any bit is set, else MOE_OK.         */
 moe_status_t moe_get_device_error(const void* ws, void* stream, int32_t* code);

@@ -17,6 +17,7 @@ MOE_DEVERR_EXPERT_ID, MOE_DEVERR_NONFINITE, MOE_DEVERR_SCHEDULE, MOE_DEVERR_TIME
 MOE_DEVERR_PAGES, MOE_DEVERR_CACHE = 32, 64
 MOE_ATTN_HEADER_BYTES = 4096
 MOE_ROPE_PLAIN, MOE_ROPE_LINEAR, MOE_ROPE_YARN = 0, 1, 2
+MOE_ROPE_MAX_AXES = 4
 MOE_DT_F32, MOE_DT_BF16, MOE_DT_NVFP4 = 0, 1, 2
 MOE_NOALLOC_MAX_ROUTER_ELEMS = 131072
 MOE_NOALLOC_MAX_SPLIT_ELEMS = 7340032
@@ -82,7 +83,8 @@ EXPORTS = (
     "moe_nvfp4_act_terms_for", "moe_block_forward", "moe_sparse_down_bytes", "moe_sparse_down_layout",
     "moe_backward_workspace_bytes", "moe_layer_backward", "moe_block_backward", "moe_backward_workspace_region",
     "moe_check_attn_config", "moe_attn_workspace_bytes", "moe_paged_plan", "moe_rope_table", "moe_rope",
-    "moe_rope_append", "moe_tree_attention",
+    "moe_rope_append", "moe_tree_attention", "moe_paged_fork", "moe_paged_compact", "moe_paged_release",
+    "moe_prefix_workspace_bytes", "moe_prefix_attention", "moe_rope_axes_table", "moe_rope_axes", "moe_rope_append_axes",
 )
 
 _lib = None
@@ -141,6 +143,15 @@ def load() -> ctypes.CDLL:
         "moe_rope": (I32, [ACFG, I32, I32, P, I64, P, P, F, I32, P, I64, P]),
         "moe_rope_append": (I32, [ACFG, I32, P, I64, P, I64, P, I64, P, P, F, P, P, I64, P, P, P, S, P]),
         "moe_tree_attention": (I32, [ACFG, I32, I32, P, I64, P, P, P, P, P, P, I32, P, I64, P, P, S, P]),
+        "moe_paged_fork": (I32, [ACFG, I32, P, P, P, I32, P, P, P, P, I32, P, P, P, P, P, S, P]),
+        "moe_paged_compact": (I32, [ACFG, I32, I32, P, P, P, P, P, P, P, P, P, S, P]),
+        "moe_paged_release": (I32, [ACFG, I32, P, P, P, P, P, I32, P, P, S, P]),
+        "moe_prefix_workspace_bytes": (S, [ACFG, I32]),
+        "moe_prefix_attention": (I32, [ACFG, I32, I32, P, I64, P, P, P, I32, P, P, P, P, P, P, I32, P, I64, P, P, S, P]),
+        "moe_rope_axes_table": (I32, [I32, P, I32, I32, ctypes.c_double, I32, ctypes.c_double, I64, P, P,
+                                      ctypes.POINTER(F)]),
+        "moe_rope_axes": (I32, [ACFG, I32, I32, P, I64, I32, P, P, P, F, I32, P, I64, P]),
+        "moe_rope_append_axes": (I32, [ACFG, I32, P, I64, P, I64, P, I64, I32, P, P, P, F, P, P, I64, P, P, P, S, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)

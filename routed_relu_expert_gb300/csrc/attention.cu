@@ -43,6 +43,9 @@ __device__ __forceinline__ int request_of(const int32_t* q_start, int R, int t) 
   return lo;
 }
 
+// SHARED: the tokens of a group's prefix are read through the group's row of the table (every row of the group by
+// itself: the pages come from memory once and from L2 after that)
+template <bool SHARED>
 __global__ void __launch_bounds__(kThreads) attention_f32_kernel(const AttnArgs a, int groups, int splits) {
   pdl_wait();
   __shared__ __align__(16) float s_q[kHeads][kAttnPartDim];
@@ -76,6 +79,12 @@ __global__ void __launch_bounds__(kThreads) attention_f32_kernel(const AttnArgs 
     o[h] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
   const int dl = lane * 4;                     // this lane's piece of the head
+  if (SHARED && blockIdx.x == 0)
+    for (int g = tid; g < a.n_groups; g += kThreads) {
+      int no_group = 0;
+      prefix_group(a.group_start, a.prefix_row, a.prefix_len, g, a.R, a.max_pages, a.page_shift, &no_group);
+      if (no_group) bad = MOE_DEVERR_CACHE;
+    }
   if (r < a.R) {
     const int q0 = a.q_start[r], n = a.q_start[r + 1] - q0, node = t - q0;
     const int64_t cap = (int64_t)a.max_pages << a.page_shift;
@@ -85,6 +94,19 @@ __global__ void __launch_bounds__(kThreads) attention_f32_kernel(const AttnArgs 
     const int ctx = (int)min((int64_t)max(len, n) - n, cap);
     const int kv = (int)min((int64_t)ctx + n, cap);
     const int32_t* table = a.block_table + (int64_t)r * a.max_pages;
+    const int32_t* table0 = table;             // of the first `shared` pages
+    int shared = 0;
+    if (SHARED) {
+      const int g = group_of(a.group_start, a.n_groups, r);
+      if (g >= 0) {
+        const PrefixGroup p = prefix_group(a.group_start, a.prefix_row, a.prefix_len, g, a.R, a.max_pages, a.page_shift,
+                                           nullptr);
+        if (r < p.end && ctx >= (int64_t)p.pages << a.page_shift) {
+          table0 = a.block_table + (int64_t)p.row * a.max_pages;
+          shared = p.pages;
+        }
+      }
+    }
     const int32_t* mask = a.tree_mask ? a.tree_mask + (int64_t)t * a.mask_words : nullptr;
     const int tiles = (kv + 31) / 32;
     const int w0 = (int)((int64_t)tiles * split / splits), w1 = (int)((int64_t)tiles * (split + 1) / splits);
@@ -99,7 +121,8 @@ __global__ void __launch_bounds__(kThreads) attention_f32_kernel(const AttnArgs 
       int64_t at = 0;
       bool zero = false;                       // a page outside the cache reads as zeros
       if (see) {
-        const int page = table[key >> a.page_shift];
+        const int at_page = key >> a.page_shift;
+        const int page = SHARED && at_page < shared ? table0[at_page] : table[at_page];
         zero = page < 0 || page >= a.n_pages;
         if (zero) bad = MOE_DEVERR_CACHE;
         else
@@ -254,7 +277,8 @@ __global__ void __launch_bounds__(kThreads) attention_f32_kernel(const AttnArgs 
 // Splits: of at least 128 keys each if the tables' rows are full (a tile for each
 // of the four warps), at most 32, while the grid is under two blocks an SM and the
 // workspace holds their counters and partials.
-cudaError_t launch_attention_f32(const AttnArgs& a, cudaStream_t s) {
+template <bool SHARED>
+static cudaError_t launch_f32(const AttnArgs& a, cudaStream_t s) {
   if (a.T <= 0) return cudaSuccess;
   const int groups = (a.G + kHeads - 1) / kHeads;
   const int64_t units = (int64_t)a.T * a.Hkv * groups;
@@ -264,8 +288,11 @@ cudaError_t launch_attention_f32(const AttnArgs& a, cudaStream_t s) {
     const int64_t keys = (int64_t)a.max_pages << a.page_shift;
     splits = std::max<int64_t>(1, std::min<int64_t>({32, 4 * kAttnMaxCtas / units, room, ceil_div(keys, 128)}));
   }
-  launch_k(attention_f32_kernel, dim3((unsigned)(units * splits)), kThreads, 0, s, a, groups, (int)splits);
+  launch_k(attention_f32_kernel<SHARED>, dim3((unsigned)(units * splits)), kThreads, 0, s, a, groups, (int)splits);
   return cudaGetLastError();
 }
+
+cudaError_t launch_attention_f32(const AttnArgs& a, cudaStream_t s) { return launch_f32<false>(a, s); }
+cudaError_t launch_prefix_attention_f32(const AttnArgs& a, cudaStream_t s) { return launch_f32<true>(a, s); }
 
 }  // namespace moe

@@ -1,5 +1,5 @@
 // Shared declarations of the paged-attention operators (plan, rotary positions
-// with the cache write, tree attention).
+// with the cache write, tree attention, pages that requests share).
 #pragma once
 
 #include "internal.h"
@@ -27,6 +27,7 @@ constexpr int kAttnPartDim = 128;
 // us beside 0.8 to 1.2 us a tile.  Cost 2, 3, 4, 5 measured on large trees over short
 // and long contexts: 110, 97, 92, 92 us; flat for 64 requests of up to 8,000 tokens.
 constexpr int kAttnPieceCost = 4;
+constexpr int kPrefixMaxRequests = 2048;   // of a call with shared prefixes (and as many groups)
 constexpr size_t kAttnPartSlots = 2 * kAttnMaxCtas;
 constexpr size_t kAttnPartBytes = kAttnPartSlots * kAttnRows * (kAttnPartDim + 2) * 4;
 constexpr size_t kAttnJoinBytes = kAttnMaxCtas * 16;   // a record a run: what the join kernel adds
@@ -44,6 +45,38 @@ struct PlanArgs {
 };
 cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t s);
 
+struct ForkArgs {
+  const int32_t *src, *dst, *lengths;
+  const int32_t* src_table;
+  int32_t *dst_table, *shares;
+  const int32_t *free_pages, *free_head;
+  int32_t* free_head_out;
+  uint8_t *k, *v;
+  AttnHeader* hdr;
+  int64_t page_stride, token_stride, head_stride;   // bytes
+  int n, R, n_free, n_pages, max_pages, page_shift, Hkv, row_bytes, same;   // same: one table
+};
+cudaError_t launch_fork(const ForkArgs& a, cudaStream_t s);
+
+struct CompactArgs {
+  const int32_t *first, *keep_start, *keep, *block_table, *shares;
+  int32_t* len_out;
+  uint8_t *k, *v;
+  AttnHeader* hdr;
+  int64_t page_stride, token_stride, head_stride;   // bytes
+  int R, N, n_pages, max_pages, page_shift, Hkv, row_bytes;
+};
+cudaError_t launch_compact(const CompactArgs& a, cudaStream_t s);
+
+struct ReleaseArgs {
+  const int32_t *held_len, *keep_len;
+  int32_t *block_table, *shares, *free_pages, *free_head;
+  int32_t* last;            // [n_pages] the last entry that gives a page back (scratch)
+  AttnHeader* hdr;
+  int R, n_free, n_pages, max_pages, page_shift;
+};
+cudaError_t launch_release(const ReleaseArgs& a, cudaStream_t s);
+
 // rows of `heads` heads that one launch turns (or, rot 0, copies)
 struct RopeRows {
   const void* src;
@@ -55,14 +88,15 @@ struct RopeRows {
 struct RopeArgs {
   RopeRows part[3];
   int n_parts;
-  const int32_t* positions;
+  const int32_t* positions;          // [axes][T]
+  const uint8_t* axis;               // of each pair; NULL: one axis
   const uint64_t* table;
   const int64_t* slot_map;
   AttnHeader* hdr;
   int64_t n_slots;
   int64_t page_stride, token_stride, head_stride;
   float scale;
-  int T, D, rot, inverse, page_shift;
+  int T, D, rot, inverse, page_shift, n_axes;
 };
 cudaError_t launch_rope(const RopeArgs& a, int dtype, int interleaved, cudaStream_t s);
 
@@ -79,10 +113,51 @@ struct AttnArgs {
   int64_t q_ld, out_ld, page_stride, token_stride, head_stride;
   float scale;
   int R, T, H, Hkv, G, D, n_pages, max_pages, page_shift, mask_words;
+  // shared prefixes (n_groups 0: none)
+  const int32_t *group_start, *prefix_row, *prefix_len;
+  int n_groups;
+  float* rows_part;         // [prefix or own][KV head][columns / 4][T * G rows][4]: output sums of whole units
+  float2* rows_ml;          // [prefix or own][KV head][T * G rows] their (max, sum)
+  int4* parts_of;           // [prefix or own][KV head][T]: where a token's partials are (PartsOf)
 };
+
+// A group of requests that share a prefix: its tokens, whole pages of them, are read through one row of the table.
+struct PrefixGroup {
+  int begin, end, row, pages;
+};
+// group g, empty and without pages where its entries are no good; *bad is set then
+__device__ __forceinline__ PrefixGroup prefix_group(const int32_t* start, const int32_t* row, const int32_t* len, int g,
+                                                    int R, int max_pages, int page_shift, int* bad) {
+  PrefixGroup p;
+  p.begin = start[g];
+  p.end = start[g + 1];
+  p.row = row[g];
+  const int n = len[g];
+  p.pages = min(max(n, 0) >> page_shift, max_pages);
+  if (p.begin < 0 || p.end < p.begin || p.end > R || p.row < 0 || p.row >= R || n < 0 || n >> page_shift > max_pages) {
+    if (bad) *bad = 1;
+    p.begin = p.end = p.row = p.pages = 0;
+  }
+  if (p.end - p.begin < 2) p.pages = 0;        // nobody to share with
+  return p;
+}
+// group of request r: the last that begins at or before it (its end is the caller's to check); -1: none
+__device__ __forceinline__ int group_of(const int32_t* start, int n_groups, int r) {
+  if (n_groups == 0 || start[0] > r) return -1;
+  int lo = 0, hi = n_groups;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (start[mid] <= r) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
 // one warp a key range, FP32 arithmetic on the CUDA cores (FP32 layers)
 cudaError_t launch_attention_f32(const AttnArgs& a, cudaStream_t s);
 // tensor cores (BF16)
 cudaError_t launch_attention_bf16(const AttnArgs& a, cudaStream_t s);
+// the same with shared prefixes
+cudaError_t launch_prefix_attention_f32(const AttnArgs& a, cudaStream_t s);
+cudaError_t launch_prefix_attention_bf16(const AttnArgs& a, cudaStream_t s);
 
 }  // namespace moe

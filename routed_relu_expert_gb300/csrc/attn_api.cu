@@ -10,6 +10,7 @@ namespace {
 
 constexpr int kMaxPlanRequests = 16384;
 constexpr int kMaxRequests = 4096;
+constexpr int kMaxForks = 4096;
 constexpr int kMaxRows = 1 << 24;
 
 inline bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
@@ -52,7 +53,18 @@ bool bad_array(const T* p) {
   return !p || !aligned(p, sizeof(T));
 }
 
+// rows of a cache: 16-byte pieces
+inline bool bad_caches(const void* k, const void* v) {
+  return !k || !v || !aligned(k, 16) || !aligned(v, 16) || k == v;
+}
+
 constexpr size_t kWorkspaceBytes = MOE_ATTN_HEADER_BYTES + kAttnPartBytes + kAttnJoinBytes;
+
+// of a configuration: moe_paged_release has a word a page where attention has its partials
+size_t workspace_bytes(const moe_attn_config_t* c) {
+  const size_t pages = (MOE_ATTN_HEADER_BYTES + (size_t)c->n_pages * 4 + 15) / 16 * 16;
+  return pages > kWorkspaceBytes ? pages : kWorkspaceBytes;
+}
 
 moe_status_t check_ws(const void* ws, size_t ws_bytes) {
   if (!ws || !aligned(ws, 16)) return MOE_ERR_INVALID_ARG;
@@ -63,6 +75,20 @@ int log2_of(int v) {
   int s = 0;
   while ((1 << s) < v) ++s;
   return s;
+}
+
+// the partials of a call with shared prefixes, behind the workspace of the other calls (bytes)
+struct PrefixLayout {
+  size_t part, ml, parts_of, end;
+};
+PrefixLayout prefix_layout(const moe_attn_config_t* c, int64_t T) {
+  const size_t rows = (size_t)T * c->n_heads, dp = c->head_dim <= 64 ? 64 : 128;
+  PrefixLayout l;
+  l.part = (workspace_bytes(c) + 255) / 256 * 256;
+  l.ml = l.part + 2 * rows * dp * 4;
+  l.parts_of = l.ml + 2 * rows * 8;
+  l.end = l.parts_of + 2 * (size_t)T * c->n_kv_heads * 16;
+  return l;
 }
 
 moe_status_t launched(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
@@ -76,7 +102,7 @@ extern "C" {
 moe_status_t moe_check_attn_config(const moe_attn_config_t* cfg) { return check_config(cfg); }
 
 size_t moe_attn_workspace_bytes(const moe_attn_config_t* cfg) {
-  return check_config(cfg) == MOE_OK ? kWorkspaceBytes : 0;
+  return check_config(cfg) == MOE_OK ? workspace_bytes(cfg) : 0;
 }
 
 moe_status_t moe_paged_plan(const moe_attn_config_t* cfg, int32_t R, int32_t T, const int32_t* ctx_len,
@@ -152,9 +178,14 @@ moe_status_t moe_rope_table(int32_t rot_dim, double theta, int32_t scaling, doub
   return MOE_OK;
 }
 
-moe_status_t moe_rope(const moe_attn_config_t* cfg, int32_t T, int32_t heads, const void* x, int64_t x_ld,
-                      const int32_t* positions, const uint64_t* table, float rot_scale, int32_t inverse, void* out,
-                      int64_t out_ld, void* stream) {
+}  // extern "C"
+
+namespace {
+
+// positions [n_axes][T] and the pairs' axes (axis NULL: one axis)
+moe_status_t rope_rows(const moe_attn_config_t* cfg, int32_t T, int32_t heads, const void* x, int64_t x_ld,
+                       const int32_t* positions, int32_t n_axes, const uint8_t* axis, const uint64_t* table,
+                       float rot_scale, int32_t inverse, void* out, int64_t out_ld, void* stream) {
   CHECK(check_config(cfg));
   if (T < 0 || heads < 1 || heads > 65536 || (inverse != 0 && inverse != 1) || !std::isfinite(rot_scale))
     return MOE_ERR_INVALID_ARG;
@@ -167,6 +198,8 @@ moe_status_t moe_rope(const moe_attn_config_t* cfg, int32_t T, int32_t heads, co
   a.part[0] = RopeRows{x, out, x_ld, out_ld, heads, 1, 0};
   a.n_parts = 1;
   a.positions = positions;
+  a.n_axes = n_axes;
+  a.axis = axis;
   a.table = table;
   a.scale = rot_scale;
   a.T = T;
@@ -176,11 +209,11 @@ moe_status_t moe_rope(const moe_attn_config_t* cfg, int32_t T, int32_t heads, co
   return launched(launch_rope(a, cfg->dtype, cfg->rope_interleaved, (cudaStream_t)stream));
 }
 
-moe_status_t moe_rope_append(const moe_attn_config_t* cfg, int32_t T, const void* q, int64_t q_ld, const void* k,
-                             int64_t k_ld, const void* v, int64_t v_ld, const int32_t* positions,
-                             const uint64_t* table, float rot_scale, const int64_t* slot_map, void* q_out,
-                             int64_t q_out_ld, void* k_cache, void* v_cache, void* ws, size_t ws_bytes,
-                             void* stream) {
+moe_status_t rope_append(const moe_attn_config_t* cfg, int32_t T, const void* q, int64_t q_ld, const void* k,
+                         int64_t k_ld, const void* v, int64_t v_ld, const int32_t* positions, int32_t n_axes,
+                         const uint8_t* axis, const uint64_t* table, float rot_scale, const int64_t* slot_map,
+                         void* q_out, int64_t q_out_ld, void* k_cache, void* v_cache, void* ws, size_t ws_bytes,
+                         void* stream) {
   CHECK(check_config(cfg));
   CHECK(check_cache(cfg));
   if (T < 0 || !std::isfinite(rot_scale)) return MOE_ERR_INVALID_ARG;
@@ -192,8 +225,7 @@ moe_status_t moe_rope_append(const moe_attn_config_t* cfg, int32_t T, const void
       bad_rows(cfg, q_out, q_out_ld, H, T))
     return MOE_ERR_INVALID_ARG;
   if (q == q_out && q_ld != q_out_ld) return MOE_ERR_INVALID_ARG;
-  if (!k_cache || !v_cache || !aligned(k_cache, 16) || !aligned(v_cache, 16) || k_cache == v_cache)
-    return MOE_ERR_INVALID_ARG;
+  if (bad_caches(k_cache, v_cache)) return MOE_ERR_INVALID_ARG;
   if (bad_array(slot_map)) return MOE_ERR_INVALID_ARG;
   if (cfg->rot_dim > 0 && (bad_array(positions) || bad_array(table))) return MOE_ERR_INVALID_ARG;
   RopeArgs a{};
@@ -202,6 +234,8 @@ moe_status_t moe_rope_append(const moe_attn_config_t* cfg, int32_t T, const void
   a.part[2] = RopeRows{v, v_cache, v_ld, 0, Hkv, 0, 1};
   a.n_parts = 3;
   a.positions = positions;
+  a.n_axes = n_axes;
+  a.axis = axis;
   a.table = table;
   a.slot_map = slot_map;
   a.hdr = reinterpret_cast<AttnHeader*>(ws);
@@ -217,27 +251,99 @@ moe_status_t moe_rope_append(const moe_attn_config_t* cfg, int32_t T, const void
   return launched(launch_rope(a, cfg->dtype, cfg->rope_interleaved, (cudaStream_t)stream));
 }
 
-moe_status_t moe_tree_attention(const moe_attn_config_t* cfg, int32_t R, int32_t T, const void* q, int64_t q_ld,
-                                const int32_t* q_start, const int32_t* kv_len, const int32_t* block_table,
-                                const void* k_cache, const void* v_cache, const int32_t* tree_mask,
-                                int32_t mask_words, void* out, int64_t out_ld, float* lse, void* ws, size_t ws_bytes,
-                                void* stream) {
+moe_status_t check_axes(const moe_attn_config_t* cfg, int32_t n_axes, const uint8_t* axis) {
   CHECK(check_config(cfg));
-  CHECK(check_cache(cfg));
-  if (R < 0 || T < 0 || (tree_mask && mask_words < 1)) return MOE_ERR_INVALID_ARG;
-  const int64_t tiles = ((int64_t)cfg->max_pages * cfg->page_size + 127) / 128 + 1 + kAttnPieceCost;
-  if (R > kMaxRequests || T > kMaxRows || (int64_t)T * cfg->n_heads * 32 >= ((int64_t)1 << 31) ||
-      ((int64_t)T + R) * cfg->n_kv_heads * tiles >= ((int64_t)1 << 31))
-    return MOE_ERR_UNSUPPORTED;
-  CHECK(check_ws(ws, ws_bytes));
-  if (T == 0) return MOE_OK;
+  return n_axes < 1 || n_axes > MOE_ROPE_MAX_AXES || (cfg->rot_dim > 0 && !axis) ? MOE_ERR_INVALID_ARG : MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status_t moe_rope(const moe_attn_config_t* cfg, int32_t T, int32_t heads, const void* x, int64_t x_ld,
+                      const int32_t* positions, const uint64_t* table, float rot_scale, int32_t inverse, void* out,
+                      int64_t out_ld, void* stream) {
+  return rope_rows(cfg, T, heads, x, x_ld, positions, 1, nullptr, table, rot_scale, inverse, out, out_ld, stream);
+}
+
+moe_status_t moe_rope_append(const moe_attn_config_t* cfg, int32_t T, const void* q, int64_t q_ld, const void* k,
+                             int64_t k_ld, const void* v, int64_t v_ld, const int32_t* positions,
+                             const uint64_t* table, float rot_scale, const int64_t* slot_map, void* q_out,
+                             int64_t q_out_ld, void* k_cache, void* v_cache, void* ws, size_t ws_bytes,
+                             void* stream) {
+  return rope_append(cfg, T, q, q_ld, k, k_ld, v, v_ld, positions, 1, nullptr, table, rot_scale, slot_map, q_out,
+                     q_out_ld, k_cache, v_cache, ws, ws_bytes, stream);
+}
+
+moe_status_t moe_rope_axes_table(int32_t n_axes, const int32_t* sections, int32_t interleaved, int32_t own_ladders,
+                                 double theta, int32_t scaling, double factor, int64_t original_context,
+                                 uint64_t* table_host, uint8_t* axis_host, float* rot_scale) {
+  if (n_axes < 1 || n_axes > MOE_ROPE_MAX_AXES || !sections || (interleaved != 0 && interleaved != 1) ||
+      (own_ladders != 0 && own_ladders != 1) || !rot_scale)
+    return MOE_ERR_INVALID_ARG;
+  int half = 0, most = 0;
+  for (int a = 0; a < n_axes; ++a) {
+    if (sections[a] < 0 || sections[a] > 64) return MOE_ERR_INVALID_ARG;
+    half += sections[a];
+    most = sections[a] > most ? sections[a] : most;
+  }
+  if (half > 64 || (half > 0 && (bad_array(table_host) || !axis_host))) return MOE_ERR_INVALID_ARG;
+  // one ladder of frequencies over all pairs, or one over each axis's pairs
+  uint64_t ladder[MOE_ROPE_MAX_AXES][64];
+  for (int a = 0; a < (own_ladders ? n_axes : 1); ++a)
+    CHECK(moe_rope_table(2 * (own_ladders ? sections[a] : half), theta, scaling, factor, original_context, ladder[a],
+                         rot_scale));
+  int i = 0;
+  auto deal = [&](int a, int j) {
+    axis_host[i] = (uint8_t)a;
+    table_host[i] = own_ladders ? ladder[a][j] : ladder[0][i];
+    ++i;
+  };
+  if (interleaved) {
+    for (int j = 0; j < most; ++j)
+      for (int a = 0; a < n_axes; ++a)
+        if (j < sections[a]) deal(a, j);
+  } else {
+    for (int a = 0; a < n_axes; ++a)
+      for (int j = 0; j < sections[a]; ++j) deal(a, j);
+  }
+  return MOE_OK;
+}
+
+moe_status_t moe_rope_axes(const moe_attn_config_t* cfg, int32_t T, int32_t heads, const void* x, int64_t x_ld,
+                           int32_t n_axes, const int32_t* positions, const uint8_t* axis, const uint64_t* table,
+                           float rot_scale, int32_t inverse, void* out, int64_t out_ld, void* stream) {
+  CHECK(check_axes(cfg, n_axes, axis));
+  return rope_rows(cfg, T, heads, x, x_ld, positions, n_axes, axis, table, rot_scale, inverse, out, out_ld, stream);
+}
+
+moe_status_t moe_rope_append_axes(const moe_attn_config_t* cfg, int32_t T, const void* q, int64_t q_ld,
+                                  const void* k, int64_t k_ld, const void* v, int64_t v_ld, int32_t n_axes,
+                                  const int32_t* positions, const uint8_t* axis, const uint64_t* table,
+                                  float rot_scale, const int64_t* slot_map, void* q_out, int64_t q_out_ld,
+                                  void* k_cache, void* v_cache, void* ws, size_t ws_bytes, void* stream) {
+  CHECK(check_axes(cfg, n_axes, axis));
+  return rope_append(cfg, T, q, q_ld, k, k_ld, v, v_ld, positions, n_axes, axis, table, rot_scale, slot_map, q_out,
+                     q_out_ld, k_cache, v_cache, ws, ws_bytes, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+// checks and arguments that both attention entry points share; T > 0 after it where it returns MOE_OK and *a is filled
+moe_status_t attention_args(const moe_attn_config_t* cfg, int32_t R, int32_t T, const void* q, int64_t q_ld,
+                            const int32_t* q_start, const int32_t* kv_len, const int32_t* block_table,
+                            const void* k_cache, const void* v_cache, const int32_t* tree_mask, int32_t mask_words,
+                            void* out, int64_t out_ld, float* lse, void* ws, AttnArgs* to) {
   if (bad_rows(cfg, q, q_ld, cfg->n_heads, T) || bad_rows(cfg, out, out_ld, cfg->n_heads, T) || q == out)
     return MOE_ERR_INVALID_ARG;
   if (R > 0 && (bad_array(q_start) || bad_array(kv_len) || (cfg->max_pages > 0 && bad_array(block_table))))
     return MOE_ERR_INVALID_ARG;
   if (!k_cache || !v_cache || !aligned(k_cache, 16) || !aligned(v_cache, 16)) return MOE_ERR_INVALID_ARG;
   if ((tree_mask && !aligned(tree_mask, 4)) || (lse && !aligned(lse, 4))) return MOE_ERR_INVALID_ARG;
-  AttnArgs a{};
+  AttnArgs& a = *to;
+  a = AttnArgs{};
   a.q = q;
   a.k = k_cache;
   a.v = v_cache;
@@ -267,8 +373,190 @@ moe_status_t moe_tree_attention(const moe_attn_config_t* cfg, int32_t R, int32_t
   a.max_pages = cfg->max_pages;
   a.page_shift = log2_of(cfg->page_size);
   a.mask_words = mask_words;
+  return MOE_OK;
+}
+
+// units that a walk over the requests (or groups) can have, in tiles and fixed costs, stay in 31 bits
+bool too_much_work(const moe_attn_config_t* cfg, int64_t blocks, int64_t T) {
+  const int64_t tiles = ((int64_t)cfg->max_pages * cfg->page_size + 127) / 128 + 1 + kAttnPieceCost;
+  return T * cfg->n_heads * 32 >= ((int64_t)1 << 31) || blocks * cfg->n_kv_heads * tiles >= ((int64_t)1 << 31);
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status_t moe_tree_attention(const moe_attn_config_t* cfg, int32_t R, int32_t T, const void* q, int64_t q_ld,
+                                const int32_t* q_start, const int32_t* kv_len, const int32_t* block_table,
+                                const void* k_cache, const void* v_cache, const int32_t* tree_mask,
+                                int32_t mask_words, void* out, int64_t out_ld, float* lse, void* ws, size_t ws_bytes,
+                                void* stream) {
+  CHECK(check_config(cfg));
+  CHECK(check_cache(cfg));
+  if (R < 0 || T < 0 || (tree_mask && mask_words < 1)) return MOE_ERR_INVALID_ARG;
+  if (R > kMaxRequests || T > kMaxRows || too_much_work(cfg, (int64_t)T + R, T)) return MOE_ERR_UNSUPPORTED;
+  CHECK(check_ws(ws, ws_bytes));
+  if (T == 0) return MOE_OK;
+  AttnArgs a;
+  CHECK(attention_args(cfg, R, T, q, q_ld, q_start, kv_len, block_table, k_cache, v_cache, tree_mask, mask_words, out,
+                       out_ld, lse, ws, &a));
   return launched(cfg->dtype == MOE_DT_F32 ? launch_attention_f32(a, (cudaStream_t)stream)
                                            : launch_attention_bf16(a, (cudaStream_t)stream));
+}
+
+size_t moe_prefix_workspace_bytes(const moe_attn_config_t* cfg, int32_t T) {
+  if (check_config(cfg) != MOE_OK || T < 0 || T > kMaxRows) return 0;
+  return cfg->dtype == MOE_DT_F32 ? workspace_bytes(cfg) : prefix_layout(cfg, T).end;
+}
+
+moe_status_t moe_prefix_attention(const moe_attn_config_t* cfg, int32_t R, int32_t T, const void* q, int64_t q_ld,
+                                  const int32_t* q_start, const int32_t* kv_len, const int32_t* block_table,
+                                  int32_t n_groups, const int32_t* group_start, const int32_t* prefix_row,
+                                  const int32_t* prefix_len, const void* k_cache, const void* v_cache,
+                                  const int32_t* tree_mask, int32_t mask_words, void* out, int64_t out_ld, float* lse,
+                                  void* ws, size_t ws_bytes, void* stream) {
+  CHECK(check_config(cfg));
+  CHECK(check_cache(cfg));
+  if (R < 0 || T < 0 || n_groups < 0 || n_groups > R || (tree_mask && mask_words < 1)) return MOE_ERR_INVALID_ARG;
+  if (R > kPrefixMaxRequests || T > kMaxRows || too_much_work(cfg, 2 * (int64_t)T + R + n_groups, T))
+    return MOE_ERR_UNSUPPORTED;
+  CHECK(check_ws(ws, ws_bytes));
+  if (ws_bytes < moe_prefix_workspace_bytes(cfg, T)) return MOE_ERR_WORKSPACE;
+  if (T == 0) return MOE_OK;
+  if (n_groups > 0 && (bad_array(group_start) || bad_array(prefix_row) || bad_array(prefix_len)))
+    return MOE_ERR_INVALID_ARG;
+  AttnArgs a;
+  CHECK(attention_args(cfg, R, T, q, q_ld, q_start, kv_len, block_table, k_cache, v_cache, tree_mask, mask_words, out,
+                       out_ld, lse, ws, &a));
+  a.n_groups = n_groups;
+  a.group_start = group_start;
+  a.prefix_row = prefix_row;
+  a.prefix_len = prefix_len;
+  if (cfg->dtype == MOE_DT_F32) return launched(launch_prefix_attention_f32(a, (cudaStream_t)stream));
+  const PrefixLayout l = prefix_layout(cfg, T);
+  uint8_t* base = reinterpret_cast<uint8_t*>(ws);
+  a.rows_part = reinterpret_cast<float*>(base + l.part);
+  a.rows_ml = reinterpret_cast<float2*>(base + l.ml);
+  a.parts_of = reinterpret_cast<int4*>(base + l.parts_of);
+  return launched(launch_prefix_attention_bf16(a, (cudaStream_t)stream));
+}
+
+moe_status_t moe_paged_fork(const moe_attn_config_t* cfg, int32_t n, const int32_t* src_rows, const int32_t* dst_rows,
+                            const int32_t* lengths, int32_t R, const int32_t* src_table, int32_t* dst_table,
+                            int32_t* page_shares, const int32_t* free_pages, int32_t n_free, const int32_t* free_head,
+                            int32_t* free_head_out, void* k_cache, void* v_cache, void* ws, size_t ws_bytes,
+                            void* stream) {
+  CHECK(check_config(cfg));
+  CHECK(check_cache(cfg));
+  if (n < 0 || R < 0 || n_free < 0) return MOE_ERR_INVALID_ARG;
+  if (n > kMaxForks || R > kMaxPlanRequests) return MOE_ERR_UNSUPPORTED;
+  CHECK(check_ws(ws, ws_bytes));
+  if (bad_array(free_head) || bad_array(free_head_out) || bad_array(page_shares)) return MOE_ERR_INVALID_ARG;
+  if (n_free > 0 && bad_array(free_pages)) return MOE_ERR_INVALID_ARG;
+  if (R > 0 && cfg->max_pages > 0 && (bad_array(src_table) || bad_array(dst_table))) return MOE_ERR_INVALID_ARG;
+  if (bad_caches(k_cache, v_cache)) return MOE_ERR_INVALID_ARG;
+  if (n > 0 && (bad_array(src_rows) || bad_array(dst_rows) || bad_array(lengths))) return MOE_ERR_INVALID_ARG;
+  // one table, or two that do not meet
+  const int64_t table_bytes = (int64_t)R * cfg->max_pages * 4, apart = (const char*)dst_table - (const char*)src_table;
+  if (apart != 0 && apart < table_bytes && -apart < table_bytes) return MOE_ERR_INVALID_ARG;
+  const int es = elem_bytes(cfg);
+  if (2ll * cfg->n_kv_heads * (cfg->head_dim * es / 16) * cfg->page_size >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED;
+  ForkArgs a{};
+  a.src = src_rows;
+  a.dst = dst_rows;
+  a.lengths = lengths;
+  a.src_table = src_table;
+  a.dst_table = dst_table;
+  a.shares = page_shares;
+  a.free_pages = free_pages;
+  a.free_head = free_head;
+  a.free_head_out = free_head_out;
+  a.k = reinterpret_cast<uint8_t*>(k_cache);
+  a.v = reinterpret_cast<uint8_t*>(v_cache);
+  a.hdr = reinterpret_cast<AttnHeader*>(ws);
+  a.page_stride = cfg->page_stride * es;
+  a.token_stride = cfg->token_stride * es;
+  a.head_stride = cfg->head_stride * es;
+  a.n = n;
+  a.R = R;
+  a.n_free = n_free;
+  a.n_pages = cfg->n_pages;
+  a.max_pages = cfg->max_pages;
+  a.page_shift = log2_of(cfg->page_size);
+  a.Hkv = cfg->n_kv_heads;
+  a.row_bytes = cfg->head_dim * es;
+  a.same = src_table == dst_table;
+  return launched(launch_fork(a, (cudaStream_t)stream));
+}
+
+moe_status_t moe_paged_compact(const moe_attn_config_t* cfg, int32_t R, int32_t N, const int32_t* first,
+                               const int32_t* keep_start, const int32_t* keep, const int32_t* block_table,
+                               const int32_t* page_shares, int32_t* len_out, void* k_cache, void* v_cache, void* ws,
+                               size_t ws_bytes, void* stream) {
+  CHECK(check_config(cfg));
+  CHECK(check_cache(cfg));
+  if (R < 0 || N < 0) return MOE_ERR_INVALID_ARG;
+  if (R > kMaxPlanRequests) return MOE_ERR_UNSUPPORTED;
+  CHECK(check_ws(ws, ws_bytes));
+  if (R == 0) return MOE_OK;
+  if (bad_array(first) || bad_array(keep_start) || (N > 0 && bad_array(keep)) ||
+      (cfg->max_pages > 0 && bad_array(block_table)))
+    return MOE_ERR_INVALID_ARG;
+  if (bad_caches(k_cache, v_cache)) return MOE_ERR_INVALID_ARG;
+  if ((page_shares && !aligned(page_shares, 4)) || (len_out && !aligned(len_out, 4))) return MOE_ERR_INVALID_ARG;
+  const int es = elem_bytes(cfg);
+  CompactArgs a{};
+  a.first = first;
+  a.keep_start = keep_start;
+  a.keep = keep;
+  a.block_table = block_table;
+  a.shares = page_shares;
+  a.len_out = len_out;
+  a.k = reinterpret_cast<uint8_t*>(k_cache);
+  a.v = reinterpret_cast<uint8_t*>(v_cache);
+  a.hdr = reinterpret_cast<AttnHeader*>(ws);
+  a.page_stride = cfg->page_stride * es;
+  a.token_stride = cfg->token_stride * es;
+  a.head_stride = cfg->head_stride * es;
+  a.R = R;
+  a.N = N;
+  a.n_pages = cfg->n_pages;
+  a.max_pages = cfg->max_pages;
+  a.page_shift = log2_of(cfg->page_size);
+  a.Hkv = cfg->n_kv_heads;
+  a.row_bytes = cfg->head_dim * es;
+  return launched(launch_compact(a, (cudaStream_t)stream));
+}
+
+moe_status_t moe_paged_release(const moe_attn_config_t* cfg, int32_t R, const int32_t* held_len,
+                               const int32_t* keep_len, int32_t* block_table, int32_t* page_shares,
+                               int32_t* free_pages, int32_t n_free, int32_t* free_head, void* ws, size_t ws_bytes,
+                               void* stream) {
+  CHECK(check_config(cfg));
+  if (R < 0 || n_free < 0) return MOE_ERR_INVALID_ARG;
+  if (R > kMaxPlanRequests || (int64_t)R * cfg->max_pages >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED;
+  CHECK(check_ws(ws, ws_bytes));
+  if (page_shares && ws_bytes < workspace_bytes(cfg)) return MOE_ERR_WORKSPACE;
+  if (bad_array(free_head) || (n_free > 0 && bad_array(free_pages))) return MOE_ERR_INVALID_ARG;
+  if (R == 0) return MOE_OK;
+  if (bad_array(held_len) || bad_array(keep_len) || (cfg->max_pages > 0 && bad_array(block_table)))
+    return MOE_ERR_INVALID_ARG;
+  if (page_shares && !aligned(page_shares, 4)) return MOE_ERR_INVALID_ARG;
+  ReleaseArgs a{};
+  a.held_len = held_len;
+  a.keep_len = keep_len;
+  a.block_table = block_table;
+  a.shares = page_shares;
+  a.free_pages = free_pages;
+  a.free_head = free_head;
+  a.hdr = reinterpret_cast<AttnHeader*>(ws);
+  a.last = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(ws) + MOE_ATTN_HEADER_BYTES);
+  a.R = R;
+  a.n_free = n_free;
+  a.n_pages = cfg->n_pages;
+  a.max_pages = cfg->max_pages;
+  a.page_shift = log2_of(cfg->page_size);
+  return launched(launch_release(a, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -11,7 +11,8 @@
 // at most; the cut to the upper 32 bits, a signed fraction of a turn in [-1/2, 1/2),
 // 2^-33 turns; their FP32 value, 2^-24 of it.  The cut is absolute: a sine of 1e-7 keeps
 // two digits, an error of 1e-9 beside the cosine's of 6e-8.  Rows are turned in FP32 and
-// rounded once, on the store.
+// rounded once, on the store.  With several axes (time, height, width) a pair takes
+// the position of its own axis; the rest is the same.
 //
 // Bound: every row is read once and written once.  A thread owns one 16-byte piece
 // of one head and walks a block's tokens with it: where the piece lies is worked
@@ -79,7 +80,7 @@ __device__ __forceinline__ void from_f(float v, bf16* p) { *p = __float2bfloat16
 // VECTOR: 16-byte pieces (the pieces that rotate are whole); else a thread has a
 // pair of elements, or one of the elements between the last pair and the next
 // 16-byte boundary, or a whole piece behind that.  tb: tokens a block; blockIdx.y: kRopeThreads pieces.
-template <typename T, bool INTER, bool VECTOR>
+template <typename T, bool INTER, bool VECTOR, bool AXES>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, int tb) {
   constexpr int N = Vec16<T>::N;
   constexpr bool SHUFFLE = VECTOR && !INTER;
@@ -155,7 +156,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, in
   auto place = [&](int p) { return p % M * n_piece + p / M; };
   for (int i = tid; i < nt * half; i += kRopeThreads) {
     const int t = i / half, p = i - t * half;
-    const uint64_t turned = (uint64_t)(int64_t)a.positions[t0 + t] * a.table[p];
+    int64_t pos = t0 + t;
+    if (AXES) pos += (int64_t)min((int)a.axis[p], a.n_axes - 1) * a.T;
+    const uint64_t turned = (uint64_t)(int64_t)a.positions[pos] * a.table[p];
     // upper 32 bits, rounded to nearest, as a signed fraction of a half turn
     const int32_t frac = (int32_t)(uint32_t)((turned + 0x80000000ull) >> 32);
     float s, c;
@@ -233,7 +236,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, in
   }
 }
 
-template <typename T>
+template <typename T, bool AXES>
 cudaError_t launch_t(const RopeArgs& a, int interleaved, cudaStream_t s) {
   constexpr int N = Vec16<T>::N;
   const bool vec = a.rot % (interleaved ? N : 2 * N) == 0;
@@ -249,11 +252,11 @@ cudaError_t launch_t(const RopeArgs& a, int interleaved, cudaStream_t s) {
   const int tb = (int)std::min<int64_t>(std::max<int64_t>((int64_t)a.T * chunks / blocks, 1), kRopeMaxTokens);
   const dim3 grid((unsigned)ceil_div(a.T, tb), (unsigned)chunks);
   if (interleaved) {
-    if (vec) launch_k(rope_kernel<T, true, true>, grid, kRopeThreads, 0, s, a, tb);
-    else launch_k(rope_kernel<T, true, false>, grid, kRopeThreads, 0, s, a, tb);
+    if (vec) launch_k(rope_kernel<T, true, true, AXES>, grid, kRopeThreads, 0, s, a, tb);
+    else launch_k(rope_kernel<T, true, false, AXES>, grid, kRopeThreads, 0, s, a, tb);
   } else {
-    if (vec) launch_k(rope_kernel<T, false, true>, grid, kRopeThreads, 0, s, a, tb);
-    else launch_k(rope_kernel<T, false, false>, grid, kRopeThreads, 0, s, a, tb);
+    if (vec) launch_k(rope_kernel<T, false, true, AXES>, grid, kRopeThreads, 0, s, a, tb);
+    else launch_k(rope_kernel<T, false, false, AXES>, grid, kRopeThreads, 0, s, a, tb);
   }
   return cudaGetLastError();
 }
@@ -262,7 +265,9 @@ cudaError_t launch_t(const RopeArgs& a, int interleaved, cudaStream_t s) {
 
 cudaError_t launch_rope(const RopeArgs& a, int dtype, int interleaved, cudaStream_t s) {
   if (a.T <= 0) return cudaSuccess;
-  return dtype == MOE_DT_F32 ? launch_t<float>(a, interleaved, s) : launch_t<bf16>(a, interleaved, s);
+  if (a.axis)
+    return dtype == MOE_DT_F32 ? launch_t<float, true>(a, interleaved, s) : launch_t<bf16, true>(a, interleaved, s);
+  return dtype == MOE_DT_F32 ? launch_t<float, false>(a, interleaved, s) : launch_t<bf16, false>(a, interleaved, s);
 }
 
 }  // namespace moe
