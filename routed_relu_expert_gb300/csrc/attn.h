@@ -13,7 +13,8 @@ constexpr int kAttnCounters = 960;
 struct AttnHeader {
   int32_t err;                       // device error bits (MOE_DEVERR_*)
   int32_t plan_ticket;               // blocks of the running plan that have read *free_head
-  int32_t pad[62];
+  int32_t met, left;                 // blocks of a cooperative launch that came to a meeting, that left
+  int32_t pad[60];
   int32_t counters[kAttnCounters];   // blocks of a split group that have stored their partial
 };
 static_assert(sizeof(AttnHeader) == MOE_ATTN_HEADER_BYTES, "attention workspace header");
@@ -63,6 +64,8 @@ struct CompactArgs {
   int32_t* len_out;
   uint8_t *k, *v;
   AttnHeader* hdr;
+  void* scratch;            // of the moves of long lists
+  size_t scratch_bytes;
   int64_t page_stride, token_stride, head_stride;   // bytes
   int R, N, n_pages, max_pages, page_shift, Hkv, row_bytes;
 };
@@ -71,6 +74,7 @@ cudaError_t launch_compact(const CompactArgs& a, cudaStream_t s);
 struct ReleaseArgs {
   const int32_t *held_len, *keep_len;
   int32_t *block_table, *shares, *free_pages, *free_head;
+  int32_t* counts;          // [blocks] entries freed (scratch)
   int32_t* last;            // [n_pages] the last entry that gives a page back (scratch)
   AttnHeader* hdr;
   int R, n_free, n_pages, max_pages, page_shift;

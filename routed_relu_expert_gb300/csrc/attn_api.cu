@@ -62,7 +62,7 @@ constexpr size_t kWorkspaceBytes = MOE_ATTN_HEADER_BYTES + kAttnPartBytes + kAtt
 
 // of a configuration: moe_paged_release has a word a page where attention has its partials
 size_t workspace_bytes(const moe_attn_config_t* c) {
-  const size_t pages = (MOE_ATTN_HEADER_BYTES + (size_t)c->n_pages * 4 + 15) / 16 * 16;
+  const size_t pages = (MOE_ATTN_HEADER_BYTES + (kAttnMaxCtas + (size_t)c->n_pages) * 4 + 15) / 16 * 16;
   return pages > kWorkspaceBytes ? pages : kWorkspaceBytes;
 }
 
@@ -506,6 +506,8 @@ moe_status_t moe_paged_compact(const moe_attn_config_t* cfg, int32_t R, int32_t 
   if ((page_shares && !aligned(page_shares, 4)) || (len_out && !aligned(len_out, 4))) return MOE_ERR_INVALID_ARG;
   const int es = elem_bytes(cfg);
   CompactArgs a{};
+  a.scratch = reinterpret_cast<uint8_t*>(ws) + MOE_ATTN_HEADER_BYTES;
+  a.scratch_bytes = kWorkspaceBytes - MOE_ATTN_HEADER_BYTES;
   a.first = first;
   a.keep_start = keep_start;
   a.keep = keep;
@@ -550,7 +552,8 @@ moe_status_t moe_paged_release(const moe_attn_config_t* cfg, int32_t R, const in
   a.free_pages = free_pages;
   a.free_head = free_head;
   a.hdr = reinterpret_cast<AttnHeader*>(ws);
-  a.last = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(ws) + MOE_ATTN_HEADER_BYTES);
+  a.counts = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(ws) + MOE_ATTN_HEADER_BYTES);
+  a.last = a.counts + kAttnMaxCtas;
   a.R = R;
   a.n_free = n_free;
   a.n_pages = cfg->n_pages;

@@ -14,6 +14,49 @@ constexpr int kThreads = 256;
 
 __device__ __forceinline__ int held(int64_t tokens, int shift) { return (int)((tokens + (1ll << shift) - 1) >> shift); }
 
+// Blocks of a cooperative launch that wait for one another.  The counters return to
+// zero by themselves: the last block to leave resets them.  A wait ends after
+// tc::kWaitLimitNs at the latest, with MOE_DEVERR_TIMEOUT.
+struct GridMeet {
+  AttnHeader* hdr;
+  int blocks, met = 0;
+  bool ok = true;
+  __device__ GridMeet(AttnHeader* h, int n) : hdr(h), blocks(n) {}
+  // what the blocks read and wrote before it is done for what they do after it
+  __device__ bool operator()() {
+    __syncthreads();
+    if (blocks == 1) return true;
+    ++met;
+    __shared__ int good;
+    if (threadIdx.x == 0) {
+      __threadfence();
+      atomicAdd(&hdr->met, 1);
+      const uint64_t t0 = globaltimer();
+      int seen, tries = 0;
+      good = 1;
+      while (true) {
+        asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(seen) : "l"(&hdr->met) : "memory");
+        if (seen >= met * blocks) break;
+        if ((++tries & 255) == 0 && globaltimer() - t0 > tc::kWaitLimitNs) {
+          good = 0;
+          set_error(&hdr->err, MOE_DEVERR_TIMEOUT);
+          break;
+        }
+      }
+    }
+    __syncthreads();
+    ok = ok && good;
+    return ok;
+  }
+  __device__ void leave() {
+    __syncthreads();
+    if (blocks > 1 && threadIdx.x == 0 && atomicAdd(&hdr->left, 1) == blocks - 1) {
+      hdr->met = 0;
+      hdr->left = 0;
+    }
+  }
+};
+
 // sum of one value a thread over the block, in every thread
 __device__ __forceinline__ int block_sum(int v, int* tmp) {
   v = __reduce_add_sync(0xffffffffu, v);
@@ -118,79 +161,151 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const ForkArgs a) {
 // ---------------------------------------------------------------------------
 // compact
 // ---------------------------------------------------------------------------
-constexpr int kStage = 256;                    // moves worked out at a time
+// a move of one token: offsets (bytes) of its first head in a cache, from -1 where it stays
+struct Move {
+  int64_t from, to;
+};
 
-// blockIdx.x: the request; blockIdx.y: kThreads of a token's 16-byte pieces
+// kept number i of request r (its list is keep[begin ..)): places ascend and lie at or before their sources
+__device__ __forceinline__ Move move_of(const CompactArgs& a, int r, int first, int begin, int i, int& bad) {
+  const int64_t cap = (int64_t)a.max_pages << a.page_shift;
+  const int page_mask = (1 << a.page_shift) - 1;
+  const int node = a.keep[i], place = i - begin;
+  if (node < place || (i > begin && a.keep[i - 1] >= node) || (int64_t)first + node >= cap) {
+    bad |= MOE_DEVERR_CACHE;
+    return {-1, -1};
+  }
+  if (node == place) return {-1, -1};
+  const int32_t* table = a.block_table + (int64_t)r * a.max_pages;
+  const int p = table[(first + node) >> a.page_shift], d = table[(first + place) >> a.page_shift];
+  if (p < 0 || p >= a.n_pages || d < 0 || d >= a.n_pages || (a.shares && a.shares[d] > 0)) {
+    bad |= MOE_DEVERR_CACHE;
+    return {-1, -1};
+  }
+  return {p * a.page_stride + ((first + node) & page_mask) * a.token_stride,
+          d * a.page_stride + ((first + place) & page_mask) * a.token_stride};
+}
+// request r's list, empty where its bounds are no good; its length goes to len_out
+__device__ __forceinline__ void list_of(const CompactArgs& a, int r, int& first, int& begin, int& end, int& bad) {
+  begin = a.keep_start[r];
+  end = a.keep_start[r + 1];
+  first = a.first[r];
+  if (begin < 0 || end < begin || end > a.N || first < 0) {
+    bad |= MOE_DEVERR_CACHE;
+    begin = end = 0;
+  }
+}
+
+// Short lists: a block has a request and kThreads of a token's 16-byte pieces, a thread
+// one of them for token after token.
+constexpr int kStage = 256;                    // moves worked out at a time
+constexpr int kMoveAhead = 8;                  // tokens whose loads a thread has in flight
 __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a) {
   pdl_wait();
-  __shared__ int64_t s_from[kStage], s_to[kStage];
+  __shared__ Move s_move[kStage];
   const int r = blockIdx.x, tid = threadIdx.x;
   const int per_head = a.row_bytes >> 4, per_token = per_head * a.Hkv;
   const int x = (int)blockIdx.y * kThreads + tid;
   const bool have = x < 2 * per_token;
   const int v = x >= per_token, z = x - v * per_token, h = z / per_head;
   uint8_t* cache = (v ? a.v : a.k) + h * a.head_stride + 16 * (z - h * per_head);
-  int begin = a.keep_start[r], end = a.keep_start[r + 1];
-  const int first = a.first[r];
-  const int64_t cap = (int64_t)a.max_pages << a.page_shift;
-  int bad = 0;
-  if (begin < 0 || end < begin || end > a.N || first < 0) {
-    bad = MOE_DEVERR_CACHE;
-    begin = end = 0;
-  }
+  int bad = 0, first, begin, end;
+  list_of(a, r, first, begin, end, bad);
   if (a.len_out && blockIdx.y == 0 && tid == 0) a.len_out[r] = max(first, 0) + end - begin;
-  const int32_t* table = a.block_table + (int64_t)r * a.max_pages;
-  const int page_mask = (1 << a.page_shift) - 1;
   for (int i0 = begin; i0 < end; i0 += kStage) {
     const int n = min(kStage, end - i0);
     __syncthreads();
-    if (tid < n) {
-      // where kept token i lies and where it goes (-1: it stays)
-      const int i = i0 + tid, node = a.keep[i], place = i - begin;
-      int64_t from = -1, to = -1;
-      if (node < place || (i > begin && a.keep[i - 1] >= node) || (int64_t)first + node >= cap) {
-        bad |= MOE_DEVERR_CACHE;
-      } else if (node > place) {
-        const int p = table[(first + node) >> a.page_shift], d = table[(first + place) >> a.page_shift];
-        if (p < 0 || p >= a.n_pages || d < 0 || d >= a.n_pages || (a.shares && a.shares[d] > 0)) {
-          bad |= MOE_DEVERR_CACHE;
-        } else {
-          from = p * a.page_stride + ((first + node) & page_mask) * a.token_stride;
-          to = d * a.page_stride + ((first + place) & page_mask) * a.token_stride;
-        }
-      }
-      s_from[tid] = from;
-      s_to[tid] = to;
-    }
+    if (tid < n) s_move[tid] = move_of(a, r, first, begin, i0 + tid, bad);
     __syncthreads();
     if (!have) continue;
-    // places ascend and lie at or before their sources: a place is written after it was read
-    for (int j = 0; j < n; ++j)
-      if (s_from[j] >= 0)
-        *reinterpret_cast<uint4*>(cache + s_to[j]) = *reinterpret_cast<const uint4*>(cache + s_from[j]);
+    // (a place is not written before its own and every earlier source is read)
+    for (int j0 = 0; j0 < n; j0 += kMoveAhead) {
+      uint4 d[kMoveAhead];
+#pragma unroll
+      for (int j = 0; j < kMoveAhead; ++j)
+        if (j0 + j < n && s_move[j0 + j].from >= 0) d[j] = *reinterpret_cast<const uint4*>(cache + s_move[j0 + j].from);
+#pragma unroll
+      for (int j = 0; j < kMoveAhead; ++j)
+        if (j0 + j < n && s_move[j0 + j].from >= 0) *reinterpret_cast<uint4*>(cache + s_move[j0 + j].to) = d[j];
+    }
   }
   if (bad) set_error(&a.hdr->err, bad);
+}
+
+// Long lists, in two launches.  The first works the moves out, a thread a token (of all
+// requests' lists as one).
+__global__ void __launch_bounds__(kThreads) compact_moves_kernel(const CompactArgs a, Move* moves, int i0, int n) {
+  pdl_wait();
+  const int x = blockIdx.x * kThreads + threadIdx.x;
+  int bad = 0, first, begin, end;
+  if (i0 == 0)
+    for (int r = x; r < a.R; r += gridDim.x * kThreads) {
+      list_of(a, r, first, begin, end, bad);
+      if (a.len_out) a.len_out[r] = max(first, 0) + end - begin;
+    }
+  if (x < n) {
+    const int i = i0 + x;
+    // the last request whose list begins at or before i
+    int lo = 0, hi = a.R;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.keep_start[mid] <= i) lo = mid; else hi = mid;
+    }
+    list_of(a, lo, first, begin, end, bad);
+    moves[x] = begin <= i && i < end ? move_of(a, lo, first, begin, i, bad) : Move{-1, -1};
+  }
+  if (bad) set_error(&a.hdr->err, bad);
+}
+
+// The second moves the tokens in waves: all blocks read their part of a wave into
+// registers, meet, and write it.  Token i of the lists goes to a place at or before
+// its source, so what a wave writes lies behind every later wave's sources and only
+// its own wave and earlier ones read there.
+constexpr int kWaveThreads = 512;
+constexpr int kWaveAhead = 16;                 // tokens a thread has in flight
+__global__ void __launch_bounds__(kWaveThreads, 1) compact_wave_kernel(const CompactArgs a, const Move* moves, int n,
+                                                                        int groups) {
+  GridMeet meet(a.hdr, (int)gridDim.x);
+  // a block has one group of a token's pieces: `per` of them, of as many tokens as it has threads for
+  const int per_head = a.row_bytes >> 4, per_token = per_head * a.Hkv, pieces = 2 * per_token;
+  const int group = blockIdx.x % groups, block = blockIdx.x / groups, blocks = gridDim.x / groups;
+  const int per = min(pieces, kWaveThreads), tokens = kWaveThreads / per;
+  const int sub = threadIdx.x / per, x = group * per + threadIdx.x - sub * per;
+  const bool have = sub < tokens && x < pieces;
+  const int v = x >= per_token, z = x - v * per_token, h = z / per_head;
+  uint8_t* cache = (v ? a.v : a.k) + h * a.head_stride + 16 * (z - h * per_head);
+  const int step = tokens * kWaveAhead;
+  const int64_t wave = (int64_t)blocks * step;
+  for (int64_t w0 = 0; w0 < n; w0 += wave) {
+    const int64_t t0 = w0 + (int64_t)block * step + sub;
+    uint4 d[kWaveAhead];
+    int64_t to[kWaveAhead];
+#pragma unroll
+    for (int j = 0; j < kWaveAhead; ++j) {
+      const int64_t t = t0 + (int64_t)j * tokens;
+      to[j] = -1;
+      if (have && t < n) {
+        const Move m = moves[t];
+        if (m.from >= 0) {
+          d[j] = *reinterpret_cast<const uint4*>(cache + m.from);
+          to[j] = m.to;
+        }
+      }
+    }
+    if (!meet()) break;
+#pragma unroll
+    for (int j = 0; j < kWaveAhead; ++j)
+      if (to[j] >= 0) *reinterpret_cast<uint4*>(cache + to[j]) = d[j];
+  }
+  meet.leave();
 }
 
 // ---------------------------------------------------------------------------
 // release
 // ---------------------------------------------------------------------------
 constexpr int kRelThreads = 1024;
-constexpr int kRelMaxCluster = 8;
-
-__device__ __forceinline__ uint32_t cluster_rank_x() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-// a word of another CTA's shared memory
-__device__ __forceinline__ int remote_int(const int* p, uint32_t rank) {
-  uint32_t at;
-  int v;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
-  return v;
-}
+constexpr int kRelWarps = kRelThreads / 32;
+constexpr int kRelEntries = 2 * kRelThreads;   // of a block, before another one helps
 
 // exclusive prefix of one value a thread over the block; *total: their sum
 __device__ __forceinline__ int block_scan(int v, int* tmp, int* total) {
@@ -219,12 +334,13 @@ __device__ __forceinline__ int block_scan(int v, int* tmp, int* total) {
   return before;
 }
 
-// one cluster; its CTAs take equal parts of all entries, in the table's order
-__global__ void __launch_bounds__(kRelThreads) release_kernel(const ReleaseArgs a) {
+// All entries that are given back, in the table's order, are cut into equal parts, a
+// block each, and a block's into its warps'; lanes take neighbours.
+__global__ void __launch_bounds__(kRelThreads, 1) release_kernel(const ReleaseArgs a) {
   extern __shared__ int prefix[];              // [R + 1] entries before each request
-  __shared__ int tmp[32], s_freed;
+  __shared__ int tmp[32];
   pdl_wait();
-  const int tid = threadIdx.x, rank = (int)cluster_rank_x(), ctas = (int)gridDim.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = (int)blockIdx.x;
   int bad = 0;
   auto span = [&](int r, int& lo) {
     int now = a.held_len[r], keep = a.keep_len[r];
@@ -246,86 +362,146 @@ __global__ void __launch_bounds__(kRelThreads) release_kernel(const ReleaseArgs 
     }
     if (tid == 0) prefix[a.R] = total;
   }
+  // blocks that take part: the same number in each of them
+  const int ctas = min((int)gridDim.x, max((int)(((int64_t)total + kRelEntries - 1) / kRelEntries), 1));
+  if (rank >= ctas) return;
+  GridMeet meet(a.hdr, ctas);
   __syncthreads();
-  // this thread's entries: a run of neighbours
   const int64_t e0 = (int64_t)total * rank / ctas, e1 = (int64_t)total * (rank + 1) / ctas;
-  const int k = (int)((e1 - e0 + kRelThreads - 1) / kRelThreads);
-  const int begin = (int)min(e0 + (int64_t)tid * k, e1), end = (int)min((int64_t)begin + k, e1);
+  const int begin = (int)(e0 + (e1 - e0) * warp / kRelWarps), end = (int)(e0 + (e1 - e0) * (warp + 1) / kRelWarps);
   int row0 = 0;
-  if (begin < end) {
-    int lo = 0, hi = a.R;                      // the last row with prefix[row] <= begin
+  {
+    int lo = 0, hi = a.R;                      // the last row with prefix[row] <= the lane's first entry
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (prefix[mid] <= begin) lo = mid; else hi = mid;
+      if (prefix[mid] <= begin + lane) lo = mid; else hi = mid;
     }
     row0 = lo;
   }
-  // f(place in the table, page or -1) of each of them
+  // f(place in the table or -1, page or -1) of each of them, all lanes together
+  constexpr int kAhead = 4;
   auto walk = [&](auto f) {
-    int r = row0, lo = 0;
-    if (begin < end) span(r, lo);
-    for (int e = begin; e < end; ++e) {
-      if (e >= prefix[r + 1]) {
-        while (e >= prefix[r + 1]) ++r;
-        span(r, lo);
-      }
-      const int at = r * a.max_pages + lo + (e - prefix[r]);
-      int p = a.block_table[at];
-      if (p < 0 || p >= a.n_pages) {
-        if (p != -1) bad |= MOE_DEVERR_CACHE;
-        p = -1;
+    int r = row0, have = -1, lo = 0;
+    for (int b = begin; b < end; b += 32 * kAhead) {
+      int at[kAhead], p[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int e = b + 32 * j + lane;
+        at[j] = p[j] = -1;
+        if (e < end) {
+          while (e >= prefix[r + 1]) ++r;
+          if (have != r) span(r, lo);
+          have = r;
+          at[j] = r * a.max_pages + lo + (e - prefix[r]);
+          p[j] = a.block_table[at[j]];
+          if (p[j] < 0 || p[j] >= a.n_pages) {
+            if (p[j] != -1) bad |= MOE_DEVERR_CACHE;
+            p[j] = -1;
+          }
+        }
       }
       f(at, p);
     }
   };
-  auto meet = [] {
-    __syncwarp();
-    tc::cluster_sync();
-  };
   if (a.shares) {
-    walk([&](int, int p) { if (p >= 0) a.last[p] = -1; });
+    walk([&](int (&)[kAhead], int (&p)[kAhead]) {
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+        if (p[j] >= 0) a.last[p[j]] = -1;
+    });
     meet();
-    walk([&](int at, int p) {
-      if (p < 0) return;
-      atomicMax(&a.last[p], at);
-      atomicSub(&a.shares[p], 1);
+    walk([&](int (&at)[kAhead], int (&p)[kAhead]) {
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+        if (p[j] >= 0) {
+          atomicMax(&a.last[p[j]], at[j]);
+          atomicSub(&a.shares[p[j]], 1);
+        }
     });
     meet();
   }
   // freed: no holder is left, and this is the last of the entries that gave it back
-  auto freed = [&](int at, int p) {
-    return p >= 0 && (!a.shares || (__ldcg(&a.shares[p]) < 0 && __ldcg(&a.last[p]) == at));
+  auto freed = [&](int (&at)[kAhead], int (&p)[kAhead], bool (&is)[kAhead], int (&left)[kAhead]) {
+    int of[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      left[j] = p[j] >= 0 && a.shares ? __ldcg(&a.shares[p[j]]) : -1;
+      of[j] = p[j] >= 0 && a.shares ? __ldcg(&a.last[p[j]]) : at[j];
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) is[j] = p[j] >= 0 && left[j] < 0 && of[j] == at[j];
   };
-  int count = 0, own;
-  walk([&](int at, int p) { count += freed(at, p); });
-  int place = block_scan(count, tmp, &own);
-  if (tid == 0) s_freed = own;
-  meet();
-  int all = 0;
-  for (int c = 0; c < ctas; ++c) {
-    const int n = c == rank ? own : remote_int(&s_freed, c);
-    if (c < rank) place += n;
-    all += n;
-  }
-  if (all > head || head > a.n_free) bad |= MOE_DEVERR_CACHE;   // more than the list gave out
-  place += head - all;
-  walk([&](int at, int p) {
-    if (freed(at, p)) {
-      if (place >= 0 && place < a.n_free) a.free_pages[place] = p;
-      ++place;
-    }
+  int count = 0;
+  walk([&](int (&at)[kAhead], int (&p)[kAhead]) {
+    bool is[kAhead];
+    int left[kAhead];
+    freed(at, p, is, left);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) count += __popc(__ballot_sync(0xffffffffu, is[j]));
   });
-  // every CTA has looked at the counts
-  meet();
-  walk([&](int at, int p) {
-    if (a.shares && freed(at, p)) {
-      if (__ldcg(&a.shares[p]) < -1) bad |= MOE_DEVERR_CACHE;   // given back more often than it was held
-      a.shares[p] = 0;
+  int own;
+  int place = block_scan(lane == 0 ? count : 0, tmp, &own);      // entries freed before this warp's, in its lane 0
+  place = __shfl_sync(0xffffffffu, place, 0);
+  int all = own;
+  if (ctas > 1) {
+    if (tid == 0) a.counts[rank] = own;
+    meet();
+    int before = 0, sum = 0;
+    for (int c = tid; c < ctas; c += kRelThreads) {
+      const int n = __ldcg(&a.counts[c]);
+      sum += n;
+      if (c < rank) before += n;
     }
-    a.block_table[at] = -1;
+    int ignored;
+    block_scan(before, tmp, &ignored);
+    place += ignored;
+    block_scan(sum, tmp, &all);
+  }
+  if (!meet.ok) {                              // (a wait that gave up: the free list stays as it is)
+    meet.leave();
+    return;
+  }
+  if (all > head || head > a.n_free) bad |= MOE_DEVERR_CACHE;    // more than the list gave out
+  place += head - all;
+  walk([&](int (&at)[kAhead], int (&p)[kAhead]) {
+    bool is[kAhead];
+    int left[kAhead];
+    freed(at, p, is, left);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const uint32_t set = __ballot_sync(0xffffffffu, is[j]);
+      const int to = place + __popc(set & lanemask_lt());
+      place += __popc(set);
+      if (is[j]) {
+        if (to >= 0 && to < a.n_free) a.free_pages[to] = p[j];
+        // (another entry of the page reads a count of -1 or 0 and that the last entry is not it: either way not freed)
+        if (left[j] < -1) bad |= MOE_DEVERR_CACHE;               // given back more often than it was held
+        if (a.shares) a.shares[p[j]] = 0;
+      }
+      if (at[j] >= 0) a.block_table[at[j]] = -1;
+    }
   });
   if (rank == 0 && tid == 0) *a.free_head = max(head - all, 0);
   if (bad) set_error(&a.hdr->err, bad);
+  meet.leave();
+}
+
+// blocks of a cooperative launch wait for one another
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cooperative(void (*kernel)(KArgs...), unsigned grid, unsigned block, size_t smem, cudaStream_t s,
+                               Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  count_launches(1);
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
 }  // namespace
@@ -339,37 +515,43 @@ cudaError_t launch_fork(const ForkArgs& a, cudaStream_t s) {
 cudaError_t launch_compact(const CompactArgs& a, cudaStream_t s) {
   if (a.R <= 0) return cudaSuccess;
   const int64_t pieces = 2ll * (a.row_bytes >> 4) * a.Hkv;
-  return launch_k(compact_kernel, dim3((unsigned)a.R, (unsigned)ceil_div(pieces, kThreads)), kThreads, 0, s, a);
+  const int64_t groups = ceil_div(pieces, kWaveThreads);
+  static PerDeviceOnce once;
+  int sms = 0;
+  const cudaError_t e = once.run([](int& v) { v = tc::num_sms(); return cudaSuccess; }, &sms);
+  if (e != cudaSuccess) return e;
+  // short lists; and tokens wider than the waves have blocks for (152 x 8 KB)
+  if (a.N <= 1024 || groups > sms)
+    return launch_k(compact_kernel, dim3((unsigned)a.R, (unsigned)ceil_div(pieces, kThreads)), kThreads, 0, s, a);
+  Move* moves = reinterpret_cast<Move*>(a.scratch);
+  const int most = (int)(a.scratch_bytes / sizeof(Move));
+  for (int i0 = 0; i0 < a.N; i0 += most) {
+    const int n = std::min(most, a.N - i0);
+    cudaError_t e2 = launch_k(compact_moves_kernel, dim3((unsigned)ceil_div(n, kThreads)), kThreads, 0, s, a, moves, i0, n);
+    // as many blocks as the list has work for, the same number in every group
+    const int64_t step = kWaveThreads / std::min<int64_t>(pieces, kWaveThreads) * kWaveAhead;
+    const int64_t blocks = std::min<int64_t>(sms / groups, ceil_div(n, step));
+    if (e2 == cudaSuccess)
+      e2 = launch_cooperative(compact_wave_kernel, (unsigned)(blocks * groups), kWaveThreads, 0, s, a, moves, n, (int)groups);
+    if (e2 != cudaSuccess) return e2;
+  }
+  return cudaSuccess;
 }
 
 cudaError_t launch_release(const ReleaseArgs& a, cudaStream_t s) {
   const size_t smem = ((size_t)a.R + 1) * 4;
   static PerDeviceOnce once;
-  int unused = 0;
+  int sms = 0;
   const cudaError_t e = once.run(
       [](int& v) {
-        v = 1;
+        v = std::min(tc::num_sms(), kAttnMaxCtas);
         return cudaFuncSetAttribute(release_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (16384 + 1) * 4);
       },
-      &unused);
+      &sms);
   if (e != cudaSuccess) return e;
-  const unsigned ctas = (int64_t)a.R * a.max_pages > 4096 ? kRelMaxCluster : 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kRelThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = ctas;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  count_launches(1);
-  return cudaLaunchKernelEx(&cfg, release_kernel, a);
+  const unsigned ctas = (unsigned)std::min<int64_t>(ceil_div((int64_t)a.R * a.max_pages, kRelEntries), sms);
+  if (ctas <= 1) return launch_k(release_kernel, dim3(1), dim3(kRelThreads), smem, s, a);
+  return launch_cooperative(release_kernel, ctas, kRelThreads, smem, s, a);
 }
 
 }  // namespace moe
