@@ -55,8 +55,8 @@
 // at masks; there, V rows past the last key are zeroed in shared memory (P is 0,
 // but 0 x NaN is not), and V rows of nodes that are not finite are zeroed too and
 // added by hand to the rows that see them.
-#include "attn.h"
-#include "tc_common.cuh"
+#include "attn_tc.cuh"
+#include "attn_walk.cuh"
 
 #include <algorithm>
 #include <type_traits>
@@ -67,16 +67,13 @@ namespace {
 
 using namespace tc;
 
-constexpr int kTile = 128;                     // keys a tile
-constexpr int kHalfBytes = kTile * 128;        // 128 rows of 64 BF16
+constexpr int kTile = kAttnTile;               // keys a tile
 constexpr int kSoftWarps = 8;
 constexpr int kThreads = 32 * (kSoftWarps + 4);
 constexpr int kLoaders = 2;                    // warps that issue the TMA copies
 constexpr int kQueue = 4;                      // pieces worked out ahead
 
 constexpr uint32_t kTmemCols = 512;
-constexpr float kRaise = 8.f;                  // log2 units by which a maximum may pass its reference (above)
-constexpr int kMaxSmem = 232448;
 
 template <int DP>
 struct Geo {
@@ -100,17 +97,10 @@ struct Piece {
   int row0, tok0, ntok;    // first row of the block in q; its first node and its nodes
   int ctx, kv;             // tokens before the nodes; all tokens of the table's row (at most ctx + nodes)
   int t0, n;               // first tile and number of tiles (those that a chain's block can see)
-  int flags;               // kStarts, kEnds, kLast, kPrefix, kJoined
+  int flags;               // kStarts, kEnds, kLast
   int parts;               // of a unit that starts here and ends in a later run: its runs
-  int skip;                // pages of the table's row before the first tile (a shared prefix's)
 };
-// kPrefix: a group's prefix; kJoined: own tokens of rows that have a prefix beside them
-constexpr int kStarts = 1, kEnds = 2, kLast = 4, kPrefix = 8, kJoined = 16;
-
-struct Req {
-  int q0, n, kv, ctx, tiles, blocks;
-  int row, skip, flags;    // (shared prefixes) the table's row; Piece::skip; kPrefix or kJoined
-};
+constexpr int kStarts = 1, kEnds = 2, kLast = 4;
 
 // fixed shared-memory words after the tiles
 struct Small {
@@ -128,271 +118,16 @@ struct Small {
   int64_t scan[kThreads / 32];
 };
 
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
-                                            uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
-      "[%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
-      : "memory");
-}
-
-// D[tmem] (+)= A[tmem] B[shared]
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 // the barrier of the two softmax warps that share rows (hardware barriers 1 .. 4)
 __device__ __forceinline__ void pair_sync(int q) { asm volatile("bar.sync %0, 64;" ::"r"(q + 1) : "memory"); }
 __device__ __forceinline__ void pair_arrive(int q) { asm volatile("bar.arrive %0, 64;" ::"r"(q + 1) : "memory"); }
-
-// one thread of a converged warp
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
-  return p != 0;
-}
-
-// 32 columns of this thread's lane, without waiting for them
-template <int O, int N>
-__device__ __forceinline__ void ld32_async(uint32_t taddr, float (&v)[N]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=f"(v[O + 0]), "=f"(v[O + 1]), "=f"(v[O + 2]), "=f"(v[O + 3]), "=f"(v[O + 4]), "=f"(v[O + 5]),
-        "=f"(v[O + 6]), "=f"(v[O + 7]), "=f"(v[O + 8]), "=f"(v[O + 9]), "=f"(v[O + 10]), "=f"(v[O + 11]),
-        "=f"(v[O + 12]), "=f"(v[O + 13]), "=f"(v[O + 14]), "=f"(v[O + 15]), "=f"(v[O + 16]), "=f"(v[O + 17]),
-        "=f"(v[O + 18]), "=f"(v[O + 19]), "=f"(v[O + 20]), "=f"(v[O + 21]), "=f"(v[O + 22]), "=f"(v[O + 23]),
-        "=f"(v[O + 24]), "=f"(v[O + 25]), "=f"(v[O + 26]), "=f"(v[O + 27]), "=f"(v[O + 28]), "=f"(v[O + 29]),
-        "=f"(v[O + 30]), "=f"(v[O + 31])
-      : "r"(taddr));
-}
-// waits for this thread's loads; the values pass through it, so that no use of
-// them can move above the wait
-template <int O, int N>
-__device__ __forceinline__ void ld32_wait(float (&v)[N]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+f"(v[O + 0]), "+f"(v[O + 1]), "+f"(v[O + 2]), "+f"(v[O + 3]), "+f"(v[O + 4]), "+f"(v[O + 5]),
-                 "+f"(v[O + 6]), "+f"(v[O + 7]), "+f"(v[O + 8]), "+f"(v[O + 9]), "+f"(v[O + 10]), "+f"(v[O + 11]),
-                 "+f"(v[O + 12]), "+f"(v[O + 13]), "+f"(v[O + 14]), "+f"(v[O + 15]), "+f"(v[O + 16]), "+f"(v[O + 17]),
-                 "+f"(v[O + 18]), "+f"(v[O + 19]), "+f"(v[O + 20]), "+f"(v[O + 21]), "+f"(v[O + 22]), "+f"(v[O + 23]),
-                 "+f"(v[O + 24]), "+f"(v[O + 25]), "+f"(v[O + 26]), "+f"(v[O + 27]), "+f"(v[O + 28]), "+f"(v[O + 29]),
-                 "+f"(v[O + 30]), "+f"(v[O + 31])
-               :
-               : "memory");
-}
-__device__ __forceinline__ void st32(uint32_t taddr, const float (&v)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
-      "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]),
-      "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]),
-      "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31])
-      : "memory");
-}
-__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t (&v)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-          taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-      : "memory");
-}
-__device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// two FP32 values in one instruction (each rounded as by itself), and the larger
-// of three: the softmax groups are bound by the instructions that they issue
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unpair(uint64_t v, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// The warp's wait for a phase: a few tries that do not suspend the warp (the
-// hot waits end within them, and a suspended warp's wake-up is dearer than they
-// are), then the bounded wait of the other tensor-core kernels.
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-__device__ __noinline__ bool wait_slow(uint32_t b, uint32_t parity, volatile int* abort_flag, int32_t* err) {
-  return __all_sync(0xffffffffu, mbar_wait<false, true>(b, parity, abort_flag, err));
-}
-template <int TRIES = 32>
-__device__ __forceinline__ bool wait_warp(uint32_t b, uint32_t parity, volatile int* abort_flag, int32_t* err) {
-#pragma unroll 1
-  for (int i = 0; i < TRIES; ++i)
-    if (__all_sync(0xffffffffu, mbar_test(b, parity))) return true;
-  return wait_slow(b, parity, abort_flag, err);
-}
-
-// shared-memory descriptor of V as the MN-major B operand: 64 values of a key
-// contiguous (one 128-byte swizzle row), 8-key groups 1024 B apart (stride), the
-// next 64 values of the head a half further (leading)
-__device__ __forceinline__ uint64_t v_desc(uint32_t addr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((addr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(kHalfBytes >> 4) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
-}
-
-// lane l of four holds x[0..3]; after it, x[i] is what lane i of the four had in x[l]
-__device__ __forceinline__ void transpose4(uint4 (&x)[4], int lane) {
-  auto swap = [&](uint4& mine, int by) {
-    mine.x = __shfl_xor_sync(0xffffffffu, mine.x, by);
-    mine.y = __shfl_xor_sync(0xffffffffu, mine.y, by);
-    mine.z = __shfl_xor_sync(0xffffffffu, mine.z, by);
-    mine.w = __shfl_xor_sync(0xffffffffu, mine.w, by);
-  };
-  // two by two blocks, then the pairs inside them
-#pragma unroll
-  for (int by = 2; by > 0; by >>= 1)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (i & by) continue;
-      uint4 send = lane & by ? x[i] : x[i | by];
-      swap(send, by);
-      if (lane & by) x[i] = send; else x[i | by] = send;
-    }
-}
-
-// ---------------------------------------------------------------------------
-// nodes whose V is not finite (out of the hot path's registers)
-// ---------------------------------------------------------------------------
-// O += p V, columns c0 .. c0 + 63 of the head, for the rows that see them (p, read
-// back from tensor memory, is 0 where a row does not)
-__device__ __noinline__ void add_odd(const AttnArgs& a, const int32_t* table, int h, int key0, uint4 odd, int c0,
-                                     uint32_t p_addr, uint32_t o_addr) {
-  for (int i = 0; i < kTile; ++i) {
-    const uint32_t word = i < 64 ? (i < 32 ? odd.x : odd.y) : (i < 96 ? odd.z : odd.w);
-    if (!(word >> (i & 31) & 1u)) continue;
-    const int key = key0 + i;
-    const int pg = table[key >> a.page_shift];
-    if (pg < 0 || pg >= a.n_pages) continue;
-    const bf16* vp = reinterpret_cast<const bf16*>(a.v) + (int64_t)pg * a.page_stride +
-                     (int64_t)(key & ((1 << a.page_shift) - 1)) * a.token_stride + (int64_t)h * a.head_stride;
-    uint32_t x;
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(x) : "r"(p_addr + (uint32_t)(i >> 1)));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(x) : : "memory");
-    const float pi = i & 1 ? bf16_hi(x) : bf16_lo(x);
-    for (int c = c0; c < c0 + 64; ++c) {
-      asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(x) : "r"(o_addr + (uint32_t)c));
-      asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(x) : : "memory");
-      if (pi != 0.f && c < a.D) x = __float_as_uint(fmaf(pi, __bfloat162float(vp[c]), __uint_as_float(x)));
-      asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(o_addr + (uint32_t)c), "r"(x) : "memory");
-      st_wait();
-    }
-  }
-}
-
-// ---------------------------------------------------------------------------
-// requests and units
-// ---------------------------------------------------------------------------
-__device__ __forceinline__ Req request(const AttnArgs& a, int r, int tb, int* bad) {
-  Req q;
-  q.q0 = min(max(a.q_start[r], 0), a.T);
-  const int q1 = min(max(a.q_start[r + 1], q.q0), a.T);
-  q.n = q1 - q.q0;
-  // a length past the table's row is cut there: its tokens before that stay where they are, nodes among them or not
-  const int cap = a.max_pages << a.page_shift;             // at most 2^30
-  const int kv = a.kv_len[r];
-  q.ctx = min(max(kv, q.n) - q.n, cap);
-  q.kv = min(q.ctx + q.n, cap);
-  if (bad && (kv < q.n || kv > cap || q.q0 != a.q_start[r])) *bad = 1;
-  q.tiles = max((q.kv + kTile - 1) / kTile, 1);
-  q.blocks = (q.n + tb - 1) / tb;
-  return q;
-}
-
-// Shared prefixes: the walk goes over the groups, then over the requests.  A group
-// counts as a request whose nodes are all of its requests' rows and whose tokens
-// are the prefix, all of them before the nodes; a request of it keeps the tokens
-// behind the prefix.
-__device__ __forceinline__ Req group_request(const AttnArgs& a, const PrefixGroup& g, int tb) {
-  Req q;
-  q.q0 = min(max(a.q_start[g.begin], 0), a.T);
-  const int q1 = min(max(a.q_start[g.end], q.q0), a.T);
-  q.n = g.pages ? q1 - q.q0 : 0;
-  q.ctx = q.kv = g.pages << a.page_shift;
-  q.tiles = max((q.kv + kTile - 1) / kTile, 1);
-  q.blocks = (q.n + tb - 1) / tb;
-  q.row = g.row;
-  q.skip = 0;
-  q.flags = kPrefix;
-  return q;
-}
-__device__ __forceinline__ Req own_request(const AttnArgs& a, int r, int pages, int tb, int* bad) {
-  Req q = request(a, r, tb, bad);
-  q.row = r;
-  q.skip = q.flags = 0;
-  const int prefix = pages << a.page_shift;    // at most the row's tokens
-  if (pages && q.ctx >= prefix) {              // (a shorter context has the prefix in its own row alone)
-    q.ctx -= prefix;
-    q.kv -= prefix;
-    q.tiles = max((q.kv + kTile - 1) / kTile, 1);
-    q.skip = pages;
-    q.flags = kJoined;
-  }
-  return q;
-}
-
-// Where the partials of a token's rows of one unit are: `parts` 0: nowhere (the
-// output is written), 1: whole, by the rows' own numbers; more: the slots of that
-// many runs from `run` on, as attention_join_kernel has them
-struct PartsOf {
-  int parts, run, row, joined;                 // row: the token's first row of the unit's tile
-};
-static_assert(sizeof(PartsOf) == sizeof(int4), "a record a token");
 
 // order of a piece's tiles in the ring: K0, K1, [K2, V0], [K3, V1], ..., V(n-2), V(n-1)
 __device__ __forceinline__ int v_item(int j, int n) {
   return j >= n - 2 ? 2 * n - (n - j) : 2 * j + 3;
 }
 
-// SHARED: groups of requests with a common prefix (`group_request`, above)
-template <int DP, bool SHARED>
+template <int DP>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a, int tb) {
   using X = Geo<DP>;
@@ -404,9 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t ring = q_smem + X::SLOT;
   uint8_t* ring_ptr = q_ptr + X::SLOT;
   Small& sm = *reinterpret_cast<Small*>(ring_ptr + X::RING);
-  const int groups_n = SHARED ? a.n_groups : 0, walk_n = groups_n + a.R;
-  int* prefix = reinterpret_cast<int*>(&sm + 1);           // [walk_n + 1]
-  int* skip = prefix + walk_n + 1;                         // [R] (SHARED) pages of the request's group's prefix
+  int* prefix = reinterpret_cast<int*>(&sm + 1);           // [R + 1]
   volatile int* abort_flag = &sm.abort;
   int32_t* err = &a.hdr->err;
 
@@ -447,17 +180,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   pdl_wait();
-  // a step of the walk, once the pages of the groups' prefixes are in `skip`
-  auto at_walk = [&](int v, int* bad) {
-    if constexpr (SHARED) {
-      if (v < groups_n)
-        return group_request(
-            a, prefix_group(a.group_start, a.prefix_row, a.prefix_len, v, a.R, a.max_pages, a.page_shift, bad), tb);
-      return own_request(a, v - groups_n, skip[v - groups_n], tb, bad);
-    } else {
-      return request(a, v, tb, bad);
-    }
-  };
   // cost before each request: its units' tiles and fixed costs; this CTA's run of the total, and the request that
   // the run begins in (with what its thread has read of it)
   int total, runs, share, extra;
@@ -465,31 +187,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto run_start = [&](int c) { return c * share + min(c, extra); };
   {
     int bad = 0;
-    if constexpr (SHARED) {
-      // group starts into the ring's memory, for each request's search
-      int* start = reinterpret_cast<int*>(ring_ptr);
-      for (int g = threadIdx.x; g <= groups_n; g += kThreads) start[g] = a.group_start[g];
-      __syncthreads();
-      for (int r = threadIdx.x; r < a.R; r += kThreads) {
-        const int g = group_of(start, groups_n, r);
-        int pages = 0;
-        if (g >= 0) {
-          const PrefixGroup p = prefix_group(a.group_start, a.prefix_row, a.prefix_len, g, a.R, a.max_pages, a.page_shift,
-                                             nullptr);
-          if (r < p.end) pages = p.pages;
-        }
-        skip[r] = pages;
-      }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncthreads();
-    }
-    const int per = (walk_n + kThreads - 1) / kThreads, r0 = min((int)threadIdx.x * per, walk_n),
-              r1 = min(r0 + per, walk_n);
+    const int per = (a.R + kThreads - 1) / kThreads, r0 = min((int)threadIdx.x * per, a.R), r1 = min(r0 + per, a.R);
     auto cost = [&](const Req& q) { return (q.tiles + kAttnPieceCost) * q.blocks * a.Hkv; };
     Req q;
     int64_t local = 0;                                     // (one request's cost fits 31 bits; row starts that are no
     for (int r = r0; r < r1; ++r) {                        // prefix sums may not add up to so few)
-      q = at_walk(r, &bad);
+      q = request(a, r, tb, &bad);
       local += cost(q);
     }
     int64_t x = local;
@@ -518,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     extra = total - share * runs;
     const int begin = run_start(blockIdx.x);
     for (int r = r0; r < r1; ++r) {
-      if (per > 1) q = at_walk(r, nullptr);
+      if (per > 1) q = request(a, r, tb, nullptr);
       prefix[r] = run;
       const int next = run + cost(q);
       if (run <= begin && begin < next) {
@@ -527,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       run = next;
     }
-    if (threadIdx.x == 0) prefix[walk_n] = total;
+    if (threadIdx.x == 0) prefix[a.R] = total;
     if (bad && blockIdx.x == 0) set_error(err, MOE_DEVERR_CACHE);
   }
   tc_fence_before();
@@ -537,7 +240,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool idle = (int)blockIdx.x >= runs;
   const int begin = idle ? 0 : run_start(blockIdx.x), end = idle ? 0 : run_start(blockIdx.x + 1);
 
-  auto table_of = [&](const Piece& p) { return a.block_table + (int64_t)p.r * a.max_pages + (SHARED ? p.skip : 0); };
   // the next piece of the queue, for every warp but the one that fills it
   int taken = 0;
   auto next = [&](Piece& p) {
@@ -567,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       p.flags = kLast;
       if (!last) {
         while (prefix[r + 1] <= pos) ++r;
-        if (have != r) q = at_walk(r, nullptr);
+        if (have != r) q = request(a, r, tb, nullptr);
         have = r;
         const int per = q.tiles + kAttnPieceCost, u = (pos - prefix[r]) / per, off = pos - prefix[r] - u * per;
         const int len = min(per - off, end - pos), t0 = max(off - kAttnPieceCost, 0);
@@ -575,8 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int unit_end = pos - off + per;
         pos += len;
         if (t1 <= t0) continue;                            // the fixed cost alone
-        p.r = SHARED ? q.row : r;
-        p.skip = SHARED ? q.skip : 0;
+        p.r = r;
         p.h = u / q.blocks;
         p.tok0 = (u - p.h * q.blocks) * tb;
         p.ntok = min(tb, q.n - p.tok0);
@@ -586,7 +287,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         p.t0 = t0;
         p.flags = (t0 == 0 ? kStarts : 0) | (t1 == q.tiles ? kEnds : 0);
         p.parts = p.flags == kStarts ? owner(unit_end - 1) - (int)blockIdx.x + 1 : 0;
-        if (SHARED) p.flags |= q.flags;
         if (!a.tree_mask) t1 = min(t1, (q.ctx + p.tok0 + p.ntok + kTile - 1) / kTile);
         p.n = max(t1 - t0, 0);
       }
@@ -630,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (Piece p; ok && next(p);) {
       if (p.n == 0) continue;
-      const int32_t* table = table_of(p);
+      const int32_t* table = a.block_table + (int64_t)p.r * a.max_pages;
       // page of this lane's box of tile j (of the piece); -1: nothing to load
       auto page_of = [&](int j) {
         const int tok = (p.t0 + j) * kTile + lane * rows;
@@ -971,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // p v of the nodes whose V is not finite
           if (!wait(sm.pv_done[b], (uint32_t)((tiles + j) >> 1) & 1u)) break;
           tc_fence_after();
-          add_odd(a, table_of(p), p.h, (p.t0 + j) * kTile, odd, 64 * w, tmem + lane_addr + X::p_col(b),
+          add_odd(a, a.block_table + (int64_t)p.r * a.max_pages, p.h, (p.t0 + j) * kTile, odd, 64 * w, tmem + lane_addr + X::p_col(b),
                   tmem + lane_addr + X::O);
           tc_fence_before();
           __syncwarp();
@@ -990,11 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait(sm.meet, meets & 1)) break;    // both halves' sums are there (and odd nodes are added)
       ++meets;
       tc_fence_after();
-      const bool uncut = (p.flags & (kStarts | kEnds)) == (kStarts | kEnds);
-      const bool whole = uncut && !(SHARED && p.flags & (kPrefix | kJoined));
-      // (SHARED) partials of uncut units, by the rows' own numbers
-      const int which = p.flags & kPrefix ? 0 : 1;
-      const int64_t rows_all = (int64_t)a.T * a.G, rows_at = (int64_t)(which * a.Hkv + p.h) * rows_all + p.row0 * a.G + row;
+      const bool whole = (p.flags & (kStarts | kEnds)) == (kStarts | kEnds);
       const int slot = 2 * (int)blockIdx.x + (p.flags & kStarts ? 1 : 0);
       if (live_warp) {
         const float sum = sums[0][row] + sums[1][row];
@@ -1034,29 +730,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else if (mine) {
             // partials: [four columns][row]
             float* out = a.part + (int64_t)slot * kAttnRows * kAttnPartDim + ((c0 / 4) * kAttnRows + row) * 4;
-            int64_t step = 4 * kAttnRows;
-            if (SHARED && uncut) {
-              out = a.rows_part + ((int64_t)(which * a.Hkv + p.h) * (DP / 4) + c0 / 4) * rows_all * 4 +
-                    ((int64_t)p.row0 * a.G + row) * 4;
-              step = 4 * rows_all;
-            }
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<float4*>(out + i * step) =
+              *reinterpret_cast<float4*>(out + 4 * i * kAttnRows) =
                   make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
           }
         }
         if (mine && w == 0) {
-          if (SHARED && uncut && !whole) a.rows_ml[rows_at] = make_float2(mc, sum);
-          else if (!whole) a.part_ml[slot * kAttnRows + row] = make_float2(mc, sum);
+          if (!whole) a.part_ml[slot * kAttnRows + row] = make_float2(mc, sum);
           else if (a.lse) a.lse[tok * a.H + head] = sum == 0.f ? -INFINITY : (mc + log2f(sum)) * 0.6931471805599453f;
         }
       }
-      if (SHARED && p.flags & kStarts) {
-        for (int i = threadIdx.x; i < p.ntok; i += 32 * kSoftWarps)
-          a.parts_of[(int64_t)(which * a.Hkv + p.h) * a.T + p.row0 + i] =
-              make_int4(whole ? 0 : uncut ? 1 : p.parts, (int)blockIdx.x, i * a.G, p.flags & kJoined);
-      } else if (p.parts) {
+      if (p.parts) {
         if (threadIdx.x == 0) a.joins[blockIdx.x] = make_int4(p.parts, p.row0, p.ntok, p.h);
         joins = true;
       }
@@ -1067,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // a warp that gave up lets its partner through (which then sees the abort flag before it waits again)
     if (*abort_flag) pair_arrive(qd);
-    if (!SHARED && threadIdx.x == 0 && !joins) a.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (threadIdx.x == 0 && !joins) a.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
   }
   tc_fence_before();
   __syncthreads();
@@ -1138,107 +823,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 2) attention_join_kernel(cons
                               (int64_t)(u.w * a.G + r2 % a.G) * a.D + 4 * c) = s_out[r][c];
 }
 
-// The same for shared prefixes: a block has 32 of a KV head's T * G rows, a lane a
-// row, a warp four columns.  A row's partials are those of its group's prefix, in
-// run order, then those of its own tokens (`parts_of`).
-__global__ void __launch_bounds__(32 * kJoinWarps, 2) prefix_join_kernel(const AttnArgs a, int ctas, int dp) {
-  pdl_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.x % a.Hkv;
-  const int64_t rows_all = (int64_t)a.T * a.G, row0 = (int64_t)(blockIdx.x / a.Hkv) * 32, rg = row0 + lane;
-  const int tok = (int)min(rg / a.G, (int64_t)a.T - 1), head = (int)(rg - (int64_t)tok * a.G);
-  const int live = a.R > 0 ? min(max(a.q_start[a.R], 0), a.T) : 0;
-  const PartsOf none = {0, 0, 0, 0};
-  auto parts_of = [&](int which) {
-    const int4 x = a.parts_of[(int64_t)(which * a.Hkv + h) * a.T + tok];
-    // (bad row starts leave a token without a unit: what stands there then is not followed)
-    const bool good = x.x >= 0 && x.y >= 0 && x.x <= ctas && x.y <= ctas - x.x && x.z >= 0 && x.z <= kAttnRows - a.G;
-    return good ? PartsOf{x.x, x.y, x.z, x.w} : none;
-  };
-  const PartsOf own = rg < rows_all && tok < live ? parts_of(1) : none;
-  if (!__any_sync(0xffffffffu, own.parts != 0)) return;
-  const PartsOf pre = own.parts && own.joined ? parts_of(0) : none;
-  __shared__ uint2 s_out[32][kJoinWarps + 1];
-  // partial k of the row
-  auto locate = [&](int k, const float2*& m, const float4*& v) {
-    const int which = k < pre.parts ? 0 : 1;
-    const PartsOf p = which ? own : pre;
-    if (which) k -= pre.parts;
-    if (p.parts == 1) {
-      const int64_t unit = which * a.Hkv + h;
-      m = a.rows_ml + unit * rows_all + rg;
-      v = reinterpret_cast<const float4*>(a.rows_part) + (unit * (dp / 4) + warp) * rows_all + rg;
-    } else {
-      const int slot = 2 * (p.run + k) + (k == 0 ? 1 : 0), row = p.row + head;
-      m = a.part_ml + slot * kAttnRows + row;
-      v = reinterpret_cast<const float4*>(a.part) + ((int64_t)slot * (kAttnPartDim / 4) + warp) * kAttnRows + row;
-    }
-  };
-  const int n = own.parts + pre.parts;
-  float top = -INFINITY, sum = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int p = 0; p < n; p += kJoinAhead) {
-    float2 m[kJoinAhead];
-    float4 v[kJoinAhead];
-#pragma unroll
-    for (int k = 0; k < kJoinAhead; ++k) {
-      m[k] = make_float2(0.f, 0.f);
-      v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (p + k < n) {
-        const float2* ml;
-        const float4* at;
-        locate(p + k, ml, at);
-        m[k] = *ml;
-        v[k] = *at;
-      }
-    }
-    float t = top;
-#pragma unroll
-    for (int k = 0; k < kJoinAhead; ++k)
-      if (m[k].y != 0.f) t = fmaxf(t, m[k].x);
-    const float g = sum == 0.f ? 0.f : ex2(top - t);
-    top = t;
-    sum *= g;
-    acc = make_float4(acc.x * g, acc.y * g, acc.z * g, acc.w * g);
-#pragma unroll
-    for (int k = 0; k < kJoinAhead; ++k) {
-      if (m[k].y == 0.f) continue;             // no visible key in that part
-      const float f = ex2(m[k].x - top);
-      sum = fmaf(m[k].y, f, sum);
-      acc.x = fmaf(v[k].x, f, acc.x);
-      acc.y = fmaf(v[k].y, f, acc.y);
-      acc.z = fmaf(v[k].z, f, acc.z);
-      acc.w = fmaf(v[k].w, f, acc.w);
-    }
-  }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  s_out[lane][warp] = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-  if (a.lse && warp == 0 && n)
-    a.lse[(int64_t)tok * a.H + h * a.G + head] =
-        sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
-  const uint32_t mine = __ballot_sync(0xffffffffu, n != 0);    // the same in every warp
-  __syncthreads();
-  const int per_row = a.D / 4;                 // warps of the block
-  const int r = threadIdx.x / per_row, c = threadIdx.x - r * per_row;
-  const int64_t r2 = row0 + r;
-  if (mine >> r & 1u)
-    *reinterpret_cast<uint2*>(reinterpret_cast<bf16*>(a.out) + r2 / a.G * a.out_ld +
-                              ((int64_t)h * a.G + r2 % a.G) * a.D + 4 * c) = s_out[r][c];
-}
-
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-// BF16 tensor of up to four dims (the first contiguous), 128-byte swizzled boxes 64 wide
-bool make_map(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
-              const cuuint32_t* box) {
-  EncodeTiledFn fn = encode_fn();
-  const cuuint32_t one[4] = {1, 1, 1, 1};
-  return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(ptr), dims, strides, box, one,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-template <int DP, bool SHARED>
+template <int DP>
 cudaError_t launch_dp(const AttnArgs& a, cudaStream_t s) {
   using X = Geo<DP>;
   const int tb = kAttnRows / a.G, page = 1 << a.page_shift;
@@ -1258,24 +846,19 @@ cudaError_t launch_dp(const AttnArgs& a, cudaStream_t s) {
     if (!make_map(&maps.k, a.k, 4, dims, strides, box) || !make_map(&maps.v, a.v, 4, dims, strides, box))
       return cudaErrorInvalidValue;
   }
-  const size_t smem = 1024 + X::SLOT + X::RING + sizeof(Small) +
-                      (SHARED ? (size_t)a.n_groups + 2 * (size_t)a.R + 1 : (size_t)a.R + 1) * 4;
+  const size_t smem = 1024 + X::SLOT + X::RING + sizeof(Small) + ((size_t)a.R + 1) * 4;
   static_assert(1024 + X::SLOT + X::RING + sizeof(Small) + 4097 * 4 <= kMaxSmem, "shared memory");
-  static_assert(1024 + X::SLOT + X::RING + sizeof(Small) + (3 * kPrefixMaxRequests + 1) * 4 <= kMaxSmem, "shared memory");
   static PerDeviceOnce once;
   int sms = 0;
   cudaError_t e = once.run(
       [](int& v) {
         v = std::min(num_sms(), kAttnMaxCtas);
-        return cudaFuncSetAttribute(attention_tc_kernel<DP, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+        return cudaFuncSetAttribute(attention_tc_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
       },
       &sms);
   if (e != cudaSuccess) return e;
-  e = launch_k(attention_tc_kernel<DP, SHARED>, dim3((unsigned)sms), dim3(kThreads), smem, s, maps, a, tb);
+  e = launch_k(attention_tc_kernel<DP>, dim3((unsigned)sms), dim3(kThreads), smem, s, maps, a, tb);
   if (e != cudaSuccess) return e;
-  if (SHARED)
-    return launch_k(prefix_join_kernel, dim3((unsigned)(ceil_div((int64_t)a.T * a.G, 32) * a.Hkv)),
-                    dim3(32 * (a.D / 4)), 0, s, a, sms, DP);
   return launch_k(attention_join_kernel, dim3((unsigned)sms, (unsigned)ceil_div(std::min(tb, a.T) * a.G, 32)), dim3(32 * (a.D / 4)), 0,
                   s, a);
 }
@@ -1284,12 +867,7 @@ cudaError_t launch_dp(const AttnArgs& a, cudaStream_t s) {
 
 cudaError_t launch_attention_bf16(const AttnArgs& a, cudaStream_t s) {
   if (a.T <= 0) return cudaSuccess;
-  return a.D <= 64 ? launch_dp<64, false>(a, s) : launch_dp<128, false>(a, s);
-}
-
-cudaError_t launch_prefix_attention_bf16(const AttnArgs& a, cudaStream_t s) {
-  if (a.T <= 0) return cudaSuccess;
-  return a.D <= 64 ? launch_dp<64, true>(a, s) : launch_dp<128, true>(a, s);
+  return a.D <= 64 ? launch_dp<64>(a, s) : launch_dp<128>(a, s);
 }
 
 }  // namespace moe

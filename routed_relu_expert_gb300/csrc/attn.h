@@ -23,12 +23,19 @@ static_assert(sizeof(AttnHeader) == MOE_ATTN_HEADER_BYTES, "attention workspace 
 // FP32 output sums ([four columns][row]) and, after all of them, (max, sum).
 constexpr int kAttnMaxCtas = 160;
 constexpr int kAttnRows = 128;
+constexpr int kAttnTile = 128;             // keys a tile
 constexpr int kAttnPartDim = 128;
 // A unit's fixed cost beside its key tiles, in tiles: a piece of a run takes 3 to 4
 // us beside 0.8 to 1.2 us a tile.  Cost 2, 3, 4, 5 measured on large trees over short
 // and long contexts: 110, 97, 92, 92 us; flat for 64 requests of up to 8,000 tokens.
 constexpr int kAttnPieceCost = 4;
 constexpr int kPrefixMaxRequests = 2048;   // of a call with shared prefixes (and as many groups)
+// The kernel for few rows: blocks of a call whose keys are split over several, row
+// blocks of 16 a block, and keys that one block is given at most.
+constexpr int kFewCtas = 1024;
+constexpr int kFewRows = 16, kFewBlocks = 2;
+constexpr int kFewKeys = 1024;
+constexpr int kFewMaxSplits = 32;
 constexpr size_t kAttnPartSlots = 2 * kAttnMaxCtas;
 constexpr size_t kAttnPartBytes = kAttnPartSlots * kAttnRows * (kAttnPartDim + 2) * 4;
 constexpr size_t kAttnJoinBytes = kAttnMaxCtas * 16;   // a record a run: what the join kernel adds
@@ -120,9 +127,15 @@ struct AttnArgs {
   // shared prefixes (n_groups 0: none)
   const int32_t *group_start, *prefix_row, *prefix_len;
   int n_groups;
-  float* rows_part;         // [prefix or own][KV head][columns / 4][T * G rows][4]: output sums of whole units
+  float* rows_part;         // [prefix or own][KV head][T * G rows][64 or 128]: output sums of whole units
   float2* rows_ml;          // [prefix or own][KV head][T * G rows] their (max, sum)
   int4* parts_of;           // [prefix or own][KV head][T]: where a token's partials are (PartsOf)
+  // the kernel for few rows: what it takes (0 tokens: nothing), splits of a unit's keys, whether it runs alone
+  int few_tokens, few_keys, few_splits, few_alone;
+  float* few_part;          // [kFewCtas * kFewBlocks slots][16 rows][64 or 128]
+  float2* few_ml;           // [slots][16 rows] (max, sum)
+  float* pair_part;         // [kAttnPartSlots slots][2 x 128 rows][64 or 128]: units that a run's end cuts
+  float2* pair_ml;          // [slots][rows] (max, sum)
 };
 
 // A group of requests that share a prefix: its tokens, whole pages of them, are read through one row of the table.
@@ -163,5 +176,6 @@ cudaError_t launch_attention_bf16(const AttnArgs& a, cudaStream_t s);
 // the same with shared prefixes
 cudaError_t launch_prefix_attention_f32(const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_prefix_attention_bf16(const AttnArgs& a, cudaStream_t s);
+cudaError_t launch_attention_few(const AttnArgs& a, cudaStream_t s);
 
 }  // namespace moe

@@ -79,7 +79,7 @@ int log2_of(int v) {
 
 // the partials of a call with shared prefixes, behind the workspace of the other calls (bytes)
 struct PrefixLayout {
-  size_t part, ml, parts_of, end;
+  size_t part, ml, parts_of, few_part, few_ml, pair_part, pair_ml, end;
 };
 PrefixLayout prefix_layout(const moe_attn_config_t* c, int64_t T) {
   const size_t rows = (size_t)T * c->n_heads, dp = c->head_dim <= 64 ? 64 : 128;
@@ -87,7 +87,11 @@ PrefixLayout prefix_layout(const moe_attn_config_t* c, int64_t T) {
   l.part = (workspace_bytes(c) + 255) / 256 * 256;
   l.ml = l.part + 2 * rows * dp * 4;
   l.parts_of = l.ml + 2 * rows * 8;
-  l.end = l.parts_of + 2 * (size_t)T * c->n_kv_heads * 16;
+  l.few_part = l.parts_of + 2 * (size_t)T * c->n_kv_heads * 16;
+  l.few_ml = l.few_part + (size_t)kFewCtas * kFewBlocks * kFewRows * dp * 4;
+  l.pair_part = l.few_ml + (size_t)kFewCtas * kFewBlocks * kFewRows * 8;
+  l.pair_ml = l.pair_part + kAttnPartSlots * 2 * kAttnRows * dp * 4;
+  l.end = l.pair_ml + kAttnPartSlots * 2 * kAttnRows * 8;
   return l;
 }
 
@@ -438,6 +442,10 @@ moe_status_t moe_prefix_attention(const moe_attn_config_t* cfg, int32_t R, int32
   a.rows_part = reinterpret_cast<float*>(base + l.part);
   a.rows_ml = reinterpret_cast<float2*>(base + l.ml);
   a.parts_of = reinterpret_cast<int4*>(base + l.parts_of);
+  a.few_part = reinterpret_cast<float*>(base + l.few_part);
+  a.few_ml = reinterpret_cast<float2*>(base + l.few_ml);
+  a.pair_part = reinterpret_cast<float*>(base + l.pair_part);
+  a.pair_ml = reinterpret_cast<float2*>(base + l.pair_ml);
   return launched(launch_prefix_attention_bf16(a, (cudaStream_t)stream));
 }
 
