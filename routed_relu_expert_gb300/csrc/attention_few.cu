@@ -6,16 +6,19 @@
 // The tiles of the tensor-memory kernel have 128 rows, and a piece of a run costs it 3 to
 // 4 us beside its tiles: a request with a few rows and a few hundred tokens of
 // its own behind the prefix is mostly that cost.  Here a unit (request or group, KV head,
-// split of the keys) is a block of four warps that work for themselves: each takes
-// 16 keys of every 64, its own K and V by cp.async into its own buffers, its own running
+// split of the keys) is a block of four or eight warps that work for themselves: each takes
+// 16 keys of every 64 or 128, its own K and V by cp.async into its own stages, its own running
 // maximum and sum, products by mma.sync (16 rows, 16 keys); they meet once, at the end.
 // Several blocks an SM hide one another's waits.  The arithmetic is the other kernel's:
 // probabilities in BF16 for the second product, sums before that rounding, the reference
 // follows the maximum only past 2^8.
 //
-// Where the rows' prefix was another kernel's and the keys are not split, the
-// block adds the prefix's partials itself and writes the output; else the partials
-// go to the join.
+// Where the rows' prefix is the other kernel's and the keys are not split, the warps
+// start from the prefix's partials in place of nothing, and the block writes the
+// output; else its partials go to the join.
+//
+// The other kernel lets this one's blocks start as its own ones end; what they need of it,
+// the prefix's partials, they wait for once their first keys are on the way.
 //
 // Bound: HBM, where there are enough units; else the latency of a block (table, keys,
 // softmax, the join of the warps).
@@ -27,9 +30,8 @@ namespace moe {
 
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kSub = 16;                       // keys of a warp at a time
+constexpr int kStages = 2;                     // 16 keys each, of a warp
 constexpr float kRaise = 8.f;                  // log2 units by which a maximum may pass its reference
 
 __device__ __forceinline__ float ex2(float x) {
@@ -64,25 +66,30 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
                : "memory");
 }
 
-template <int DP>
+template <int DP, int kWarps>
 struct Geo {
   static constexpr int CH = DP / 8;                          // 16-byte chunks of a head
   static constexpr int TILE = kSub * DP * 2;                 // 16 keys of K or V
-  static constexpr int RING = 3 * TILE;                      // of a warp: K, and V twice
+  static constexpr int RING = 2 * kStages * TILE;            // of a warp: K and V of a stage
   static constexpr int ROW = DP + 4;                         // floats of a row in the join (four banks apart)
   static constexpr int SMEM = kWarps * RING > kWarps * kFewRows * ROW * 4 ? kWarps * RING : kWarps * kFewRows * ROW * 4;
 };
 
-template <int DP>
-__global__ void __launch_bounds__(kThreads, 4) attention_few_kernel(const AttnArgs a) {
-  using X = Geo<DP>;
+// kWarps: 4, three blocks an SM; or 8, where there are fewer units than SMs have blocks
+template <int DP, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, kWarps == 4 ? 3 : 1) attention_few_kernel(const AttnArgs a) {
+  using X = Geo<DP, kWarps>;
+  constexpr int kThreads = 32 * kWarps;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float s_m[kWarps][kFewRows], s_l[kWarps][kFewRows];
   __shared__ int s_pages, s_merge;
   __shared__ __align__(128) uint4 s_q[kFewRows * X::CH];
-  pdl_wait();
+  if (a.few_alone) pdl_wait();                 // (else the other kernel has waited, and let this one start)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int unit = blockIdx.x / a.few_splits, split = blockIdx.x - unit * a.few_splits;
+  // eight warps: a block a row block; four: a block takes them one after the other
+  constexpr int kApart = kWarps == 8 ? kFewBlocks : 1;
+  const int part = blockIdx.x / kApart, rb0 = blockIdx.x - part * kApart;
+  const int unit = part / a.few_splits, split = part - unit * a.few_splits;
   const int walk = unit / a.Hkv, h = unit - walk * a.Hkv;
   const int tb = kFewRows / a.G;               // tokens of a row block
   int bad = 0;
@@ -106,42 +113,45 @@ __global__ void __launch_bounds__(kThreads, 4) attention_few_kernel(const AttnAr
   } else {
     // the request's group, every thread looking at some
     const int r = walk - a.n_groups;
+    if (tid == 0) s_pages = 0;
     q = own_request(a, r, 0, tb, &bad);
     if (a.n_groups > 0) {
-      if (tid == 0) s_pages = 0;
       __syncthreads();
+      PrefixGroup p;
+      bool found = false;
       for (int i = tid; i < a.n_groups; i += kThreads) {
-        const PrefixGroup p = prefix_group(a.group_start, a.prefix_row, a.prefix_len, i, a.R, a.max_pages, a.page_shift,
+        const PrefixGroup x = prefix_group(a.group_start, a.prefix_row, a.prefix_len, i, a.R, a.max_pages, a.page_shift,
                                            nullptr);
         // (of the groups that begin at or before r the last one counts, whatever its end)
-        if (a.group_start[i] <= r && (i + 1 == a.n_groups || a.group_start[i + 1] > r) && r < p.end && p.pages) {
-          s_pages = p.pages;
-          s_merge = !few(a, group_request(a, p, tb));
+        if (a.group_start[i] <= r && (i + 1 == a.n_groups || a.group_start[i + 1] > r) && r < x.end && x.pages) {
+          p = x;
+          found = true;
+          s_pages = x.pages;
         }
       }
       __syncthreads();
-      const int pages = s_pages, prefix = pages << a.page_shift;
-      if (pages && q.ctx >= prefix) {          // as own_request
-        q.ctx -= prefix;
-        q.kv -= prefix;
-        q.skip = pages;
-        q.flags = kJoined;
-        merge = s_merge;
-      }
+      behind_prefix(a, q, s_pages);
+      if (found) s_merge = !few(a, group_request(a, p, tb));     // (read behind the next barrier)
     }
   }
   if (bad && h == 0 && split == 0 && tid == 0) set_error(&a.hdr->err, MOE_DEVERR_CACHE);
-  if (q.n == 0 || !few(a, q)) return;
-  // this block's keys: tiles of 64, the same number a split
+  if (rb0 >= q.blocks || !few(a, q)) {
+    if (blockIdx.x == 0) pdl_wait();           // this kernel does not end before the other
+    return;
+  }
+  // this block's keys: tiles of 16 a warp, the same number a split
   constexpr int kTile = kSub * kWarps;
   const int tiles = max((q.kv + kTile - 1) / kTile, 1), per = (tiles + a.few_splits - 1) / a.few_splits;
   const int parts = (tiles + per - 1) / per;
-  if (split >= parts) return;
+  if (split >= parts) {
+    if (blockIdx.x == 0) pdl_wait();
+    return;
+  }
   const int sub0 = split * per * kWarps + warp, sub1 = min((split + 1) * per, tiles) * kWarps;
   const int32_t* table = a.block_table + (int64_t)q.row * a.max_pages + q.skip;
   const bf16 *kc = reinterpret_cast<const bf16*>(a.k) + (int64_t)h * a.head_stride,
              *vc = reinterpret_cast<const bf16*>(a.v) + (int64_t)h * a.head_stride;
-  const uint32_t kt = (uint32_t)__cvta_generic_to_shared(smem) + warp * X::RING;
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * X::RING;
   const uint32_t q_smem = (uint32_t)__cvta_generic_to_shared(s_q);
   const float c = a.scale * 1.4426950408889634f;
   const int g = lane >> 2, t4 = lane & 3;      // the row (and + 8) and the pair of columns that a lane has of a product
@@ -156,37 +166,47 @@ __global__ void __launch_bounds__(kThreads, 4) attention_few_kernel(const AttnAr
     }
     return (int64_t)pg * a.page_stride + (int64_t)(key & ((1 << a.page_shift) - 1)) * a.token_stride;
   };
-  // 16 keys of a cache into a buffer; at: a lane's key (both halves of the warp have all 16)
-  auto copy = [&](const bf16* cache, uint32_t dst, int64_t at) {
+  // 16 keys into a stage; at: a lane's key (both halves of the warp have all 16)
+  auto copy = [&](int stage, int64_t at) {
     constexpr int KEYS = 32 / X::CH;           // keys of a step of the warp
+    const uint32_t dst = ring + stage * 2 * X::TILE;
     const int ch = lane % X::CH;
 #pragma unroll
     for (int s = 0; s < kSub / KEYS; ++s) {
       const int key = s * KEYS + lane / X::CH;
       const int64_t off = __shfl_sync(0xffffffffu, at, key);
       const int bytes = off >= 0 && ch * 8 < a.D ? 16 : 0;
-      copy16(dst + key * DP * 2 + ((ch ^ (key & 7)) << 4), cache + (bytes ? off + ch * 8 : 0), bytes);
+      const int64_t from = bytes ? off + ch * 8 : 0;
+      const uint32_t to = dst + key * DP * 2 + ((ch ^ (key & 7)) << 4);
+      copy16(to, kc + from, bytes);
+      copy16(to + X::TILE, vc + from, bytes);
     }
     copy_commit();
   };
+  // a lane's key of the warp's 16 from `sub` on
+  auto keys = [&](int sub) -> int64_t { return sub < sub1 ? place(sub * kSub + (lane & 15)) : -1; };
 
-  for (int rb = 0; rb < q.blocks; ++rb) {
+  for (int rb = rb0; rb < q.blocks; rb += kApart) {
     const int tok0 = q.q0 + rb * tb, ntok = min(tb, q.n - rb * tb), valid = ntok * a.G;
-    int64_t at = sub0 < sub1 ? place(sub0 * kSub + (lane & 15)) : -1;
-    copy(kc, kt, at);
-    copy(vc, kt + X::TILE, at);
-    at = sub0 + kWarps < sub1 ? place((sub0 + kWarps) * kSub + (lane & 15)) : -1;
     // Q, read again for every 16 keys (in registers it would cost a block an SM)
-    __syncthreads();
     for (int i = tid; i < kFewRows * X::CH; i += kThreads) {
       const int row = i / X::CH, ch = i - row * X::CH, tk = row / a.G;
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (row < valid && ch * 8 < a.D)
-        x = *reinterpret_cast<const uint4*>(reinterpret_cast<const bf16*>(a.q) + (int64_t)(tok0 + tk) * a.q_ld +
-                                            (int64_t)(h * a.G + row - tk * a.G) * a.D + 8 * ch);
-      s_q[row * X::CH + (ch ^ (row & 7))] = x;
+      const bool in = row < valid && ch * 8 < a.D;
+      copy16(q_smem + row * DP * 2 + ((ch ^ (row & 7)) << 4),
+             reinterpret_cast<const bf16*>(a.q) +
+                 (in ? (int64_t)(tok0 + tk) * a.q_ld + (int64_t)(h * a.G + row - tk * a.G) * a.D + 8 * ch : 0),
+             in ? 16 : 0);
     }
-    __syncthreads();
+    copy_commit();
+    int64_t at[kStages];
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) at[i] = keys(sub0 + i * kWarps);
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) copy(i, at[i]);
+    int64_t next = keys(sub0 + kStages * kWarps);
+    copy_wait<kStages>();
+    __syncthreads();                           // Q is there, and the word on the prefix
+    merge = parts == 1 && q.flags & kJoined && s_merge;
     float o[DP / 8][4];
 #pragma unroll
     for (int i = 0; i < DP / 8; ++i)
@@ -194,12 +214,64 @@ __global__ void __launch_bounds__(kThreads, 4) attention_few_kernel(const AttnAr
       for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
     float mc[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
-    int turn = 0;                              // the V buffer
+    if (!a.few_alone) pdl_wait();
+    if (merge) {
+      // a warp starts from every kWarps'th of the prefix's partials
+      PartsOf pre[2];
+      int hd[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int row = g + 8 * i, tk = row / a.G;
+        hd[i] = row - tk * a.G;
+        pre[i] = parts_of(a, 0, h, tok0 + min(tk, ntok - 1));
+        if (row >= valid) pre[i].parts = 0;
+      }
+      float2 x[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (warp < pre[i].parts) {
+          const float2* ml;
+          const float4* from;
+          partial<DP>(a, pre[i], 0, h, tok0 * a.G + g + 8 * i, hd[i], warp, ml, from);
+          x[i] = __ldcg(ml);
+#pragma unroll
+          for (int j = 0; j < DP / 8; ++j) {
+            const float2 y = __ldcg(reinterpret_cast<const float2*>(from) + t4 + 4 * j);
+            o[j][2 * i] = y.x;
+            o[j][2 * i + 1] = y.y;
+          }
+        }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (x[i].y != 0.f) {                   // (a part without a visible key has zeros)
+          mc[i] = x[i].x;
+          l[i] = t4 == 0 ? x[i].y : 0.f;       // (the lanes of a row are added up at the end)
+        }
+#pragma unroll 1
+        for (int k = warp + kWarps; k < pre[i].parts; k += kWarps) {
+          const float2* ml;
+          const float4* from;
+          partial<DP>(a, pre[i], 0, h, tok0 * a.G + g + 8 * i, hd[i], k, ml, from);
+          const float2 z = __ldcg(ml);
+          if (z.y == 0.f) continue;
+          const float top = fmaxf(mc[i], z.x), f0 = mc[i] == -INFINITY ? 0.f : ex2(mc[i] - top), f1 = ex2(z.x - top);
+          mc[i] = top;
+          l[i] = l[i] * f0 + (t4 == 0 ? z.y * f1 : 0.f);
+#pragma unroll
+          for (int j = 0; j < DP / 8; ++j) {
+            const float2 y = __ldcg(reinterpret_cast<const float2*>(from) + t4 + 4 * j);
+            o[j][2 * i] = o[j][2 * i] * f0 + y.x * f1;
+            o[j][2 * i + 1] = o[j][2 * i + 1] * f0 + y.y * f1;
+          }
+        }
+      }
+    }
+
+    int stage = 0;
     for (int sub = sub0; sub < sub1; sub += kWarps) {
-      const uint32_t vt = kt + X::TILE * (1 + turn);
-      const bool more = sub + kWarps < sub1;
+      const uint32_t kt = ring + stage * 2 * X::TILE, vt = kt + X::TILE;
       const int k0 = sub * kSub;
-      copy_wait<1>();                          // K of these keys (V may still come)
+      copy_wait<kStages - 1>();
       __syncwarp();
       // scores of 16 rows and 16 keys
       float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
@@ -215,16 +287,6 @@ __global__ void __launch_bounds__(kThreads, 4) attention_few_kernel(const AttnAr
           mma_bf16_16816(s[1], x[0], x[1], x[2], x[3], b[2], b[3]);
         }
       }
-      __syncwarp();                            // K is read: the next keys' K comes into its place
-      if (more) {
-        copy(kc, kt, at);
-        copy(vc, kt + X::TILE * (2 - turn), at);
-        at = sub + 2 * kWarps < sub1 ? place((sub + 2 * kWarps) * kSub + (lane & 15)) : -1;
-        copy_wait<2>();                        // this turn's V
-      } else {
-        copy_wait<0>();
-      }
-      __syncwarp();
       uint32_t odd = 0;                        // keys whose V is not finite, nodes among them alone
       if (k0 + kSub > q.ctx) {
         // what each row sees of the nodes
@@ -329,11 +391,13 @@ __global__ void __launch_bounds__(kThreads, 4) attention_few_kernel(const AttnAr
           mma_bf16_16816(o[2 * i + 1], p[0], p[1], p[2], p[3], b[2], b[3]);
         }
       }
-      __syncwarp();                            // V is read before its buffer is filled again
-      turn ^= 1;
+      __syncwarp();                            // the stage is read before it is filled again
+      copy(stage, next);
+      next = keys(sub + (kStages + 1) * kWarps);
+      if (++stage == kStages) stage = 0;
     }
 
-    // ---- the four warps' parts, in warp order ----
+    // ---- the warps' parts, in warp order ----
     copy_wait<0>();
     __syncthreads();
     float* so = reinterpret_cast<float*>(smem);
@@ -365,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 4) attention_few_kernel(const AttnAr
     }
     const int which = q.flags & kPrefix ? 0 : 1;
     const bool whole = parts == 1 && (!q.flags || merge);
-    const int slot = (int)blockIdx.x * kFewBlocks + rb;
+    const int slot = part * kFewBlocks + rb;
     const int rows_all = a.T * a.G, rg = tok0 * a.G + row;
     const int64_t side = which * a.Hkv + h;
     if (row < valid) {
@@ -384,30 +448,6 @@ __global__ void __launch_bounds__(kThreads, 4) attention_few_kernel(const AttnAr
         }
       }
       if (whole) {
-        if (merge) {
-          // the prefix's partials, in order
-          const PartsOf pre = parts_of(a, 0, h, tok0 + tk);
-          for (int k = 0; k < pre.parts; ++k) {
-            const float2* ml;
-            const float4* at_v;
-            partial<DP>(a, pre, 0, h, rg, hd, k, ml, at_v);
-            const float2 x = __ldcg(ml);
-            float4 v[kPer];
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) v[i] = __ldcg(at_v + c0 + kCols * i);
-            if (x.y == 0.f) continue;
-            const float t = fmaxf(top, x.x), f0 = sum == 0.f ? 0.f : ex2(top - t), f1 = ex2(x.x - t);
-            top = t;
-            sum = fmaf(sum, f0, x.y * f1);
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-              acc[i].x = fmaf(acc[i].x, f0, v[i].x * f1);
-              acc[i].y = fmaf(acc[i].y, f0, v[i].y * f1);
-              acc[i].z = fmaf(acc[i].z, f0, v[i].z * f1);
-              acc[i].w = fmaf(acc[i].w, f0, v[i].w * f1);
-            }
-          }
-        }
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         bf16* out = reinterpret_cast<bf16*>(a.out) + (int64_t)(tok0 + tk) * a.out_ld + (int64_t)head * a.D;
 #pragma unroll
@@ -432,26 +472,39 @@ __global__ void __launch_bounds__(kThreads, 4) attention_few_kernel(const AttnAr
   }
 }
 
-template <int DP>
+template <int DP, int kWarps>
 cudaError_t launch_dp(const AttnArgs& a, cudaStream_t s) {
   static PerDeviceOnce once;
   int unused = 0;
   const cudaError_t e = once.run(
       [](int& v) {
         v = 1;
-        return cudaFuncSetAttribute(attention_few_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<DP>::SMEM);
+        return cudaFuncSetAttribute(attention_few_kernel<DP, kWarps>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    Geo<DP, kWarps>::SMEM);
       },
       &unused);
   if (e != cudaSuccess) return e;
   const int64_t units = (int64_t)(a.n_groups + a.R) * a.Hkv;
-  return launch_k(attention_few_kernel<DP>, dim3((unsigned)std::max<int64_t>(units * a.few_splits, 1)), kThreads,
-                  Geo<DP>::SMEM, s, a);
+  return launch_k(attention_few_kernel<DP, kWarps>, dim3((unsigned)std::max<int64_t>(units * a.few_splits * (kWarps == 8 ? kFewBlocks : 1), 1)),
+                  dim3(32 * kWarps), Geo<DP, kWarps>::SMEM, s, a);
 }
 
 }  // namespace
 
+// Few units: blocks of eight warps, their keys split while that leaves SMs without one; else blocks of four.
+void few_shape(AttnArgs* a) {
+  const int64_t units = (int64_t)(a->n_groups + a->R) * a->Hkv, sms = 152;
+  if (a->G > kFewRows) return;                 // (a token's rows do not fit a block's 16)
+  a->few_tokens = kFewBlocks * (kFewRows / a->G);
+  a->few_warps = units < 2 * sms ? 8 : 4;
+  a->few_splits = (int)std::min<int64_t>(std::max<int64_t>(sms / std::max<int64_t>(units, 1), 1), kFewMaxSplits);
+  a->few_keys = a->few_splits * a->few_warps * kFewKeys;
+  a->few_alone = a->T <= a->few_tokens && (int64_t)a->max_pages << a->page_shift <= a->few_keys;
+}
+
 cudaError_t launch_attention_few(const AttnArgs& a, cudaStream_t s) {
-  return a.D <= 64 ? launch_dp<64>(a, s) : launch_dp<128>(a, s);
+  if (a.few_warps == 8) return a.D <= 64 ? launch_dp<64, 8>(a, s) : launch_dp<128, 8>(a, s);
+  return a.D <= 64 ? launch_dp<64, 4>(a, s) : launch_dp<128, 4>(a, s);
 }
 
 }  // namespace moe

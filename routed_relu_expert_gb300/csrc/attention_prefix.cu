@@ -73,7 +73,7 @@ constexpr int kStarts = 1, kEnds = 2, kLast = 4;         // beside kPrefix, kJoi
 struct Small {
   uint64_t full[10], empty[10];
   uint64_t piece_full[kQueue], piece_empty[kQueue];
-  uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], both, first_alone, drain;
+  uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], warm[2], both, first_alone, drain;
   // nodes whose V is not finite: [both groups at it, or the first alone][special tile's parity][half of the head][32 keys]
   uint32_t odd[2][2][2][4];
   Piece piece[kQueue];
@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(sm.s_full[w]), 1);
       mbar_init(bar(sm.p_full[w]), kSoftWarps / 2);
       mbar_init(bar(sm.o_full[w]), 1);
+      mbar_init(bar(sm.warm[w]), kSoftWarps / 2);
     }
     mbar_init(bar(sm.both), kSoftWarps);
     mbar_init(bar(sm.first_alone), kSoftWarps / 2);
@@ -137,6 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   pdl_wait();
+  pdl_release();                               // the kernel for few rows fills the SMs as this one's blocks end
   // a step of the walk, once the pages of the groups' prefixes are in `skip`
   auto at_walk = [&](int v, int* bad) {
     Req q;
@@ -155,29 +157,42 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto run_start = [&](int c) { return c * share + min(c, extra); };
   {
     int bad = 0;
-    // group starts into the ring's memory, for each request's search
-    int* start = reinterpret_cast<int*>(ring_ptr);
-    for (int g = threadIdx.x; g < groups_n; g += kThreads) start[g] = a.group_start[g];
+    // the groups into the ring's memory, for each request's search; a thread's first request beside them
+    int32_t* start = reinterpret_cast<int32_t*>(ring_ptr);
+    int32_t *rows = start + groups_n + 1, *lens = rows + groups_n;
+    for (int g = threadIdx.x; g <= groups_n; g += kThreads) {
+      start[g] = groups_n ? a.group_start[g] : 0;
+      if (g < groups_n) {
+        rows[g] = a.prefix_row[g];
+        lens[g] = a.prefix_len[g];
+      }
+    }
+    const int per = (walk_n + kThreads - 1) / kThreads, v0 = min((int)threadIdx.x * per, walk_n),
+              v1 = min(v0 + per, walk_n);
+    Req q;
+    const bool ahead = v0 < v1 && v0 >= groups_n;
+    if (ahead) q = own_request(a, v0 - groups_n, 0, tb, &bad);
     __syncthreads();
     for (int r = threadIdx.x; r < a.R; r += kThreads) {
       const int g = group_of(start, groups_n, r);
       int pages = 0;
       if (g >= 0) {
-        const PrefixGroup p = prefix_group(a.group_start, a.prefix_row, a.prefix_len, g, a.R, a.max_pages, a.page_shift,
-                                           nullptr);
+        const PrefixGroup p = prefix_group(start, rows, lens, g, a.R, a.max_pages, a.page_shift, nullptr);
         if (r < p.end) pages = p.pages;
       }
       skip[r] = pages;
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
-    const int per = (walk_n + kThreads - 1) / kThreads, v0 = min((int)threadIdx.x * per, walk_n),
-              v1 = min(v0 + per, walk_n);
     auto cost = [&](const Req& q) { return (q.tiles + kPieceCost) * q.blocks * a.Hkv; };
-    Req q;
     int64_t local = 0;                                     // (one step's cost fits 31 bits; row starts that are no
     for (int v = v0; v < v1; ++v) {                        // prefix sums may not add up to so few)
-      q = at_walk(v, &bad);
+      if (v == v0 && ahead) {
+        behind_prefix(a, q, skip[v - groups_n]);
+        if (few(a, q)) q.blocks = 0;
+      } else {
+        q = at_walk(v, &bad);
+      }
       local += cost(q);
     }
     int64_t x = local;
@@ -344,10 +359,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t dst = ring + (uint32_t)(slot * X::SLOT + hh * kHalfBytes);
         if (elect_one()) mbar_expect_tx(b, (uint32_t)((boxes - first + step - 1) / step * 128 * rows));
         __syncwarp();
-        for (int i = first; i < boxes; i += step) {
-          const int pg = __shfl_sync(0xffffffffu, pid, i);
-          if (elect_one()) tma_load_4d(dst + (uint32_t)(i * rows * 128), map, 64 * hh, off, p.h, pg, b);
-        }
+        // (a lane a box: the first tiles of a run are there 3000 cycles sooner than with one lane for all)
+        if (lane < boxes && (step == 1 || (lane & 1) == first))
+          tma_load_4d(dst + (uint32_t)(lane * rows * 128), map, 64 * hh, off, p.h, pid, b);
         __syncwarp();
         ++it;
         if (++slot == NS) {
@@ -382,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int slot = 0, pieces = 0;
     uint32_t phase = 0;
     int tiles[2] = {0, 0};                                 // of all pieces so far, a row tile each
-    bool ok = true, issued = false;
+    bool ok = true, issued = false, warm[2] = {false, false};
     auto wait = [&](uint64_t& b, uint32_t parity) {
       ok = ok && wait_warp(bar(b), parity, abort_flag, err);
       return ok;
@@ -395,6 +409,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // S of row tile w from the K tile in slot k; behind it, what it frees
     auto scores = [&](int w, int k, bool free_k, bool free_q) {
+      if (!warm[w]) {                                      // (below: the group has written its columns for the last time)
+        warm[w] = true;
+        if (!wait(sm.warm[w], 0)) return;
+        tc_fence_after();
+      }
       if (elect_one()) {
         const uint64_t da = smem_desc_sw128(q_smem + (uint32_t)(w * X::SLOT)),
                        db = smem_desc_sw128(ring + (uint32_t)(k * X::SLOT));
@@ -480,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     int tiles = 0, items = 0, pieces = 0, meets_both = 0, meets_alone = 0;
-    bool ok = true;
+    bool ok = true, warm = false;
     auto wait = [&](uint64_t& b, uint32_t parity) {
       ok = wait_warp(bar(b), parity, abort_flag, err);
       return ok;
@@ -502,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (p.n > 0) {
         // the products add to O
         const float zero[32] = {};
-#pragma unroll
+#pragma unroll 1
         for (int c0 = 0; c0 < DP; c0 += 32) st32(o_addr + c0, zero);
         st_wait();
       }
@@ -550,10 +569,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 8; ++i) any |= odd[i >> 2][i & 3];
         return any ? odd : nullptr;
       };
-      for (int j = 0; j < p.n && ok; ++j) {
-        if (!wait(sm.s_full[w], (uint32_t)(tiles + j) & 1u)) break;
+      // Before its first tile a group goes over whatever its columns hold: that fetches the instructions, some 4000
+      // cycles' wait, while the first keys are on their way
+      const bool warms = !warm && p.n > 0;
+      for (int j = warms ? -1 : 0; j < p.n && ok; ++j) {
+        if (j >= 0 && !wait(sm.s_full[w], (uint32_t)(tiles + j) & 1u)) break;
         const int key0 = (p.t0 + j) * kTile;
-        const bool special = key0 + kTile > p.ctx;
+        const bool special = j >= 0 && key0 + kTile > p.ctx;
         const uint32_t(*odd)[4] = nullptr;
         if (__builtin_expect(special, 0)) odd = clean(j);
         if (!ok) break;
@@ -670,6 +692,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         tc_fence_before();
+        if (j < 0) {
+          mc = -INFINITY;
+          l = 0.f;
+          warm = true;
+          arrive(sm.warm[w]);
+          continue;
+        }
         arrive(sm.p_full[w]);
       }
       tiles += p.n;
@@ -691,8 +720,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (live_warp) {
         // a row without a visible key has sum 0 and O = 0 (never written if the piece has no tile)
         const float g = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-        for (int c0 = 0; c0 < DP; c0 += 32) {
+#pragma unroll 1
+        for (int c0 = 0; c0 < DP; c0 += 32) {  // (run once a piece: what it costs is fetching its instructions)
           float o[32];
           if (p.n > 0) {
             ld32_async<0>(o_addr + c0, o);
@@ -883,13 +912,7 @@ cudaError_t launch_dp(const AttnArgs& a, cudaStream_t s) {
 cudaError_t launch_prefix_attention_bf16(const AttnArgs& args, cudaStream_t s) {
   if (args.T <= 0) return cudaSuccess;
   AttnArgs a = args;
-  if (a.G <= kFewRows) {
-    const int64_t units = (int64_t)(a.n_groups + a.R) * a.Hkv;
-    a.few_tokens = kFewBlocks * (kFewRows / a.G);
-    a.few_splits = (int)std::min<int64_t>(std::max<int64_t>(kFewCtas / std::max<int64_t>(units, 1), 1), kFewMaxSplits);
-    a.few_keys = a.few_splits * kFewKeys;
-    a.few_alone = a.T <= a.few_tokens && (int64_t)a.max_pages << a.page_shift <= a.few_keys;
-  }
+  few_shape(&a);
   return a.D <= 64 ? launch_dp<64>(a, s) : launch_dp<128>(a, s);
 }
 

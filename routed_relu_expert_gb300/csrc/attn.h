@@ -31,10 +31,10 @@ constexpr int kAttnPartDim = 128;
 constexpr int kAttnPieceCost = 4;
 constexpr int kPrefixMaxRequests = 2048;   // of a call with shared prefixes (and as many groups)
 // The kernel for few rows: blocks of a call whose keys are split over several, row
-// blocks of 16 a block, and keys that one block is given at most.
-constexpr int kFewCtas = 1024;
+// blocks of 16 a block, and keys that a warp of a block is given at most.
+constexpr int kFewCtas = 160;
 constexpr int kFewRows = 16, kFewBlocks = 2;
-constexpr int kFewKeys = 1024;
+constexpr int kFewKeys = 256;              // a warp
 constexpr int kFewMaxSplits = 32;
 constexpr size_t kAttnPartSlots = 2 * kAttnMaxCtas;
 constexpr size_t kAttnPartBytes = kAttnPartSlots * kAttnRows * (kAttnPartDim + 2) * 4;
@@ -131,7 +131,7 @@ struct AttnArgs {
   float2* rows_ml;          // [prefix or own][KV head][T * G rows] their (max, sum)
   int4* parts_of;           // [prefix or own][KV head][T]: where a token's partials are (PartsOf)
   // the kernel for few rows: what it takes (0 tokens: nothing), splits of a unit's keys, whether it runs alone
-  int few_tokens, few_keys, few_splits, few_alone;
+  int few_tokens, few_keys, few_splits, few_warps, few_alone;
   float* few_part;          // [kFewCtas * kFewBlocks slots][16 rows][64 or 128]
   float2* few_ml;           // [slots][16 rows] (max, sum)
   float* pair_part;         // [kAttnPartSlots slots][2 x 128 rows][64 or 128]: units that a run's end cuts
@@ -176,6 +176,7 @@ cudaError_t launch_attention_bf16(const AttnArgs& a, cudaStream_t s);
 // the same with shared prefixes
 cudaError_t launch_prefix_attention_f32(const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_prefix_attention_bf16(const AttnArgs& a, cudaStream_t s);
+void few_shape(AttnArgs* a);
 cudaError_t launch_attention_few(const AttnArgs& a, cudaStream_t s);
 
 }  // namespace moe

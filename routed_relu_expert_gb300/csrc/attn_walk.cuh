@@ -46,10 +46,8 @@ __device__ __forceinline__ Req group_request(const AttnArgs& a, const PrefixGrou
   q.flags = kPrefix;
   return q;
 }
-__device__ __forceinline__ Req own_request(const AttnArgs& a, int r, int pages, int tb, int* bad) {
-  Req q = request(a, r, tb, bad);
-  q.row = r;
-  q.skip = q.flags = 0;
+// what request q keeps behind a prefix of `pages` pages
+__device__ __forceinline__ void behind_prefix(const AttnArgs& a, Req& q, int pages) {
   const int prefix = pages << a.page_shift;    // at most the row's tokens
   if (pages && q.ctx >= prefix) {              // (a shorter context has the prefix in its own row alone)
     q.ctx -= prefix;
@@ -58,6 +56,12 @@ __device__ __forceinline__ Req own_request(const AttnArgs& a, int r, int pages, 
     q.skip = pages;
     q.flags = kJoined;
   }
+}
+__device__ __forceinline__ Req own_request(const AttnArgs& a, int r, int pages, int tb, int* bad) {
+  Req q = request(a, r, tb, bad);
+  q.row = r;
+  q.skip = q.flags = 0;
+  behind_prefix(a, q, pages);
   return q;
 }
 // whether the kernel for few rows takes a step of the walk (else the one of 128-row tiles does)
@@ -80,7 +84,7 @@ __device__ __forceinline__ PartsOf parts_of(const AttnArgs& a, int which, int h,
   // slots of runs: the first run's second, then the next runs' first ones; of few rows: every kFewBlocks'th
   const int last = x.y + (x.w & kFewSlots ? kFewBlocks * (x.x - 1) : 2 * x.x - 3);
   // (bad row starts leave a token without a unit: what stands there then is not followed)
-  const bool good = x.x >= 0 && x.x <= kAttnMaxCtas && x.y >= 0 && x.y < 2 * kFewCtas * kFewBlocks && x.z >= 0 &&
+  const bool good = x.x >= 0 && x.x <= kAttnMaxCtas && x.y >= 0 && x.y < (int)(kAttnPartSlots + kFewCtas * kFewBlocks) && x.z >= 0 &&
                     (x.x < 2 || (x.w & kFewSlots ? last < kFewCtas * kFewBlocks && x.z <= kFewRows - a.G
                                                  : (x.y & 1) && last < (int)kAttnPartSlots && x.z <= 2 * kAttnRows - a.G));
   return good ? PartsOf{x.x, x.y, x.z, x.w} : PartsOf{0, 0, 0, 0};
