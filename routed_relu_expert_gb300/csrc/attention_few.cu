@@ -5,24 +5,21 @@
 //
 // The tiles of the tensor-memory kernel have 128 rows, and a piece of a run costs it 3 to
 // 4 us beside its tiles: a request with a few rows and a few hundred tokens of
-// its own behind the prefix is mostly that cost.  Here a unit (request or group, KV head,
-// split of the keys) is a block of four or eight warps that work for themselves: each takes
-// 16 keys of every 64 or 128, its own K and V by cp.async into its own stages, its own running
-// maximum and sum, products by mma.sync (16 rows, 16 keys); they meet once, at the end.
-// Several blocks an SM hide one another's waits.  The arithmetic is the other kernel's:
-// probabilities in BF16 for the second product, sums before that rounding, the reference
-// follows the maximum only past 2^8.
+// its own behind the prefix is mostly that cost.  Here a unit is (request or group, KV
+// head, 16 rows), its keys are taken 16 at a time, and the 16-key steps of all units, in
+// order, are cut into equal runs, one a warp: every warp has the same work whatever the
+// lengths, and waits for no other.  Its K and V come by cp.async into its own two stages;
+// products by mma.sync.  Units that a run's end cuts, and rows that have a prefix, leave
+// FP32 partials for the join.  The arithmetic is the other kernel's: probabilities in
+// BF16 for the second product, sums before that rounding, the reference follows the
+// maximum only past 2^8.
 //
-// Where the rows' prefix is the other kernel's and the keys are not split, the warps
-// start from the prefix's partials in place of nothing, and the block writes the
-// output; else its partials go to the join.
+// The other kernel lets this one's blocks start as its own ones end (they need nothing of it).
 //
-// The other kernel lets this one's blocks start as its own ones end; what they need of it,
-// the prefix's partials, they wait for once their first keys are on the way.
-//
-// Bound: HBM, where there are enough units; else the latency of a block (table, keys,
-// softmax, the join of the warps).
+// Bound: HBM, where there are enough keys; else the latency of a run (lengths, table, keys,
+// softmax, the join).
 #include "attn_walk.cuh"
+#include "tc_common.cuh"
 
 #include <algorithm>
 
@@ -30,8 +27,11 @@ namespace moe {
 
 namespace {
 
-constexpr int kSub = 16;                       // keys of a warp at a time
-constexpr int kStages = 2;                     // 16 keys each, of a warp
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kSub = 16;                       // keys a step
+constexpr int kUnitCost = 2;                   // a unit's fixed cost beside its steps, in steps
+constexpr int kMinRun = 4, kMaxParts = 64;     // steps of a run at least; runs of a unit at most (about)
 constexpr float kRaise = 8.f;                  // log2 units by which a maximum may pass its reference
 
 __device__ __forceinline__ float ex2(float x) {
@@ -66,33 +66,27 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
                : "memory");
 }
 
-template <int DP, int kWarps>
+template <int DP>
 struct Geo {
   static constexpr int CH = DP / 8;                          // 16-byte chunks of a head
   static constexpr int TILE = kSub * DP * 2;                 // 16 keys of K or V
-  static constexpr int RING = 2 * kStages * TILE;            // of a warp: K and V of a stage
-  static constexpr int ROW = DP + 4;                         // floats of a row in the join (four banks apart)
-  static constexpr int SMEM = kWarps * RING > kWarps * kFewRows * ROW * 4 ? kWarps * RING : kWarps * kFewRows * ROW * 4;
+  static constexpr int RING = 4 * TILE;                      // of a warp: two stages of K and V
+  static constexpr int SMEM = kWarps * RING;                 // and the walk's words
 };
 
-// kWarps: 4, three blocks an SM; or 8, where there are fewer units than SMs have blocks
-template <int DP, int kWarps>
-__global__ void __launch_bounds__(32 * kWarps, kWarps == 4 ? 3 : 1) attention_few_kernel(const AttnArgs a) {
-  using X = Geo<DP, kWarps>;
-  constexpr int kThreads = 32 * kWarps;
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 3) attention_few_kernel(const AttnArgs a, int shift) {
+  using X = Geo<DP>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float s_m[kWarps][kFewRows], s_l[kWarps][kFewRows];
-  __shared__ int s_pages, s_merge;
-  __shared__ __align__(128) uint4 s_q[kFewRows * X::CH];
+  __shared__ int64_t s_scan[kWarps];
+  __shared__ int s_most;
+  const int walk_n = a.n_groups + a.R;
+  int* prefix = reinterpret_cast<int*>(smem + X::SMEM);      // [walk_n + 1] cost before each step of the walk
+  int* skip = prefix + walk_n + 1;                           // [R] pages of the request's group's prefix
   if (a.few_alone) pdl_wait();                 // (else the other kernel has waited, and let this one start)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // eight warps: a block a row block; four: a block takes them one after the other
-  constexpr int kApart = kWarps == 8 ? kFewBlocks : 1;
-  const int part = blockIdx.x / kApart, rb0 = blockIdx.x - part * kApart;
-  const int unit = part / a.few_splits, split = part - unit * a.few_splits;
-  const int walk = unit / a.Hkv, h = unit - walk * a.Hkv;
-  const int tb = kFewRows / a.G;               // tokens of a row block
-  int bad = 0;
+  const int tb = kFewRows / a.G;               // tokens of a unit
+  const int grain = kSub << shift;             // keys that count as one step of the cost
 
   // rows that belong to no request (the other kernel's to clear where it runs too)
   if (a.few_alone) {
@@ -105,108 +99,141 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 4 ? 3 : 1) attention_fe
     }
   }
 
-  Req q;
-  bool merge = false;                          // the rows' prefix is the other kernel's
-  if (walk < a.n_groups) {
-    q = group_request(
-        a, prefix_group(a.group_start, a.prefix_row, a.prefix_len, walk, a.R, a.max_pages, a.page_shift, &bad), tb);
-  } else {
-    // the request's group, every thread looking at some
-    const int r = walk - a.n_groups;
-    if (tid == 0) s_pages = 0;
-    q = own_request(a, r, 0, tb, &bad);
-    if (a.n_groups > 0) {
-      __syncthreads();
-      PrefixGroup p;
-      bool found = false;
-      for (int i = tid; i < a.n_groups; i += kThreads) {
-        const PrefixGroup x = prefix_group(a.group_start, a.prefix_row, a.prefix_len, i, a.R, a.max_pages, a.page_shift,
-                                           nullptr);
-        // (of the groups that begin at or before r the last one counts, whatever its end)
-        if (a.group_start[i] <= r && (i + 1 == a.n_groups || a.group_start[i + 1] > r) && r < x.end && x.pages) {
-          p = x;
-          found = true;
-          s_pages = x.pages;
-        }
-      }
-      __syncthreads();
-      behind_prefix(a, q, s_pages);
-      if (found) s_merge = !few(a, group_request(a, p, tb));     // (read behind the next barrier)
+  // the walk, as the other kernel has it: cost before each step, runs of the total
+  auto at_walk = [&](int v, int* bad) {
+    Req q = v < a.n_groups ? group_request(a, prefix_group(a.group_start, a.prefix_row, a.prefix_len, v, a.R, a.max_pages,
+                                                           a.page_shift, bad), tb)
+                           : own_request(a, v - a.n_groups, skip[v - a.n_groups], tb, bad);
+    q.tiles = max((q.kv + grain - 1) / grain, 1);
+    if (!few(a, q)) q.blocks = 0;
+    return q;
+  };
+  int total, runs, share, extra;
+  auto run_start = [&](int c) { return c * share + min(c, extra); };
+  {
+    int bad = 0;
+    if (tid == 0) s_most = 0;
+    prefix_pages<kThreads>(a, reinterpret_cast<int32_t*>(smem), skip);
+    const int per = (walk_n + kThreads - 1) / kThreads, v0 = min(tid * per, walk_n), v1 = min(v0 + per, walk_n);
+    auto cost = [&](const Req& q) { return (q.tiles + kUnitCost) * q.blocks * a.Hkv; };
+    Req q;
+    int64_t local = 0;
+    int most = 0;
+    for (int v = v0; v < v1; ++v) {
+      q = at_walk(v, &bad);
+      local += cost(q);
+      if (q.blocks) most = max(most, q.tiles);
     }
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0 && most) atomicMax(&s_most, most);
+    int64_t all;
+    const int64_t before = block_prefix<kThreads>(local, s_scan, &all);
+    if (all > INT32_MAX) {                                 // (row starts that are no prefix sums)
+      bad = 1;
+      all = 0;
+    }
+    total = (int)all;
+    int at = (int)before;
+    for (int v = v0; v < v1; ++v) {
+      if (per > 1) q = at_walk(v, nullptr);
+      prefix[v] = at;
+      at += cost(q);
+    }
+    if (tid == 0) prefix[walk_n] = total;
+    if (bad && blockIdx.x == 0) set_error(&a.hdr->err, MOE_DEVERR_CACHE);
+    __syncthreads();
+    const int least = max(kMinRun, (s_most + kMaxParts - 1) / kMaxParts);
+    runs = min((int)gridDim.x * kWarps, max(total / least, 1));
+    share = total / runs;
+    extra = total - share * runs;
   }
-  if (bad && h == 0 && split == 0 && tid == 0) set_error(&a.hdr->err, MOE_DEVERR_CACHE);
-  if (rb0 >= q.blocks || !few(a, q)) {
-    if (blockIdx.x == 0) pdl_wait();           // this kernel does not end before the other
+  // runs go round the blocks first, so that few of them have an SM each
+  const int run = blockIdx.x + gridDim.x * warp;
+  if (run >= runs || total == 0) {
+    if (!a.few_alone && blockIdx.x == 0 && warp == kWarps - 1) pdl_wait();     // this kernel does not end before the other
     return;
   }
-  // this block's keys: tiles of 16 a warp, the same number a split
-  constexpr int kTile = kSub * kWarps;
-  const int tiles = max((q.kv + kTile - 1) / kTile, 1), per = (tiles + a.few_splits - 1) / a.few_splits;
-  const int parts = (tiles + per - 1) / per;
-  if (split >= parts) {
-    if (blockIdx.x == 0) pdl_wait();
-    return;
-  }
-  const int sub0 = split * per * kWarps + warp, sub1 = min((split + 1) * per, tiles) * kWarps;
-  const int32_t* table = a.block_table + (int64_t)q.row * a.max_pages + q.skip;
-  const bf16 *kc = reinterpret_cast<const bf16*>(a.k) + (int64_t)h * a.head_stride,
-             *vc = reinterpret_cast<const bf16*>(a.v) + (int64_t)h * a.head_stride;
+  auto owner = [&](int at) {                               // the run that holds position `at`
+    const int longer = (share + 1) * extra;                // positions in the longer runs
+    return at < longer ? at / (share + 1) : extra + (at - longer) / share;
+  };
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * X::RING;
-  const uint32_t q_smem = (uint32_t)__cvta_generic_to_shared(s_q);
   const float c = a.scale * 1.4426950408889634f;
   const int g = lane >> 2, t4 = lane & 3;      // the row (and + 8) and the pair of columns that a lane has of a product
+  const int64_t rows_all = (int64_t)a.T * a.G;
 
-  // where key `key` lies in a cache, elements; -1: nowhere
-  auto place = [&](int key) -> int64_t {
-    if (key >= q.kv) return -1;
-    const int pg = table[key >> a.page_shift];
-    if (pg < 0 || pg >= a.n_pages) {
-      set_error(&a.hdr->err, MOE_DEVERR_CACHE);
-      return -1;
+  const int end = run_start(run + 1);
+  int v = 0;
+  {
+    int hi = walk_n;                           // the last step that begins at or before the run
+    while (hi - v > 1) {
+      const int mid = (v + hi) >> 1;
+      if (prefix[mid] <= run_start(run)) v = mid; else hi = mid;
     }
-    return (int64_t)pg * a.page_stride + (int64_t)(key & ((1 << a.page_shift) - 1)) * a.token_stride;
-  };
-  // 16 keys into a stage; at: a lane's key (both halves of the warp have all 16)
-  auto copy = [&](int stage, int64_t at) {
-    constexpr int KEYS = 32 / X::CH;           // keys of a step of the warp
-    const uint32_t dst = ring + stage * 2 * X::TILE;
-    const int ch = lane % X::CH;
+  }
+  for (int pos = run_start(run); pos < end;) {
+    while (prefix[v + 1] <= pos) ++v;
+    const Req q = at_walk(v, nullptr);
+    const int per = q.tiles + kUnitCost, u = (pos - prefix[v]) / per, off = pos - prefix[v] - u * per;
+    const int len = min(per - off, end - pos), t0 = max(off - kUnitCost, 0), t1 = off + len - kUnitCost;
+    const int unit_end = pos - off + per;
+    pos += len;
+    if (t1 <= t0) continue;                    // the fixed cost alone
+    const int h = u / q.blocks, rb = u - h * q.blocks;
+    const bool starts = t0 == 0, ends = t1 == q.tiles;
+    const int sub0 = t0 << shift, sub1 = min(t1 << shift, max((q.kv + kSub - 1) / kSub, 1));
+    const int32_t* table = a.block_table + (int64_t)q.row * a.max_pages + q.skip;
+    const bf16 *kc = reinterpret_cast<const bf16*>(a.k) + (int64_t)h * a.head_stride,
+               *vc = reinterpret_cast<const bf16*>(a.v) + (int64_t)h * a.head_stride;
+    // where key `key` lies in a cache, elements; -1: nowhere
+    auto place = [&](int key) -> int64_t {
+      if (key >= q.kv) return -1;
+      const int pg = table[key >> a.page_shift];
+      if (pg < 0 || pg >= a.n_pages) {
+        set_error(&a.hdr->err, MOE_DEVERR_CACHE);
+        return -1;
+      }
+      return (int64_t)pg * a.page_stride + (int64_t)(key & ((1 << a.page_shift) - 1)) * a.token_stride;
+    };
+    // a lane's key of 16
+    auto keys = [&](int sub) -> int64_t { return sub < sub1 ? place(sub * kSub + (lane & 15)) : -1; };
+    // 16 keys into a stage; at: a lane's key (both halves of the warp have all 16)
+    auto copy = [&](int stage, int64_t at) {
+      constexpr int KEYS = 32 / X::CH;         // keys of a step of the warp
+      const uint32_t dst = ring + stage * 2 * X::TILE;
+      const int ch = lane % X::CH;
 #pragma unroll
-    for (int s = 0; s < kSub / KEYS; ++s) {
-      const int key = s * KEYS + lane / X::CH;
-      const int64_t off = __shfl_sync(0xffffffffu, at, key);
-      const int bytes = off >= 0 && ch * 8 < a.D ? 16 : 0;
-      const int64_t from = bytes ? off + ch * 8 : 0;
-      const uint32_t to = dst + key * DP * 2 + ((ch ^ (key & 7)) << 4);
-      copy16(to, kc + from, bytes);
-      copy16(to + X::TILE, vc + from, bytes);
-    }
-    copy_commit();
-  };
-  // a lane's key of the warp's 16 from `sub` on
-  auto keys = [&](int sub) -> int64_t { return sub < sub1 ? place(sub * kSub + (lane & 15)) : -1; };
-
-  for (int rb = rb0; rb < q.blocks; rb += kApart) {
+      for (int s = 0; s < kSub / KEYS; ++s) {
+        const int key = s * KEYS + lane / X::CH;
+        const int64_t o = __shfl_sync(0xffffffffu, at, key);
+        const int bytes = o >= 0 && ch * 8 < a.D ? 16 : 0;
+        const int64_t from = bytes ? o + ch * 8 : 0;
+        const uint32_t to = dst + key * DP * 2 + ((ch ^ (key & 7)) << 4);
+        copy16(to, kc + from, bytes);
+        copy16(to + X::TILE, vc + from, bytes);
+      }
+      copy_commit();
+    };
+    const int64_t at0 = keys(sub0), at1 = keys(sub0 + 1);
+    copy(0, at0);
+    copy(1, at1);
+    int64_t at = keys(sub0 + 2);
     const int tok0 = q.q0 + rb * tb, ntok = min(tb, q.n - rb * tb), valid = ntok * a.G;
-    // Q, read again for every 16 keys (in registers it would cost a block an SM)
-    for (int i = tid; i < kFewRows * X::CH; i += kThreads) {
-      const int row = i / X::CH, ch = i - row * X::CH, tk = row / a.G;
-      const bool in = row < valid && ch * 8 < a.D;
-      copy16(q_smem + row * DP * 2 + ((ch ^ (row & 7)) << 4),
-             reinterpret_cast<const bf16*>(a.q) +
-                 (in ? (int64_t)(tok0 + tk) * a.q_ld + (int64_t)(h * a.G + row - tk * a.G) * a.D + 8 * ch : 0),
-             in ? 16 : 0);
+    // Q as the A operand: rows g and g + 8
+    uint32_t qf[DP / 16][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int row = g + 8 * i, tk = row / a.G;
+      const bf16* p = reinterpret_cast<const bf16*>(a.q) + (int64_t)(tok0 + tk) * a.q_ld +
+                      (int64_t)(h * a.G + row - tk * a.G) * a.D;
+#pragma unroll
+      for (int k = 0; k < DP / 16; ++k)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int col = 16 * k + 8 * j + 2 * t4;
+          qf[k][2 * j + i] = row < valid && col < a.D ? *reinterpret_cast<const uint32_t*>(p + col) : 0u;
+        }
     }
-    copy_commit();
-    int64_t at[kStages];
-#pragma unroll
-    for (int i = 0; i < kStages; ++i) at[i] = keys(sub0 + i * kWarps);
-#pragma unroll
-    for (int i = 0; i < kStages; ++i) copy(i, at[i]);
-    int64_t next = keys(sub0 + kStages * kWarps);
-    copy_wait<kStages>();
-    __syncthreads();                           // Q is there, and the word on the prefix
-    merge = parts == 1 && q.flags & kJoined && s_merge;
     float o[DP / 8][4];
 #pragma unroll
     for (int i = 0; i < DP / 8; ++i)
@@ -214,77 +241,23 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 4 ? 3 : 1) attention_fe
       for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
     float mc[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
-    if (!a.few_alone) pdl_wait();
-    if (merge) {
-      // a warp starts from every kWarps'th of the prefix's partials
-      PartsOf pre[2];
-      int hd[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int row = g + 8 * i, tk = row / a.G;
-        hd[i] = row - tk * a.G;
-        pre[i] = parts_of(a, 0, h, tok0 + min(tk, ntok - 1));
-        if (row >= valid) pre[i].parts = 0;
-      }
-      float2 x[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (warp < pre[i].parts) {
-          const float2* ml;
-          const float4* from;
-          partial<DP>(a, pre[i], 0, h, tok0 * a.G + g + 8 * i, hd[i], warp, ml, from);
-          x[i] = __ldcg(ml);
-#pragma unroll
-          for (int j = 0; j < DP / 8; ++j) {
-            const float2 y = __ldcg(reinterpret_cast<const float2*>(from) + t4 + 4 * j);
-            o[j][2 * i] = y.x;
-            o[j][2 * i + 1] = y.y;
-          }
-        }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (x[i].y != 0.f) {                   // (a part without a visible key has zeros)
-          mc[i] = x[i].x;
-          l[i] = t4 == 0 ? x[i].y : 0.f;       // (the lanes of a row are added up at the end)
-        }
-#pragma unroll 1
-        for (int k = warp + kWarps; k < pre[i].parts; k += kWarps) {
-          const float2* ml;
-          const float4* from;
-          partial<DP>(a, pre[i], 0, h, tok0 * a.G + g + 8 * i, hd[i], k, ml, from);
-          const float2 z = __ldcg(ml);
-          if (z.y == 0.f) continue;
-          const float top = fmaxf(mc[i], z.x), f0 = mc[i] == -INFINITY ? 0.f : ex2(mc[i] - top), f1 = ex2(z.x - top);
-          mc[i] = top;
-          l[i] = l[i] * f0 + (t4 == 0 ? z.y * f1 : 0.f);
-#pragma unroll
-          for (int j = 0; j < DP / 8; ++j) {
-            const float2 y = __ldcg(reinterpret_cast<const float2*>(from) + t4 + 4 * j);
-            o[j][2 * i] = o[j][2 * i] * f0 + y.x * f1;
-            o[j][2 * i + 1] = o[j][2 * i + 1] * f0 + y.y * f1;
-          }
-        }
-      }
-    }
-
     int stage = 0;
-    for (int sub = sub0; sub < sub1; sub += kWarps) {
+    for (int sub = sub0; sub < sub1; ++sub) {
       const uint32_t kt = ring + stage * 2 * X::TILE, vt = kt + X::TILE;
       const int k0 = sub * kSub;
-      copy_wait<kStages - 1>();
+      copy_wait<1>();
       __syncwarp();
       // scores of 16 rows and 16 keys
       float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
       {
         // matrices: keys 0-7 and 8-15, two chunks each
-        const int key = (lane & 7) + ((lane >> 4) << 3), half = lane >> 3 & 1, q_row = lane & 15;
+        const int key = (lane & 7) + ((lane >> 4) << 3), half = lane >> 3 & 1;
 #pragma unroll
         for (int k = 0; k < DP / 16; ++k) {
-          uint32_t x[4], b[4];
-          ldsm4(q_smem + q_row * DP * 2 + (((2 * k + (lane >> 4)) ^ (q_row & 7)) << 4), x);
+          uint32_t b[4];
           ldsm4(kt + key * DP * 2 + (((2 * k + half) ^ (key & 7)) << 4), b);
-          mma_bf16_16816(s[0], x[0], x[1], x[2], x[3], b[0], b[1]);
-          mma_bf16_16816(s[1], x[0], x[1], x[2], x[3], b[2], b[3]);
+          mma_bf16_16816(s[0], qf[k][0], qf[k][1], qf[k][2], qf[k][3], b[0], b[1]);
+          mma_bf16_16816(s[1], qf[k][0], qf[k][1], qf[k][2], qf[k][3], b[2], b[3]);
         }
       }
       uint32_t odd = 0;                        // keys whose V is not finite, nodes among them alone
@@ -361,13 +334,13 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 4 ? 3 : 1) attention_fe
           const uint32_t w0 = __shfl_sync(0xffffffffu, key < 8 ? p[0] : p[2], from);
           const uint32_t w1 = __shfl_sync(0xffffffffu, key < 8 ? p[1] : p[3], from);
           const float p0 = key & 1 ? bf16_hi(w0) : bf16_lo(w0), p1 = key & 1 ? bf16_hi(w1) : bf16_lo(w1);
-          const int64_t off = place(k0 + key);
-          if (off < 0) continue;
+          const int64_t off_v = place(k0 + key);
+          if (off_v < 0) continue;
 #pragma unroll
           for (int i = 0; i < DP / 8; ++i) {
             const int col = 8 * i + 2 * t4;
             if (col >= a.D) continue;
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(vc + off + col);
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(vc + off_v + col);
             if (p0 != 0.f) {
               o[i][0] = fmaf(p0, bf16_lo(w), o[i][0]);
               o[i][1] = fmaf(p0, bf16_hi(w), o[i][1]);
@@ -392,119 +365,81 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 4 ? 3 : 1) attention_fe
         }
       }
       __syncwarp();                            // the stage is read before it is filled again
-      copy(stage, next);
-      next = keys(sub + (kStages + 1) * kWarps);
-      if (++stage == kStages) stage = 0;
+      copy(stage, at);
+      at = keys(sub + 3);
+      stage ^= 1;
     }
+    copy_wait<0>();                            // (the next piece's keys come into the same stages)
 
-    // ---- the warps' parts, in warp order ----
-    copy_wait<0>();
-    __syncthreads();
-    float* so = reinterpret_cast<float*>(smem);
+    // ---- the piece's end: the rows, or their partials ----
+    const int which = q.flags & kPrefix ? 0 : 1, slot = 2 * run + (starts ? 1 : 0);
+    const bool uncut = starts && ends, whole = uncut && !q.flags;
+    const int64_t side = which * a.Hkv + h;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-      if (t4 == 0) {
-        s_m[warp][g + 8 * i] = mc[i];
-        s_l[warp][g + 8 * i] = l[i];
-      }
-#pragma unroll
-      for (int j = 0; j < DP / 8; ++j)
-        *reinterpret_cast<float2*>(so + (warp * kFewRows + g + 8 * i) * X::ROW + 8 * j + 2 * t4) =
-            make_float2(o[j][2 * i], o[j][2 * i + 1]);
-    }
-    __syncthreads();
-    constexpr int kCols = kThreads / kFewRows;   // threads of a row: columns 4 (c0 + kCols i)
-    constexpr int kPer = DP / 4 / kCols;
-    const int row = tid / kCols, c0 = tid - row * kCols, tk = row / a.G, hd = row - tk * a.G, head = h * a.G + hd;
-    float top = -INFINITY, sum = 0.f, f[kWarps];
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w)
-      if (s_l[w][row] != 0.f) top = fmaxf(top, s_m[w][row]);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      f[w] = s_l[w][row] == 0.f ? 0.f : ex2(s_m[w][row] - top);       // (no visible key in that part)
-      if (s_l[w][row] != 0.f) sum = fmaf(s_l[w][row], f[w], sum);
-    }
-    const int which = q.flags & kPrefix ? 0 : 1;
-    const bool whole = parts == 1 && (!q.flags || merge);
-    const int slot = part * kFewBlocks + rb;
-    const int rows_all = a.T * a.G, rg = tok0 * a.G + row;
-    const int64_t side = which * a.Hkv + h;
-    if (row < valid) {
-      float4 acc[kPer];
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          if (f[w] == 0.f) continue;
-          const float4 x = *reinterpret_cast<const float4*>(so + (w * kFewRows + row) * X::ROW + 4 * (c0 + kCols * i));
-          acc[i].x = fmaf(x.x, f[w], acc[i].x);
-          acc[i].y = fmaf(x.y, f[w], acc[i].y);
-          acc[i].z = fmaf(x.z, f[w], acc[i].z);
-          acc[i].w = fmaf(x.w, f[w], acc[i].w);
-        }
-      }
+      const int row = g + 8 * i, tk = row / a.G, head = h * a.G + row - tk * a.G;
+      float sum = l[i] + __shfl_xor_sync(0xffffffffu, l[i], 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      if (row >= valid) continue;
       if (whole) {
+        // a row without a visible key has sum 0 and O = 0
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        bf16* out = reinterpret_cast<bf16*>(a.out) + (int64_t)(tok0 + tk) * a.out_ld + (int64_t)head * a.D;
+        bf16* out = reinterpret_cast<bf16*>(a.out) + (int64_t)(tok0 + tk) * a.out_ld + (int64_t)head * a.D + 2 * t4;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          if (4 * (c0 + kCols * i) < a.D)
-            *reinterpret_cast<uint2*>(out + 4 * (c0 + kCols * i)) =
-                make_uint2(pack_bf16(acc[i].x * inv, acc[i].y * inv), pack_bf16(acc[i].z * inv, acc[i].w * inv));
-        if (a.lse && c0 == 0)
-          a.lse[(int64_t)(tok0 + tk) * a.H + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+        for (int j = 0; j < DP / 8; ++j)
+          if (8 * j < a.D) *reinterpret_cast<uint32_t*>(out + 8 * j) = pack_bf16(o[j][2 * i] * inv, o[j][2 * i + 1] * inv);
+        if (a.lse && t4 == 0)
+          a.lse[(int64_t)(tok0 + tk) * a.H + head] = sum == 0.f ? -INFINITY : (mc[i] + log2f(sum)) * 0.6931471805599453f;
       } else {
-        const int64_t at_row = parts == 1 ? side * rows_all + rg : (int64_t)slot * kFewRows + row;
-        float4* part = reinterpret_cast<float4*>(parts == 1 ? a.rows_part : a.few_part) + at_row * (DP / 4);
+        const int64_t at_row = uncut ? side * rows_all + (int64_t)tok0 * a.G + row : (int64_t)slot * kFewRows + row;
+        float* to = (uncut ? a.rows_part : a.few_part) + at_row * DP + 2 * t4;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) part[c0 + kCols * i] = acc[i];
-        if (c0 == 0) (parts == 1 ? a.rows_ml : a.few_ml)[at_row] = make_float2(top, sum);
+        for (int j = 0; j < DP / 8; ++j)
+          *reinterpret_cast<float2*>(to + 8 * j) = make_float2(o[j][2 * i], o[j][2 * i + 1]);
+        if (t4 == 0) (uncut ? a.rows_ml : a.few_ml)[at_row] = make_float2(mc[i], sum);
       }
     }
-    if (split == 0 && tid < ntok)
-      a.parts_of[side * a.T + tok0 + tid] = make_int4(whole ? 0 : parts, parts > 1 ? slot : 0, tid * a.G,
-                                                      (q.flags & kJoined) | (parts > 1 ? kFewSlots : 0));
-    __syncthreads();                           // the buffers are the next row block's
+    if (starts && lane < ntok)
+      a.parts_of[side * a.T + tok0 + lane] =
+          make_int4(whole ? 0 : uncut ? 1 : owner(unit_end - 1) - run + 1, uncut ? 0 : slot, lane * a.G,
+                    (q.flags & kJoined) | (uncut ? 0 : kFewSlots));
   }
+  if (!a.few_alone && blockIdx.x == 0 && warp == kWarps - 1) pdl_wait();       // as above
 }
 
-template <int DP, int kWarps>
+template <int DP>
 cudaError_t launch_dp(const AttnArgs& a, cudaStream_t s) {
+  using X = Geo<DP>;
   static PerDeviceOnce once;
-  int unused = 0;
+  int blocks = 0;
   const cudaError_t e = once.run(
       [](int& v) {
-        v = 1;
-        return cudaFuncSetAttribute(attention_few_kernel<DP, kWarps>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    Geo<DP, kWarps>::SMEM);
+        v = std::min(3 * tc::num_sms(), kFewRuns / kWarps);
+        return cudaFuncSetAttribute(attention_few_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    X::SMEM + (3 * kPrefixMaxRequests + 1) * 4);
       },
-      &unused);
+      &blocks);
   if (e != cudaSuccess) return e;
-  const int64_t units = (int64_t)(a.n_groups + a.R) * a.Hkv;
-  return launch_k(attention_few_kernel<DP, kWarps>, dim3((unsigned)std::max<int64_t>(units * a.few_splits * (kWarps == 8 ? kFewBlocks : 1), 1)),
-                  dim3(32 * kWarps), Geo<DP, kWarps>::SMEM, s, a);
+  // keys that count as one step of the cost: 16, or as many more as keep the cost of all units in 31 bits
+  const int64_t units = 2ll * (a.n_groups + a.R) * a.Hkv, keys = (int64_t)a.max_pages << a.page_shift;
+  int shift = 0;
+  while (units * (((keys + (kSub << shift) - 1) >> shift) / kSub + 1 + kUnitCost) >= ((int64_t)1 << 31)) ++shift;
+  // no more blocks than the longest tables' rows have runs for
+  const int64_t most = units * (keys / kSub + 1 + kUnitCost) / kMinRun + 1;
+  return launch_k(attention_few_kernel<DP>, dim3((unsigned)std::min<int64_t>(blocks, most)), dim3(kThreads),
+                  X::SMEM + ((size_t)a.n_groups + 2 * a.R + 1) * 4, s, a, shift);
 }
 
 }  // namespace
 
-// Few units: blocks of eight warps, their keys split while that leaves SMs without one; else blocks of four.
 void few_shape(AttnArgs* a) {
-  const int64_t units = (int64_t)(a->n_groups + a->R) * a->Hkv, sms = 152;
-  if (a->G > kFewRows) return;                 // (a token's rows do not fit a block's 16)
+  if (a->G > kFewRows) return;                 // (a token's rows do not fit a unit's 16)
   a->few_tokens = kFewBlocks * (kFewRows / a->G);
-  a->few_warps = units < 2 * sms ? 8 : 4;
-  a->few_splits = (int)std::min<int64_t>(std::max<int64_t>(sms / std::max<int64_t>(units, 1), 1), kFewMaxSplits);
-  a->few_keys = a->few_splits * a->few_warps * kFewKeys;
-  a->few_alone = a->T <= a->few_tokens && (int64_t)a->max_pages << a->page_shift <= a->few_keys;
+  a->few_alone = a->T <= a->few_tokens;
 }
 
 cudaError_t launch_attention_few(const AttnArgs& a, cudaStream_t s) {
-  if (a.few_warps == 8) return a.D <= 64 ? launch_dp<64, 8>(a, s) : launch_dp<128, 8>(a, s);
-  return a.D <= 64 ? launch_dp<64, 4>(a, s) : launch_dp<128, 4>(a, s);
+  return a.D <= 64 ? launch_dp<64>(a, s) : launch_dp<128>(a, s);
 }
 
 }  // namespace moe

@@ -8,8 +8,7 @@
 // KV head, block of up to 2 x 128 rows); its keys are tiles of 128, and the tiles of all
 // units, in order, are cut into equal runs, one per CTA (one CTA an SM).  Units of a few
 // rows go to the kernel of attention_few.cu.  Rows with a prefix and units that a run's
-// end cuts leave FP32 partials, which the kernel for few rows or prefix_join_kernel adds
-// in a fixed order.
+// end cuts leave FP32 partials, which prefix_join_kernel adds in a fixed order.
 //
 // Inside a CTA two tiles of 128 rows take turns on the tensor cores, each with a softmax
 // group of four warps, a thread a row: while one tile's scores are exponentiated, the
@@ -157,33 +156,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto run_start = [&](int c) { return c * share + min(c, extra); };
   {
     int bad = 0;
-    // the groups into the ring's memory, for each request's search; a thread's first request beside them
-    int32_t* start = reinterpret_cast<int32_t*>(ring_ptr);
-    int32_t *rows = start + groups_n + 1, *lens = rows + groups_n;
-    for (int g = threadIdx.x; g <= groups_n; g += kThreads) {
-      start[g] = groups_n ? a.group_start[g] : 0;
-      if (g < groups_n) {
-        rows[g] = a.prefix_row[g];
-        lens[g] = a.prefix_len[g];
-      }
-    }
+    // a thread's first request beside the groups, which lie in the ring's memory meanwhile
     const int per = (walk_n + kThreads - 1) / kThreads, v0 = min((int)threadIdx.x * per, walk_n),
               v1 = min(v0 + per, walk_n);
     Req q;
     const bool ahead = v0 < v1 && v0 >= groups_n;
     if (ahead) q = own_request(a, v0 - groups_n, 0, tb, &bad);
-    __syncthreads();
-    for (int r = threadIdx.x; r < a.R; r += kThreads) {
-      const int g = group_of(start, groups_n, r);
-      int pages = 0;
-      if (g >= 0) {
-        const PrefixGroup p = prefix_group(start, rows, lens, g, a.R, a.max_pages, a.page_shift, nullptr);
-        if (r < p.end) pages = p.pages;
-      }
-      skip[r] = pages;
-    }
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    __syncthreads();
+    prefix_pages<kThreads>(a, reinterpret_cast<int32_t*>(ring_ptr), skip);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");       // (before TMA writes there)
     auto cost = [&](const Req& q) { return (q.tiles + kPieceCost) * q.blocks * a.Hkv; };
     int64_t local = 0;                                     // (one step's cost fits 31 bits; row starts that are no
     for (int v = v0; v < v1; ++v) {                        // prefix sums may not add up to so few)
@@ -195,21 +175,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       local += cost(q);
     }
-    int64_t x = local;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, x, off);
-      if (lane >= off) x += y;
-    }
-    if (lane == 31) sm.scan[warp] = x;
-    __syncthreads();
-    int64_t before = x - local, all = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      const int64_t s = sm.scan[w];
-      if (w < warp) before += s;
-      all += s;
-    }
+    int64_t all;
+    const int64_t before = block_prefix<kThreads>(local, sm.scan, &all);
     if (all > INT32_MAX) {
       bad = 1;
       all = 0;                                             // nothing is computed

@@ -30,12 +30,10 @@ constexpr int kAttnPartDim = 128;
 // and long contexts: 110, 97, 92, 92 us; flat for 64 requests of up to 8,000 tokens.
 constexpr int kAttnPieceCost = 4;
 constexpr int kPrefixMaxRequests = 2048;   // of a call with shared prefixes (and as many groups)
-// The kernel for few rows: blocks of a call whose keys are split over several, row
-// blocks of 16 a block, and keys that a warp of a block is given at most.
-constexpr int kFewCtas = 160;
+// The kernel for few rows: its runs (warps) at most, rows of a unit, units of a KV head
+// that a request may have.
+constexpr int kFewRuns = 2048;
 constexpr int kFewRows = 16, kFewBlocks = 2;
-constexpr int kFewKeys = 256;              // a warp
-constexpr int kFewMaxSplits = 32;
 constexpr size_t kAttnPartSlots = 2 * kAttnMaxCtas;
 constexpr size_t kAttnPartBytes = kAttnPartSlots * kAttnRows * (kAttnPartDim + 2) * 4;
 constexpr size_t kAttnJoinBytes = kAttnMaxCtas * 16;   // a record a run: what the join kernel adds
@@ -130,9 +128,9 @@ struct AttnArgs {
   float* rows_part;         // [prefix or own][KV head][T * G rows][64 or 128]: output sums of whole units
   float2* rows_ml;          // [prefix or own][KV head][T * G rows] their (max, sum)
   int4* parts_of;           // [prefix or own][KV head][T]: where a token's partials are (PartsOf)
-  // the kernel for few rows: what it takes (0 tokens: nothing), splits of a unit's keys, whether it runs alone
-  int few_tokens, few_keys, few_splits, few_warps, few_alone;
-  float* few_part;          // [kFewCtas * kFewBlocks slots][16 rows][64 or 128]
+  // the kernel for few rows: nodes that it takes (0: none), whether it runs alone
+  int few_tokens, few_alone;
+  float* few_part;          // [2 kFewRuns slots][16 rows][64 or 128]
   float2* few_ml;           // [slots][16 rows] (max, sum)
   float* pair_part;         // [kAttnPartSlots slots][2 x 128 rows][64 or 128]: units that a run's end cuts
   float2* pair_ml;          // [slots][rows] (max, sum)

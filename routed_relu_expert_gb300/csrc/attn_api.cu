@@ -88,8 +88,8 @@ PrefixLayout prefix_layout(const moe_attn_config_t* c, int64_t T) {
   l.ml = l.part + 2 * rows * dp * 4;
   l.parts_of = l.ml + 2 * rows * 8;
   l.few_part = l.parts_of + 2 * (size_t)T * c->n_kv_heads * 16;
-  l.few_ml = l.few_part + (size_t)kFewCtas * kFewBlocks * kFewRows * dp * 4;
-  l.pair_part = l.few_ml + (size_t)kFewCtas * kFewBlocks * kFewRows * 8;
+  l.few_ml = l.few_part + 2 * (size_t)kFewRuns * kFewRows * dp * 4;
+  l.pair_part = l.few_ml + 2 * (size_t)kFewRuns * kFewRows * 8;
   l.pair_ml = l.pair_part + kAttnPartSlots * 2 * kAttnRows * dp * 4;
   l.end = l.pair_ml + kAttnPartSlots * 2 * kAttnRows * 8;
   return l;
