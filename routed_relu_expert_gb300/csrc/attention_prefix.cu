@@ -41,6 +41,7 @@ constexpr int kQueue = 4;                      // pieces worked out ahead
 constexpr uint32_t kTmemCols = 512;
 // a unit's fixed cost beside its tiles, in tiles
 constexpr int kPieceCost = 3;
+constexpr int kMinRun = 6;                     // of a run: with fewer, the SMs are the other kernel's sooner
 
 template <int DP>
 struct Geo {
@@ -183,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     total = (int)all;
     int run = (int)before;
-    runs = min((int)gridDim.x, max(total, 1));
+    runs = min((int)gridDim.x, max(total / kMinRun, 1));
     share = total / runs;
     extra = total - share * runs;
     const int begin = run_start(blockIdx.x);
@@ -753,9 +754,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // their maxima and sums come a lane each, so that a row waits for one round of them.
 constexpr int kJoinThreads = 256;
 template <int DP>
-__global__ void __launch_bounds__(kJoinThreads, 5) prefix_join_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kJoinThreads, 4) prefix_join_kernel(const AttnArgs a) {
   constexpr int L = DP / 4;                    // lanes a row
-  constexpr int kAhead = 4;                    // partials in flight
+  constexpr int kAhead = 8;                    // partials in flight
   pdl_wait();
   const int lane = threadIdx.x & 31, sub = lane % L;
   const int rows_all = a.T * a.G, id = (blockIdx.x * kJoinThreads + threadIdx.x) / L;
