@@ -44,9 +44,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// 16 bytes, zeros where `bytes` is 0
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+// 16 bytes, zeros where `bytes` is 0; policy: how long L2 keeps them
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(bytes),
+               "l"(policy)
+               : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -197,6 +199,10 @@ __global__ void __launch_bounds__(kThreads, 3) attention_few_kernel(const AttnAr
     };
     // a lane's key of 16
     auto keys = [&](int sub) -> int64_t { return sub < sub1 ? place(sub * kSub + (lane & 15)) : -1; };
+    // own tokens are read once and leave L2 before the partials (92 -> 89 us for 128 requests of 250 tokens each)
+    uint64_t policy;
+    if (q.flags & kPrefix) asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
+    else asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
     // 16 keys into a stage; at: a lane's key (both halves of the warp have all 16)
     auto copy = [&](int stage, int64_t at) {
       constexpr int KEYS = 32 / X::CH;         // keys of a step of the warp
@@ -209,8 +215,8 @@ __global__ void __launch_bounds__(kThreads, 3) attention_few_kernel(const AttnAr
         const int bytes = o >= 0 && ch * 8 < a.D ? 16 : 0;
         const int64_t from = bytes ? o + ch * 8 : 0;
         const uint32_t to = dst + key * DP * 2 + ((ch ^ (key & 7)) << 4);
-        copy16(to, kc + from, bytes);
-        copy16(to + X::TILE, vc + from, bytes);
+        copy16(to, kc + from, bytes, policy);
+        copy16(to + X::TILE, vc + from, bytes, policy);
       }
       copy_commit();
     };

@@ -40,7 +40,7 @@ constexpr int kLoaders = 2;                    // warps that issue the TMA copie
 constexpr int kQueue = 4;                      // pieces worked out ahead
 constexpr uint32_t kTmemCols = 512;
 // a unit's fixed cost beside its tiles, in tiles
-constexpr int kPieceCost = 3;
+constexpr int kPieceCost = 4;
 constexpr int kMinRun = 6;                     // of a run: with fewer, the SMs are the other kernel's sooner
 
 template <int DP>
