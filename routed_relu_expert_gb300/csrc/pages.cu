@@ -22,21 +22,25 @@ struct GridMeet {
   int blocks, met = 0;
   bool ok = true;
   __device__ GridMeet(AttnHeader* h, int n) : hdr(h), blocks(n) {}
-  // what the blocks read and wrote before it is done for what they do after it
-  __device__ bool operator()() {
+  // what this block has read and written until here is done for who waits for it
+  __device__ void arrive() {
     __syncthreads();
-    if (blocks == 1) return true;
-    ++met;
-    __shared__ int good;
-    if (threadIdx.x == 0) {
+    if (blocks > 1 && threadIdx.x == 0) {
       __threadfence();
       atomicAdd(&hdr->met, 1);
+    }
+  }
+  // until every block has arrived `times` times
+  __device__ bool wait(int times) {
+    if (blocks == 1) return true;
+    __shared__ int good;
+    if (threadIdx.x == 0) {
       const uint64_t t0 = globaltimer();
       int seen, tries = 0;
       good = 1;
       while (true) {
         asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(seen) : "l"(&hdr->met) : "memory");
-        if (seen >= met * blocks) break;
+        if (seen >= times * blocks) break;
         if ((++tries & 255) == 0 && globaltimer() - t0 > tc::kWaitLimitNs) {
           good = 0;
           set_error(&hdr->err, MOE_DEVERR_TIMEOUT);
@@ -46,7 +50,12 @@ struct GridMeet {
     }
     __syncthreads();
     ok = ok && good;
+    __syncthreads();                           // (the word is the next wait's)
     return ok;
+  }
+  __device__ bool operator()() {
+    arrive();
+    return wait(++met);
   }
   __device__ void leave() {
     __syncthreads();
@@ -65,13 +74,13 @@ __device__ __forceinline__ int block_sum(int v, int* tmp) {
   int all = 0;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) all += tmp[w];
-  __syncthreads();
   return all;
 }
 
 // ---------------------------------------------------------------------------
 // fork
 // ---------------------------------------------------------------------------
+constexpr int kForkAhead = 4;                  // 16-byte pieces that a thread has in flight
 // blockIdx.x: the fork; blockIdx.y: a part of its page's tokens
 __global__ void __launch_bounds__(kThreads) fork_kernel(const ForkArgs a) {
   pdl_wait();
@@ -83,22 +92,23 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const ForkArgs a) {
     const int s = a.src[j], d = a.dst[j], n = a.lengths[j];
     return s >= 0 && s < a.R && d >= 0 && d < a.R && n >= 0 && n <= cap && !(a.same && s == d);
   };
-  // new pages of the forks before this one and of all; forks that meet this one's rows
+  // new pages of the forks before this one and of all (two counts of at most 4096 in a word); forks that meet
+  // this one's rows
   const bool have = i < a.n;                   // (no fork at all: one block, for free_head_out)
   const int s = have ? a.src[i] : 0, d = have ? a.dst[i] : 0;
-  int before = 0, all = 0, clash = 0;
+  int counts = 0, clash = 0;
   for (int j = tid; j < a.n; j += kThreads) {
-    const int need = valid(j) && (a.lengths[j] & page_mask);
-    all += need;
-    if (j < i) before += need;
-    if (valid(j) && ((j < i && a.dst[j] == d) || (a.same && a.dst[j] == s))) clash = 1;
+    const bool good = valid(j);
+    const int need = good && (a.lengths[j] & page_mask);
+    counts += need << 16 | (j < i ? need : 0);
+    if (good && ((j < i && a.dst[j] == d) || (a.same && a.dst[j] == s))) clash = 1;
   }
   const int head = max(*a.free_head, 0);
   int bad = *a.free_head < 0 ? MOE_DEVERR_CACHE : 0;
-  before = block_sum(before, tmp);
-  all = block_sum(all, tmp);
-  clash = block_sum(clash, tmp);
-  const bool ok = have && valid(i) && clash == 0;
+  clash = __syncthreads_or(clash);
+  counts = block_sum(counts, tmp);
+  const int before = counts & 0xffff, all = counts >> 16;
+  const bool ok = have && valid(i) && !clash;
   if (have && !ok) bad |= MOE_DEVERR_CACHE;
   if (ok) {
     const int len = a.lengths[i], full = len >> a.page_shift, rest = len & page_mask;
@@ -135,13 +145,22 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const ForkArgs a) {
         // 16-byte pieces: [K or V][token][head][piece]
         const int per_head = a.row_bytes >> 4, per_token = per_head * a.Hkv, per_cache = per_token * rest;
         const int step = kThreads * (int)gridDim.y;
-        for (int x = (int)blockIdx.y * kThreads + tid; x < 2 * per_cache; x += step) {
-          const int v = x >= per_cache, y = x - v * per_cache, t = y / per_token, z = y - t * per_token;
-          const int h = z / per_head, c = z - h * per_head;
-          uint8_t* cache = v ? a.v : a.k;
-          const int64_t off = t * a.token_stride + h * a.head_stride + 16 * c;
-          *reinterpret_cast<uint4*>(cache + fresh * a.page_stride + off) =
-              *reinterpret_cast<const uint4*>(cache + old * a.page_stride + off);
+        const int64_t move = (int64_t)(fresh - old) * a.page_stride;
+        for (int x0 = (int)blockIdx.y * kThreads + tid; x0 < 2 * per_cache; x0 += kForkAhead * step) {
+          uint4 d[kForkAhead];
+          uint8_t* at[kForkAhead];
+#pragma unroll
+          for (int i = 0; i < kForkAhead; ++i) {
+            const int x = x0 + i * step;
+            if (x >= 2 * per_cache) break;
+            const int v = x >= per_cache, y = x - v * per_cache, t = y / per_token, z = y - t * per_token;
+            const int h = z / per_head, c = z - h * per_head;
+            at[i] = (v ? a.v : a.k) + old * a.page_stride + t * a.token_stride + h * a.head_stride + 16 * c;
+            d[i] = *reinterpret_cast<const uint4*>(at[i]);
+          }
+#pragma unroll
+          for (int i = 0; i < kForkAhead; ++i)
+            if (x0 + i * step < 2 * per_cache) *reinterpret_cast<uint4*>(at[i] + move) = d[i];
         }
       }
     }
@@ -257,14 +276,19 @@ __global__ void __launch_bounds__(kThreads) compact_moves_kernel(const CompactAr
   if (bad) set_error(&a.hdr->err, bad);
 }
 
-// The second moves the tokens in waves: all blocks read their part of a wave into
-// registers, meet, and write it.  Token i of the lists goes to a place at or before
-// its source, so what a wave writes lies behind every later wave's sources and only
-// its own wave and earlier ones read there.
+// The second moves the tokens in waves: all blocks read their part of a wave into shared
+// memory, meet, and write it; the next two waves' reads are on their way meanwhile, and a
+// block has met the others for the next wave before it writes this one.  Token i of the lists
+// goes to a place at or before its source, so what a wave writes lies behind every later
+// wave's sources and only its own wave and earlier ones read there.  A thread reads and
+// writes its own 16-byte pieces.
 constexpr int kWaveThreads = 512;
-constexpr int kWaveAhead = 16;                 // tokens a thread has in flight
+constexpr int kWaves = 3;                      // in a block's shared memory
+constexpr int kWaveAhead = 9;                  // pieces of a thread a wave (72 KB a block)
+constexpr size_t kWaveSmem = (size_t)kWaves * kWaveThreads * kWaveAhead * 16;
 __global__ void __launch_bounds__(kWaveThreads, 1) compact_wave_kernel(const CompactArgs a, const Move* moves, int n,
                                                                         int groups) {
+  extern __shared__ uint4 held_pieces[];       // [wave modulo kWaves][piece][thread]
   GridMeet meet(a.hdr, (int)gridDim.x);
   // a block has one group of a token's pieces: `per` of them, of as many tokens as it has threads for
   const int per_head = a.row_bytes >> 4, per_token = per_head * a.Hkv, pieces = 2 * per_token;
@@ -276,27 +300,44 @@ __global__ void __launch_bounds__(kWaveThreads, 1) compact_wave_kernel(const Com
   uint8_t* cache = (v ? a.v : a.k) + h * a.head_stride + 16 * (z - h * per_head);
   const int step = tokens * kWaveAhead;
   const int64_t wave = (int64_t)blocks * step;
-  for (int64_t w0 = 0; w0 < n; w0 += wave) {
-    const int64_t t0 = w0 + (int64_t)block * step + sub;
-    uint4 d[kWaveAhead];
-    int64_t to[kWaveAhead];
+  const int waves = (int)((n + wave - 1) / wave);
+  // of this thread's pieces of a wave: where they lie (FROM), or go; -1: nothing to move
+  auto moves_of = [&](int w, bool from, int64_t (&at)[kWaveAhead]) {
 #pragma unroll
     for (int j = 0; j < kWaveAhead; ++j) {
-      const int64_t t = t0 + (int64_t)j * tokens;
-      to[j] = -1;
-      if (have && t < n) {
-        const Move m = moves[t];
-        if (m.from >= 0) {
-          d[j] = *reinterpret_cast<const uint4*>(cache + m.from);
-          to[j] = m.to;
-        }
-      }
+      const int64_t t = w * wave + (int64_t)block * step + sub + (int64_t)j * tokens;
+      at[j] = !have || t >= n ? -1 : from ? moves[t].from : moves[t].to;
     }
-    if (!meet()) break;
+  };
+  auto piece = [&](int w, int j) { return held_pieces + (w % kWaves * kWaveAhead + j) * kWaveThreads + threadIdx.x; };
+  int64_t from[kWaveAhead], to[kWaveAhead];
+  auto read = [&](int w) {
 #pragma unroll
     for (int j = 0; j < kWaveAhead; ++j)
-      if (to[j] >= 0) *reinterpret_cast<uint4*>(cache + to[j]) = d[j];
+      if (from[j] >= 0)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(piece(w, j))), "l"(cache + from[j])
+                     : "memory");
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  moves_of(0, true, from);
+  read(0);
+  moves_of(1, true, from);
+  read(1);
+  moves_of(2, true, from);
+  asm volatile("cp.async.wait_group 1;" ::: "memory");
+  meet.arrive();                               // wave 0 is read
+  for (int w = 0; w < waves; ++w) {
+    read(w + 2);
+    moves_of(w + 3, true, from);
+    moves_of(w, false, to);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    meet.arrive();                             // wave w + 1 is
+    if (!meet.wait(w + 1)) break;
+#pragma unroll
+    for (int j = 0; j < kWaveAhead; ++j)
+      if (to[j] >= 0) *reinterpret_cast<uint4*>(cache + to[j]) = *piece(w, j);
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
   meet.leave();
 }
 
@@ -378,28 +419,41 @@ __global__ void __launch_bounds__(kRelThreads, 1) release_kernel(const ReleaseAr
     }
     row0 = lo;
   }
-  // f(place in the table or -1, page or -1) of each of them, all lanes together
+  // f(place in the table or -1, page or -1) of each of them, all lanes together; the first ones, which are all where
+  // the blocks are not short of SMs, are looked up once
   constexpr int kAhead = 4;
-  auto walk = [&](auto f) {
-    int r = row0, have = -1, lo = 0;
-    for (int b = begin; b < end; b += 32 * kAhead) {
-      int at[kAhead], p[kAhead];
+  int r = row0, have = -1, lo = 0;
+  auto look = [&](int b, int (&at)[kAhead], int (&p)[kAhead]) {
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const int e = b + 32 * j + lane;
-        at[j] = p[j] = -1;
-        if (e < end) {
-          while (e >= prefix[r + 1]) ++r;
-          if (have != r) span(r, lo);
-          have = r;
-          at[j] = r * a.max_pages + lo + (e - prefix[r]);
-          p[j] = a.block_table[at[j]];
-          if (p[j] < 0 || p[j] >= a.n_pages) {
-            if (p[j] != -1) bad |= MOE_DEVERR_CACHE;
-            p[j] = -1;
-          }
-        }
+    for (int j = 0; j < kAhead; ++j) {
+      const int e = b + 32 * j + lane;
+      at[j] = p[j] = -1;
+      if (e < end) {
+        while (e >= prefix[r + 1]) ++r;
+        if (have != r) span(r, lo);
+        have = r;
+        at[j] = r * a.max_pages + lo + (e - prefix[r]);
+        p[j] = a.block_table[at[j]];
       }
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (p[j] < 0 || p[j] >= a.n_pages) {
+        if (p[j] != -1) bad |= MOE_DEVERR_CACHE;
+        p[j] = -1;
+      }
+  };
+  int at0[kAhead], p0[kAhead];
+  look(begin, at0, p0);
+  const int r_next = r, have_next = have, lo_next = lo;
+  auto walk = [&](auto f) {
+    f(at0, p0);
+    r = r_next;
+    have = have_next;
+    lo = lo_next;
+    for (int b = begin + 32 * kAhead; b < end; b += 32 * kAhead) {
+      int at[kAhead], p[kAhead];
+      look(b, at, p);
       f(at, p);
     }
   };
@@ -518,7 +572,12 @@ cudaError_t launch_compact(const CompactArgs& a, cudaStream_t s) {
   const int64_t groups = ceil_div(pieces, kWaveThreads);
   static PerDeviceOnce once;
   int sms = 0;
-  const cudaError_t e = once.run([](int& v) { v = tc::num_sms(); return cudaSuccess; }, &sms);
+  const cudaError_t e = once.run(
+      [](int& v) {
+        v = tc::num_sms();
+        return cudaFuncSetAttribute(compact_wave_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kWaveSmem);
+      },
+      &sms);
   if (e != cudaSuccess) return e;
   // short lists; and tokens wider than the waves have blocks for (152 x 8 KB)
   if (a.N <= 1024 || groups > sms)
@@ -532,7 +591,8 @@ cudaError_t launch_compact(const CompactArgs& a, cudaStream_t s) {
     const int64_t step = kWaveThreads / std::min<int64_t>(pieces, kWaveThreads) * kWaveAhead;
     const int64_t blocks = std::min<int64_t>(sms / groups, ceil_div(n, step));
     if (e2 == cudaSuccess)
-      e2 = launch_cooperative(compact_wave_kernel, (unsigned)(blocks * groups), kWaveThreads, 0, s, a, moves, n, (int)groups);
+      e2 = launch_cooperative(compact_wave_kernel, (unsigned)(blocks * groups), kWaveThreads, kWaveSmem, s, a, moves, n,
+                              (int)groups);
     if (e2 != cudaSuccess) return e2;
   }
   return cudaSuccess;
