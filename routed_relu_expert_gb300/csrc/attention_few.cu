@@ -1,5 +1,6 @@
-// Attention with shared prefixes where a request (or a group) has few rows: up to 32
-// of a KV head.  BF16 rows and caches, FP32 scores, softmax and sums.
+// Attention with shared prefixes where a request (or a group) has few rows: up to 32 of
+// a KV head, or any number where all of them together have few keys.  BF16 rows and
+// caches, FP32 scores, softmax and sums.
 //
 //   S = Q K^T,  p = exp2(c S - m),  l = sum p,  O = sum p V,  out = O / l
 //
@@ -32,6 +33,11 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kSub = 16;                       // keys a step
 constexpr int kUnitCost = 2;                   // a unit's fixed cost beside its steps, in steps
 constexpr int kMinRun = 4, kMaxParts = 64;     // steps of a run at least; runs of a unit at most (about)
+// This kernel takes all rows where every 16 of them together read at most so many bytes of keys and values, by the
+// tables' width.  Both ways, graph replay, us: 16 requests behind 500 common tokens 21.9 for 30.1, 64 of them (136 MB) 34 for 41, 17 in three groups
+// behind 1500 to 3001 (80 MB) 25.7 for 28.8, 12 behind 2000 (72 MB) 26 for 30; 32 (172 MB) 35 for 35, 64 (344 MB) 57 for 44,
+// 8 behind 8000 (174 MB) 43 for 33.
+constexpr int64_t kFewBytes = 96ll << 20;
 constexpr float kRaise = 8.f;                  // log2 units by which a maximum may pass its reference
 
 __device__ __forceinline__ float ex2(float x) {
@@ -427,7 +433,7 @@ cudaError_t launch_dp(const AttnArgs& a, cudaStream_t s) {
       &blocks);
   if (e != cudaSuccess) return e;
   // keys that count as one step of the cost: 16, or as many more as keep the cost of all units in 31 bits
-  const int64_t units = 2ll * (a.n_groups + a.R) * a.Hkv, keys = (int64_t)a.max_pages << a.page_shift;
+  const int64_t units = 2ll * (a.n_groups + a.R + ceil_div(a.T, kFewRows / a.G)) * a.Hkv, keys = (int64_t)a.max_pages << a.page_shift;
   int shift = 0;
   while (units * (((keys + (kSub << shift) - 1) >> shift) / kSub + 1 + kUnitCost) >= ((int64_t)1 << 31)) ++shift;
   // no more blocks than the longest tables' rows have runs for
@@ -440,7 +446,11 @@ cudaError_t launch_dp(const AttnArgs& a, cudaStream_t s) {
 
 void few_shape(AttnArgs* a) {
   if (a->G > kFewRows) return;                 // (a token's rows do not fit a unit's 16)
-  a->few_tokens = kFewBlocks * (kFewRows / a->G);
+  const int tb = kFewRows / a->G;
+  a->few_tokens = kFewBlocks * tb;
+  // all of them where reading a prefix once for every 16 rows is less than a second kernel costs
+  const int64_t keys = (int64_t)ceil_div(a->T, tb) * a->Hkv * ((int64_t)a->max_pages << a->page_shift);
+  if (keys <= kFewBytes / (a->D <= 64 ? 256 : 512)) a->few_tokens = std::max(a->few_tokens, a->T);
   a->few_alone = a->T <= a->few_tokens;
 }
 

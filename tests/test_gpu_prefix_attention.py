@@ -11,9 +11,25 @@ from test_gpu_attention import BF, FP, HALF, Step, _code, _err, _i32, _m
 pytestmark = pytest.mark.gpu
 
 
+@pytest.fixture(autouse=True, params=["as wide as the lengths", "wide tables"])
+def table_width(request, monkeypatch):
+    """Where the tables' width bounds the work to little, one kernel takes all rows; every test
+    runs with tables of 2^19 tokens, too, where units of many rows have a kernel of their own."""
+    monkeypatch.setattr(Shared, "tokens", 1 << 19 if request.param == "wide tables" else 0)
+
+
 class Shared(Step):
     """groups: (first request, one past the last, prefix tokens, table row of the prefix); the
     own rows of a group's requests do not have the shared pages (only prefix_row has)."""
+    tokens = 0                                               # that a table's row has room for, at least
+
+    def widen(self, table):
+        """The table on the device, with room for self.tokens, and a configuration for it."""
+        self.cfg = _m().make_attn_config(self.H, self.Hkv, self.D, page_size=self.page, n_pages=self.k.shape[0],
+                                         max_pages=max(table.shape[1], self.tokens // self.page), dtype=_code(self.dt),
+                                         k_cache=self.k)
+        self.table_d = torch.full((self.R, self.cfg.max_pages), -1, dtype=torch.int32, device="cuda")
+        self.table_d[:, :table.shape[1]] = torch.as_tensor(table)
 
     def __init__(self, ctx, new, H, Hkv, D, page, dt, groups, *, own_rows=False, **kw):
         super().__init__(ctx, new, H, Hkv, D, page, dt, **kw)
@@ -27,7 +43,7 @@ class Shared(Step):
                     continue                                 # attended through its own row alone
                 self.table[r, :whole] = self.table[row, :whole]
                 device[r, :whole] = self.table[row, :whole] if own_rows or r == row else -1
-        self.table_d = torch.from_numpy(device).cuda()
+        self.widen(device)
         bounds = [groups[0][0]] + [g[1] for g in groups] if groups else [0]
         assert all(g[0] == x for g, x in zip(groups, bounds))
         self.start, self.row, self.length = _i32(bounds), _i32([g[3] for g in groups]), _i32([g[2] for g in groups])
@@ -159,7 +175,8 @@ def test_bad_groups_are_flagged_and_share_nothing(dt):
     for change in (dict(start=[-1, 2]), dict(start=[0, 9]), dict(start=[2, 1]), dict(row=[7]), dict(row=[-1]),
                    dict(length=[-16]), dict(length=[10 ** 6])):
         s = make()
-        s.table_d, s.k, s.v = plain.table_d, plain.k, plain.v
+        s.k, s.v = plain.k, plain.v
+        s.widen(plain.table)
         for name, value in change.items():
             setattr(s, name, _i32(value))
         out, lse = s.run()
@@ -197,14 +214,16 @@ def test_offsets_past_32_bits(dt):
     store = torch.empty(2 * n, dtype=dt, device="cuda")
     k, v = (store.as_strided((2, page, Hkv, D), (stride, Hkv * D, D, 1), at) for at in (0, n))
     s = Shared([16, 16], [3, 3], H, Hkv, D, page, dt, [(0, 2, 16, 0)], seed=11, tree=False)
+    near = s.k, s.v
     a, b = int(s.table[0, 0]), int(s.table[0, 1])
     for p, x in ((1, a), (0, b)):
         k[p], v[p] = s.k[x], s.v[x]
     s.k[int(s.table[1, 1])], s.v[int(s.table[1, 1])] = s.k[b], s.v[b]        # the second request's own page, too
-    cfg = M.make_attn_config(H, Hkv, D, page_size=page, n_pages=2, max_pages=2, dtype=_code(dt), k_cache=k)
+    s.k, s.v = k, v
+    s.widen(np.array([[1, 0], [-1, 0]], np.int32))
     out, lse = torch.empty((6, H, D), dtype=dt, device="cuda"), torch.empty((6, H), device="cuda")
-    M.moe_prefix_attention(cfg, s.q, s.q_start, s.kv_len, _i32([[1, 0], [-1, 0]]), s.start, s.row, s.length, k, v, out, s.ws,
-                           lse=lse)
+    M.moe_prefix_attention(s.cfg, s.q, s.q_start, s.kv_len, s.table_d, s.start, s.row, s.length, k, v, out, s.ws, lse=lse)
+    s.k, s.v = near
     s.check(out, lse)
 
 
