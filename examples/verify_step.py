@@ -58,14 +58,10 @@ class Layer:
         root down): their K and V move to the request's next tokens, and the pages of the
         rejected ones go back."""
         c = self.cache
+        start = torch.zeros(len(lengths) + 1, dtype=torch.int32, device="cuda")
+        start[1:] = torch.cumsum(lengths, 0)
         owner = torch.repeat_interleave(torch.arange(len(lengths), device="cuda"), lengths)
-        first = torch.cumsum(lengths, 0) - lengths
-        token = ctx_len[owner].long() + torch.arange(rows.numel(), device="cuda") - first[owner]
-        page = c.block_table[owner, token // PAGE].long()
-        for store in (c.k_cache, c.v_cache):
-            flat = store.view(-1, HKV, HEAD)
-            flat[page * PAGE + token % PAGE] = flat[plan.slot_map[rows]]   # (read whole before it is written)
-        after = ctx_len + lengths.to(torch.int32)
+        after = c.compact(ctx_len, start, (rows - plan.q_start[owner]).to(torch.int32))
         c.release(plan.kv_len, after)
         return after
 

@@ -75,6 +75,13 @@ CASES = [
     ([2100, 2048], [1, 2], 128, 1, 64, 1024, True, False, [(0, 2, 2048, 0)]),              # one token a block
     ([600] * 6, [1] * 6, 1, 1, 8, 8, False, False, [(0, 3, 600, 0), (3, 6, 333, 5)]),
     ([128 * 5] * 9, [4] * 9, 16, 2, 128, 256, True, False, [(0, 9, 640, 3)]),              # pages larger than a tile
+    # as many rows as two blocks of 16 have, one more and one fewer: 16, 17, 4, 5 and 1 query heads a KV head
+    ([330, 300, 301, 340], [1, 2, 3, 2], 32, 2, 64, 16, True, False, [(0, 2, 300, 0), (2, 4, 290, 3)]),
+    ([330, 300, 301], [1, 2, 1], 17, 1, 64, 16, True, False, [(0, 3, 300, 0)]),
+    ([150, 140, 500, 7, 141], [8, 9, 7, 8, 1], 8, 2, 128, 16, True, False, [(0, 2, 140, 0), (2, 3, 20, 2), (3, 5, 7, 3)]),
+    ([150, 140, 500, 150], [6, 7, 5, 12], 10, 2, 64, 16, False, True, [(0, 4, 140, 2)]),
+    ([64, 50, 81, 64], [32, 33, 31, 1], 2, 2, 64, 16, True, False, [(0, 2, 48, 0), (2, 4, 64, 3)]),
+    ([30000, 29990, 200], [1, 2, 1], 8, 2, 128, 64, False, False, [(0, 2, 10000, 0)]),     # long rows, few of them
     ([700 + i for i in range(40)], [1 + i % 3 for i in range(40)], 8, 2, 64, 16, True, False,
      [(0, 13, 700, 0), (13, 26, 333, 20), (26, 40, 50, 39)]),
 ]

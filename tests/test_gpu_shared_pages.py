@@ -431,6 +431,56 @@ def test_release_in_a_graph_and_on_another_stream():
         assert all(np.array_equal(_np(a).reshape(-1), np.asarray(b).reshape(-1)) for a, b in zip(state, want))
 
 
+def test_two_graphs_of_launches_whose_blocks_meet():
+    """Lists and tables long enough for blocks that wait for one another; two captured calls
+    share a workspace, and lengths are read at the replay."""
+    M = _m()
+    d = lambda x: torch.from_numpy(np.asarray(x, np.int32).copy()).cuda()
+    c = Compact([3, 40], [9000, 7000], [5000, 6000], 16, Hkv=8, D=64)
+    r = Release([8000, 4001], [(7 * i) % 1000 for i in range(600)], 16, group=16)
+    r.ws = c.ws if c.ws.numel() >= r.ws.numel() else r.ws
+    k, v, lens = c.k.clone(), c.v.clone(), _i32([0, 0])
+    start = np.concatenate([[0], np.cumsum([len(x) for x in c.keep])])
+    lists = [d(c.first), d(start), d(np.concatenate(c.keep)), d(c.table)]
+    state = [d(r.table), d(r.shares), d(r.free), _i32([r.head])]
+    begin, now, keep = [x.clone() for x in state], d(r.now), d(r.now * 0)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):                            # first calls outside a graph
+        M.moe_paged_compact(c.cfg, *lists, k, v, r.ws, len_out=lens)
+        M.moe_paged_release(r.cfg, now, keep, state[0], state[2], state[3], r.ws, page_shares=state[1])
+    side.synchronize()
+    graphs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()]
+    with torch.cuda.graph(graphs[0]):
+        k.copy_(c.k)
+        v.copy_(c.v)
+        M.moe_paged_compact(c.cfg, *lists, k, v, r.ws, len_out=lens)
+    with torch.cuda.graph(graphs[1]):
+        for x, y in zip(state, begin):
+            x.copy_(y)
+        M.moe_paged_release(r.cfg, now, keep, state[0], state[2], state[3], r.ws, page_shares=state[1])
+    for cut in (1.0, 0.0, 0.5):
+        left = (r.now * cut).astype(int)
+        keep.copy_(d(left))
+        c.keep[0] = c.keep[0][:int(5000 * cut)]              # a shorter list: what is behind it belongs to no request
+        lists[1].copy_(d([0, len(c.keep[0]), len(c.keep[0]) + len(c.keep[1])]))
+        lists[2][:len(c.keep[0]) + len(c.keep[1])] = d(np.concatenate(c.keep))
+        for g in graphs:
+            g.replay()
+        wk, wv = c.want()
+        assert torch.equal(k, wk) and torch.equal(v, wv) and lens.tolist() == [3 + len(c.keep[0]), 40 + len(c.keep[1])]
+        want = release_reference(r.table, r.shares, r.free, r.head, r.now, left, 16)
+        assert all(np.array_equal(_np(a).reshape(-1), np.asarray(b).reshape(-1)) for a, b in zip(state, want))
+    assert _err(r.ws) == 0
+
+
+@pytest.mark.parametrize("Hkv,dt", [(32, FP), (20, FP), (32, BF), (33, BF)])
+def test_compact_of_long_lists_and_wide_tokens(Hkv, dt):
+    """More pieces a token than a block of the long lists' kernel has threads, and none beside it."""
+    s = Compact([5, 0], [1700, 900], [1500, 20], 16, dt=dt, Hkv=Hkv, D=128)
+    s.check()
+    assert _err(s.ws) == 0
+
+
 # ---------------------------------------------------------------------------
 # offsets past 32 bits
 # ---------------------------------------------------------------------------
