@@ -566,12 +566,15 @@ moe_status_t moe_paged_fork(const moe_attn_config_t* cfg, int32_t n, const int32
  *   R          requests, 0..16384;  N: entries of keep
  *   first [R], keep_start [R+1], keep [N] int32: ascending numbers, from 0, a request
  *   page_shares [n_pages] int32 or NULL: where given, a shared page is not written to
- *   len_out    [R] int32 out or NULL: first + number of kept tokens
+ *   len_out    [R] int32 out or NULL: first + number of kept tokens; not the memory of
+ *              first, keep_start or keep (MOE_ERR_INVALID_ARG)
  * Kept numbers that do not ascend, tokens past the table's row, pages outside the
  * cache and shared pages that would be written: the token is not moved, with
  * MOE_DEVERR_CACHE (so is a request whose keep_start or first is out of range left
  * as it is, with len_out = max(first, 0)).  The pages stay the request's; the ones behind the
- * kept tokens go back with moe_paged_release.                                      */
+ * kept tokens go back with moe_paged_release.  Above 1024 entries the blocks of a
+ * cooperative launch wait for one another, 4 seconds at most: then MOE_DEVERR_TIMEOUT, and
+ * some tokens are not moved.                                                      */
 moe_status_t moe_paged_compact(const moe_attn_config_t* cfg, int32_t R, int32_t N, const int32_t* first,
                                const int32_t* keep_start, const int32_t* keep, const int32_t* block_table,
                                const int32_t* page_shares, int32_t* len_out, void* k_cache, void* v_cache, void* ws,
@@ -589,7 +592,9 @@ moe_status_t moe_paged_compact(const moe_attn_config_t* cfg, int32_t R, int32_t 
  *   free_pages [n_free] int32, free_head [1] int32, in and out
  * Entries -1 are passed over.  Negative lengths (count as 0), page ids outside the
  * cache, a page given back more often than it is held, and more pages than the list
- * gave out (the first ones are dropped): MOE_DEVERR_CACHE.                          */
+ * gave out (the first ones are dropped): MOE_DEVERR_CACHE.  Blocks wait for one
+ * another as in moe_paged_compact where R * max_pages is above 2048; after
+ * MOE_DEVERR_TIMEOUT the list and the table are as they were, the counts need not be.  */
 moe_status_t moe_paged_release(const moe_attn_config_t* cfg, int32_t R, const int32_t* held_len,
                                const int32_t* keep_len, int32_t* block_table, int32_t* page_shares,
                                int32_t* free_pages, int32_t n_free, int32_t* free_head, void* ws, size_t ws_bytes,

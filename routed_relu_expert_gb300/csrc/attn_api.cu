@@ -58,6 +58,11 @@ inline bool bad_caches(const void* k, const void* v) {
   return !k || !v || !aligned(k, 16) || !aligned(v, 16) || k == v;
 }
 
+// whether two arrays have memory in common
+inline bool meet(const int32_t* a, int64_t n, const int32_t* b, int64_t m) {
+  return a && b && (uintptr_t)a < (uintptr_t)b + 4 * m && (uintptr_t)b < (uintptr_t)a + 4 * n;
+}
+
 constexpr size_t kWorkspaceBytes = MOE_ATTN_HEADER_BYTES + kAttnPartBytes + kAttnJoinBytes;
 
 // of a configuration: moe_paged_release has a word a page where attention has its partials
@@ -512,6 +517,9 @@ moe_status_t moe_paged_compact(const moe_attn_config_t* cfg, int32_t R, int32_t 
     return MOE_ERR_INVALID_ARG;
   if (bad_caches(k_cache, v_cache)) return MOE_ERR_INVALID_ARG;
   if ((page_shares && !aligned(page_shares, 4)) || (len_out && !aligned(len_out, 4))) return MOE_ERR_INVALID_ARG;
+  // (other blocks read the lists while a length is written)
+  if (meet(len_out, R, first, R) || meet(len_out, R, keep_start, (int64_t)R + 1) || meet(len_out, R, keep, N))
+    return MOE_ERR_INVALID_ARG;
   const int es = elem_bytes(cfg);
   CompactArgs a{};
   a.scratch = reinterpret_cast<uint8_t*>(ws) + MOE_ATTN_HEADER_BYTES;

@@ -49,7 +49,9 @@ def test_compact_refusals(lib):  # noqa: F811
 
     for kw in (dict(rows=-1), dict(kept=-1), dict(first=None), dict(start=None), dict(keep=None), dict(table=None),
                dict(kc=None), dict(vc=None), dict(kc=_ptr(7)), dict(vc=_ptr(7, 8)), dict(shares=_ptr(4, 2)),
-               dict(out=_ptr(5, 1)), dict(keep=_ptr(2, 2)), dict(ws=None), dict(cfg=_cfg(n_pages=0))):
+               dict(out=_ptr(5, 1)), dict(keep=_ptr(2, 2)), dict(ws=None), dict(cfg=_cfg(n_pages=0)),
+               # lengths written where the lists are read
+               dict(out=_ptr(0)), dict(out=_ptr(0, 4)), dict(out=_ptr(0, -4)), dict(out=_ptr(1, 8)), dict(out=_ptr(2, 16))):
         assert call(**kw) == N.MOE_ERR_INVALID_ARG, kw
     assert call(rows=20000) == N.MOE_ERR_UNSUPPORTED
     assert call(ws_bytes=n - 1) == N.MOE_ERR_WORKSPACE
