@@ -572,7 +572,7 @@ moe_status_t moe_paged_fork(const moe_attn_config_t* cfg, int32_t n, const int32
  * cache and shared pages that would be written: the token is not moved, with
  * MOE_DEVERR_CACHE (so is a request whose keep_start or first is out of range left
  * as it is, with len_out = max(first, 0)).  The pages stay the request's; the ones behind the
- * kept tokens go back with moe_paged_release.  Above 1024 entries the blocks of a
+ * kept tokens go back with moe_paged_release.  For long lists the blocks of a
  * cooperative launch wait for one another, 4 seconds at most: then MOE_DEVERR_TIMEOUT, and
  * some tokens are not moved.                                                      */
 moe_status_t moe_paged_compact(const moe_attn_config_t* cfg, int32_t R, int32_t N, const int32_t* first,
@@ -593,7 +593,7 @@ moe_status_t moe_paged_compact(const moe_attn_config_t* cfg, int32_t R, int32_t 
  * Entries -1 are passed over.  Negative lengths (count as 0), page ids outside the
  * cache, a page given back more often than it is held, and more pages than the list
  * gave out (the first ones are dropped): MOE_DEVERR_CACHE.  Blocks wait for one
- * another as in moe_paged_compact where R * max_pages is above 2048; after
+ * another as in moe_paged_compact where R * max_pages is above 1024; after
  * MOE_DEVERR_TIMEOUT the list and the table are as they were, the counts need not be.  */
 moe_status_t moe_paged_release(const moe_attn_config_t* cfg, int32_t R, const int32_t* held_len,
                                const int32_t* keep_len, int32_t* block_table, int32_t* page_shares,

@@ -80,6 +80,11 @@ __device__ __forceinline__ int block_sum(int v, int* tmp) {
 // ---------------------------------------------------------------------------
 // fork
 // ---------------------------------------------------------------------------
+// Every block adds up the pages that the forks before its own take, shares its source's
+// whole pages and copies a part of the last one's tokens: one launch, no order among blocks.
+// Bound: L2 and HBM for many forks, the chain of dependent loads (rows, table, page, tokens)
+// for few.  512 forks of 16 prompts of up to 8000 tokens (120 MB of copied tokens): 24.8 us,
+// 4.8 TB/s, as with 8 and 32 pieces a thread (64: 26 to 30); one fork 4.2 us.
 constexpr int kForkAhead = 4;                  // 16-byte pieces that a thread has in flight
 // blockIdx.x: the fork; blockIdx.y: a part of its page's tokens
 __global__ void __launch_bounds__(kThreads) fork_kernel(const ForkArgs a) {
@@ -216,7 +221,8 @@ __device__ __forceinline__ void list_of(const CompactArgs& a, int r, int& first,
 }
 
 // Short lists: a block has a request and kThreads of a token's 16-byte pieces, a thread
-// one of them for token after token.
+// one of them for token after token.  Bound: the chain of dependent loads (list, table,
+// tokens), a list's tokens eight at a time; 64 requests that keep 6 of 16 nodes: 2.8 us.
 constexpr int kStage = 256;                    // moves worked out at a time
 constexpr int kMoveAhead = 8;                  // tokens whose loads a thread has in flight
 __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a) {
@@ -251,6 +257,10 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a) 
   if (bad) set_error(&a.hdr->err, bad);
 }
 
+// Which of the two, graph replay, us, short / long: lists of 8 on average (512 requests) 6.2 / 13.1, of 16 (64) 8.2 / 12.3,
+// of 32 (16) 10.3 / 12.3, of 64 (16) 17.8 / 12.3; one list of 200 24.6 / 12.3, of 4000 474 / 16.4, of 66667 31000 / 113.
+// kShortAll: so that one list among short ones cannot take longer than a few hundred us.
+constexpr int kShortList = 32, kShortAll = 4096;
 // Long lists, in two launches.  The first works the moves out, a thread a token (of all
 // requests' lists as one).
 __global__ void __launch_bounds__(kThreads) compact_moves_kernel(const CompactArgs a, Move* moves, int i0, int n) {
@@ -281,7 +291,9 @@ __global__ void __launch_bounds__(kThreads) compact_moves_kernel(const CompactAr
 // block has met the others for the next wave before it writes this one.  Token i of the lists
 // goes to a place at or before its source, so what a wave writes lies behind every later
 // wave's sources and only its own wave and earlier ones read there.  A thread reads and
-// writes its own 16-byte pieces.
+// writes its own 16-byte pieces.  Bound: HBM, reads and writes in turn.  66667 of 100001
+// tokens of 4 KB (546 MB): 110 us, 5.0 TB/s or 73 % of a plain copy; a wave at a time 155,
+// the next one's reads beside the meeting 133.
 constexpr int kWaveThreads = 512;
 constexpr int kWaves = 3;                      // in a block's shared memory
 constexpr int kWaveAhead = 9;                  // pieces of a thread a wave (72 KB a block)
@@ -346,7 +358,7 @@ __global__ void __launch_bounds__(kWaveThreads, 1) compact_wave_kernel(const Com
 // ---------------------------------------------------------------------------
 constexpr int kRelThreads = 1024;
 constexpr int kRelWarps = kRelThreads / 32;
-constexpr int kRelEntries = 2 * kRelThreads;   // of a block, before another one helps
+constexpr int kRelEntries = kRelThreads;       // of a block, before another one helps (2048: 20.4 for 18.7 us, 4096: 25.6)
 
 // exclusive prefix of one value a thread over the block; *total: their sum
 __device__ __forceinline__ int block_scan(int v, int* tmp, int* total) {
@@ -376,7 +388,12 @@ __device__ __forceinline__ int block_scan(int v, int* tmp, int* total) {
 }
 
 // All entries that are given back, in the table's order, are cut into equal parts, a
-// block each, and a block's into its warps'; lanes take neighbours.
+// block each, and a block's into its warps'; lanes take neighbours.  A page's holders go
+// down by atomics on whole numbers, whose order does not matter; which of its entries is the last
+// in the table, and so gives it back, is a maximum; places in the list come from prefix sums
+// of warps, blocks and the grid.  Bound: the latency of the phases and of up to three meetings
+// (2 us each).  1024 requests, most of their pages shared by 16: 18.7 us; 64 requests: 6.0 us;
+// with one block for everything the 1024 took 142 us.
 __global__ void __launch_bounds__(kRelThreads, 1) release_kernel(const ReleaseArgs a) {
   extern __shared__ int prefix[];              // [R + 1] entries before each request
   __shared__ int tmp[32];
@@ -580,7 +597,7 @@ cudaError_t launch_compact(const CompactArgs& a, cudaStream_t s) {
       &sms);
   if (e != cudaSuccess) return e;
   // short lists; and tokens wider than the waves have blocks for (152 x 8 KB)
-  if (a.N <= 1024 || groups > sms)
+  if (a.N <= std::min<int64_t>((int64_t)kShortList * a.R, kShortAll) || groups > sms)
     return launch_k(compact_kernel, dim3((unsigned)a.R, (unsigned)ceil_div(pieces, kThreads)), kThreads, 0, s, a);
   Move* moves = reinterpret_cast<Move*>(a.scratch);
   const int most = (int)(a.scratch_bytes / sizeof(Move));
