@@ -34,11 +34,16 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kSub = 16;                       // keys a step
 constexpr int kUnitCost = 2;                   // a unit's fixed cost beside its steps, in steps
-constexpr int kMinRun = 4, kMaxParts = 64;     // steps of a run at least; runs of a unit at most (about)
+// steps of a run at least (2 / 3 / 4 / 6, us: two samples behind 500 tokens 12.5 / 12.2 / 13.8 / 14.6, behind 2000 18.8 /
+// 16.3 / 17.1 / 16.8); runs of a unit at most (about)
+constexpr int kMinRun = 3, kMaxParts = 64;
+// blocks an SM (2 / 3: 16 requests behind 500 tokens 14.4 / 15.2, 128 behind 8000 89.4 / 89.5 and with twice the nodes
+// 129 / 127); with three stages a warp 14.8 and 91.8
+constexpr int kBlocks = 2;
 // This kernel takes all rows where every 16 of them together read at most so many bytes of keys and values, by the
-// tables' width.  Both ways, graph replay, us: 16 requests behind 500 common tokens 21.9 for 30.1, 64 of them (136 MB) 34 for 41, 17 in three groups
-// behind 1500 to 3001 (80 MB) 25.7 for 28.8, 12 behind 2000 (72 MB) 26 for 30; 32 (172 MB) 35 for 35, 64 (344 MB) 57 for 44,
-// 8 behind 8000 (174 MB) 43 for 33.
+// tables' width.  Both ways, graph replay, us: 16 requests behind 500 common tokens 21.9 for 30.1, 64 of them (136 MB)
+// 34 for 41, 17 in three groups behind 1500 to 3001 (80 MB) 25.7 for 28.8, 12 behind 2000 (72 MB) 26 for 30; 32 (172
+// MB) 35 for 35, 64 (344 MB) 57 for 44, 8 behind 8000 (174 MB) 43 for 33.
 constexpr int64_t kFewBytes = 96ll << 20;
 constexpr float kRaise = 8.f;                  // log2 units by which a maximum may pass its reference
 
@@ -85,7 +90,7 @@ struct Geo {
 };
 
 template <int DP>
-__global__ void __launch_bounds__(kThreads, 3) attention_few_kernel(const AttnArgs a, int shift) {
+__global__ void __launch_bounds__(kThreads, kBlocks) attention_few_kernel(const AttnArgs a, int shift) {
   using X = Geo<DP>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t s_scan[kWarps];
@@ -428,7 +433,7 @@ cudaError_t launch_dp(const AttnArgs& a, cudaStream_t s) {
   int blocks = 0;
   const cudaError_t e = once.run(
       [](int& v) {
-        v = std::min(3 * tc::num_sms(), kFewRuns / kWarps);
+        v = std::min(kBlocks * tc::num_sms(), kFewRuns / kWarps);
         return cudaFuncSetAttribute(attention_few_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     X::SMEM + (3 * kPrefixMaxRequests + 1) * 4);
       },
