@@ -22,39 +22,40 @@ struct GridMeet {
   int blocks, met = 0;
   bool ok = true;
   __device__ GridMeet(AttnHeader* h, int n) : hdr(h), blocks(n) {}
-  // what this block has read and written until here is done for who waits for it
+  // what this block has read until here (and, WRITTEN, written) is done for who waits for it.  Reads need no fence: they
+  // have returned their values.
+  template <bool WRITTEN>
   __device__ void arrive() {
     __syncthreads();
     if (blocks > 1 && threadIdx.x == 0) {
-      __threadfence();
+      if (WRITTEN) __threadfence();
       atomicAdd(&hdr->met, 1);
     }
   }
   // until every block has arrived `times` times
   __device__ bool wait(int times) {
     if (blocks == 1) return true;
-    __shared__ int good;
+    __shared__ int good[2];                    // (in turn: a word is written again two waits later)
     if (threadIdx.x == 0) {
       const uint64_t t0 = globaltimer();
-      int seen, tries = 0;
-      good = 1;
+      int seen, tries = 0, fine = 1;
       while (true) {
         asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(seen) : "l"(&hdr->met) : "memory");
         if (seen >= times * blocks) break;
         if ((++tries & 255) == 0 && globaltimer() - t0 > tc::kWaitLimitNs) {
-          good = 0;
+          fine = 0;
           set_error(&hdr->err, MOE_DEVERR_TIMEOUT);
           break;
         }
       }
+      good[times & 1] = fine;
     }
     __syncthreads();
-    ok = ok && good;
-    __syncthreads();                           // (the word is the next wait's)
+    ok = ok && good[times & 1];
     return ok;
   }
   __device__ bool operator()() {
-    arrive();
+    arrive<true>();
     return wait(++met);
   }
   __device__ void leave() {
@@ -292,8 +293,10 @@ __global__ void __launch_bounds__(kThreads) compact_moves_kernel(const CompactAr
 // goes to a place at or before its source, so what a wave writes lies behind every later
 // wave's sources and only its own wave and earlier ones read there.  A thread reads and
 // writes its own 16-byte pieces.  Bound: HBM, reads and writes in turn.  66667 of 100001
-// tokens of 4 KB (546 MB): 110 us, 5.0 TB/s or 73 % of a plain copy; a wave at a time 155,
-// the next one's reads beside the meeting 133.
+// tokens of 4 KB (546 MB): 94 us, 5.8 TB/s or 86 % of a plain copy (a wave at a time 155,
+// the next one's reads beside the meeting 133, two waves' reads 110, without a fence for
+// writes that nobody waits for 94); a wave costs half a microsecond beside its bytes, so
+// that more and smaller ones are slower (four of 48 KB 101, four of 32 KB 111).
 constexpr int kWaveThreads = 512;
 constexpr int kWaves = 3;                      // in a block's shared memory
 constexpr int kWaveAhead = 9;                  // pieces of a thread a wave (72 KB a block)
@@ -331,19 +334,19 @@ __global__ void __launch_bounds__(kWaveThreads, 1) compact_wave_kernel(const Com
                      : "memory");
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  moves_of(0, true, from);
-  read(0);
-  moves_of(1, true, from);
-  read(1);
-  moves_of(2, true, from);
-  asm volatile("cp.async.wait_group 1;" ::: "memory");
-  meet.arrive();                               // wave 0 is read
+  for (int w = 0; w < kWaves - 1; ++w) {
+    moves_of(w, true, from);
+    read(w);
+  }
+  moves_of(kWaves - 1, true, from);
+  asm volatile("cp.async.wait_group %0;" ::"n"(kWaves - 2) : "memory");
+  meet.arrive<false>();                        // wave 0 is read
   for (int w = 0; w < waves; ++w) {
-    read(w + 2);
-    moves_of(w + 3, true, from);
+    read(w + kWaves - 1);
+    moves_of(w + kWaves, true, from);
     moves_of(w, false, to);
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
-    meet.arrive();                             // wave w + 1 is
+    asm volatile("cp.async.wait_group %0;" ::"n"(kWaves - 2) : "memory");
+    meet.arrive<false>();                      // wave w + 1 is
     if (!meet.wait(w + 1)) break;
 #pragma unroll
     for (int j = 0; j < kWaveAhead; ++j)
