@@ -473,6 +473,50 @@ def test_two_graphs_of_launches_whose_blocks_meet():
     assert _err(r.ws) == 0
 
 
+def test_the_most_forks_and_requests():
+    s = Fork([50, 33], [(i % 2, 2 + i, 1 + i % 33) for i in range(4096)], 8, D=8)
+    s.check()
+    assert _err(s.ws) == 0
+    R = 16384
+    s = Compact([i % 9 for i in range(R)], [1 + i % 4 for i in range(R)], [i % 2 for i in range(R)], 8, D=8)
+    s.check()
+    assert _err(s.ws) == 0
+    s = Release([16, 40], [i % 30 for i in range(R)], 8, group=4)
+    for keep in (s.now * 0, np.maximum(s.now - 11, 0)):
+        s.check(keep)
+    assert _err(s.ws) == 0
+
+
+def test_calls_on_several_streams_at_once():
+    """Each with a workspace of its own; those whose blocks wait for one another, too."""
+    M = _m()
+    d = lambda x: torch.from_numpy(np.asarray(x, np.int32).copy()).cuda()
+    lists = [Compact([3], [9000 + 500 * i], [6000], 16, Hkv=8, D=64, seed=i) for i in range(3)]
+    tables = [Release([8000, 4001], [(7 * i) % 1000 for i in range(400)], 16, group=16, seed=i) for i in range(3)]
+    args, runs = [], []
+    for c in lists:
+        start = [0, len(c.keep[0])]
+        args.append((c.cfg, d(c.first), d(start), d(c.keep[0]), d(c.table), c.k.clone(), c.v.clone(), c.ws))
+    for r in tables:
+        runs.append([d(r.table), d(r.shares), d(r.free), _i32([r.head]), d(r.now), d(r.now * 0)])
+    streams = [torch.cuda.Stream() for _ in range(6)]
+    torch.cuda.synchronize()
+    for i in range(3):
+        with torch.cuda.stream(streams[2 * i]):
+            M.moe_paged_compact(*args[i])
+        with torch.cuda.stream(streams[2 * i + 1]):
+            t, sh, f, h, now, keep = runs[i]
+            M.moe_paged_release(tables[i].cfg, now, keep, t, f, h, tables[i].ws, page_shares=sh)
+    torch.cuda.synchronize()
+    for c, a in zip(lists, args):
+        wk, wv = c.want()
+        assert torch.equal(a[5], wk) and torch.equal(a[6], wv) and _err(c.ws) == 0
+    for r, state in zip(tables, runs):
+        want = release_reference(r.table, r.shares, r.free, r.head, r.now, r.now * 0, 16)
+        assert all(np.array_equal(_np(a).reshape(-1), np.asarray(b).reshape(-1)) for a, b in zip(state, want))
+        assert _err(r.ws) == 0
+
+
 @pytest.mark.parametrize("Hkv,dt", [(32, FP), (20, FP), (32, BF), (33, BF)])
 def test_compact_of_long_lists_and_wide_tokens(Hkv, dt):
     """More pieces a token than a block of the long lists' kernel has threads, and none beside it."""
