@@ -761,11 +761,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Bound: latency of the record, the pairs and the columns, then HBM and L2; 128 requests (30
 // MB of partials) 9.7 us, 17 requests 6 to 8 us.  Done in the kernel for few rows,
 // prefix partials cost it more than this launch.
-constexpr int kJoinThreads = 256;
-template <int DP>
-__global__ void __launch_bounds__(kJoinThreads, 4) prefix_join_kernel(const AttnArgs a) {
+// kAhead: a row's partials in flight, 16 where all rows are resident at once with as many registers, else 8 (16 / 8, us
+// a call: two samples behind 2000 tokens 15.1 / 16.1, 17 requests 20.9 / 21.3, 128 requests 88 / 84).
+constexpr int kJoinThreads = 128;
+constexpr int kJoinBlocks = 4;                 // an SM, with 16 in flight
+template <int DP, int kAhead>
+__global__ void __launch_bounds__(kJoinThreads, kAhead == 16 ? kJoinBlocks : 2 * kJoinBlocks)
+    prefix_join_kernel(const AttnArgs a) {
   constexpr int L = DP / 4;                    // lanes a row
-  constexpr int kAhead = 8;                    // partials in flight
   pdl_wait();
   const int lane = threadIdx.x & 31, sub = lane % L;
   const int rows_all = a.T * a.G, id = (blockIdx.x * kJoinThreads + threadIdx.x) / L;
@@ -881,7 +884,9 @@ cudaError_t launch_dp(const AttnArgs& a, cudaStream_t s) {
   if (a.few_tokens) e = launch_attention_few(a, s);
   if (e != cudaSuccess) return e;
   const int64_t lanes = (int64_t)a.T * a.H * (DP / 4);
-  return launch_k(prefix_join_kernel<DP>, dim3((unsigned)ceil_div(lanes, kJoinThreads)), dim3(kJoinThreads), 0, s, a);
+  const bool one_wave = lanes <= (int64_t)sms * kJoinBlocks * kJoinThreads;
+  const auto join = one_wave ? prefix_join_kernel<DP, 16> : prefix_join_kernel<DP, 8>;
+  return launch_k(join, dim3((unsigned)ceil_div(lanes, kJoinThreads)), dim3(kJoinThreads), 0, s, a);
 }
 
 }  // namespace
