@@ -593,7 +593,7 @@ moe_status_t moe_paged_compact(const moe_attn_config_t* cfg, int32_t R, int32_t 
  * Entries -1 are passed over.  Negative lengths (count as 0), page ids outside the
  * cache, a page given back more often than it is held, and more pages than the list
  * gave out (the first ones are dropped): MOE_DEVERR_CACHE.  Blocks wait for one
- * another as in moe_paged_compact where R * max_pages is above 1024; after
+ * another as in moe_paged_compact where R * max_pages is above 4096; after
  * MOE_DEVERR_TIMEOUT the list and the table are as they were, the counts need not be.  */
 moe_status_t moe_paged_release(const moe_attn_config_t* cfg, int32_t R, const int32_t* held_len,
                                const int32_t* keep_len, int32_t* block_table, int32_t* page_shares,
