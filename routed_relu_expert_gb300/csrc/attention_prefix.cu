@@ -26,8 +26,8 @@
 //
 // Bound: a step of two row tiles takes about 3500 cycles where its products need 2048: the
 // chain of scores, exponentials and P of the tile whose turn it is.  128 requests of up to 4
-// nodes behind 8000 common tokens (32 heads over 8 of 128): 48 us for the prefix's 42 GFLOP, 870
-// TFLOP/s; with all keys through this kernel the call took 104 us, with attention_few.cu
+// nodes behind 8000 common tokens (32 heads over 8 of 128): 48 us for the prefix's 34 GFLOP, 700
+// TFLOP/s (in full row tiles 42 GFLOP, 870); with all keys through this kernel the call took 104 us, with attention_few.cu
 // beside it 89; every request through tree attention reads the prefix 128 times.
 #include "attn_tc.cuh"
 #include "attn_walk.cuh"

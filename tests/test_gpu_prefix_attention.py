@@ -81,6 +81,10 @@ CASES = [
     ([150, 140, 500, 7, 141], [8, 9, 7, 8, 1], 8, 2, 128, 16, True, False, [(0, 2, 140, 0), (2, 3, 20, 2), (3, 5, 7, 3)]),
     ([150, 140, 500, 150], [6, 7, 5, 12], 10, 2, 64, 16, False, True, [(0, 4, 140, 2)]),
     ([64, 50, 81, 64], [32, 33, 31, 1], 2, 2, 64, 16, True, False, [(0, 2, 48, 0), (2, 4, 64, 3)]),
+    # a few rows behind blocks of 256, of requests and of groups
+    ([150, 140, 500, 141, 7], [65, 64, 73, 2, 72], 8, 2, 64, 16, True, False, [(0, 2, 140, 0), (2, 4, 130, 3)]),
+    ([150, 140, 130, 141], [17, 18, 19, 34], 32, 2, 128, 16, False, True, [(0, 2, 140, 0), (2, 4, 128, 3)]),
+    ([64, 50, 81], [256, 32, 257], 3, 3, 40, 8, False, False, [(0, 2, 48, 0)]),
     ([30000, 29990, 200], [1, 2, 1], 8, 2, 128, 64, False, False, [(0, 2, 10000, 0)]),     # long rows, few of them
     ([700 + i for i in range(40)], [1 + i % 3 for i in range(40)], 8, 2, 64, 16, True, False,
      [(0, 13, 700, 0), (13, 26, 333, 20), (26, 40, 50, 39)]),
