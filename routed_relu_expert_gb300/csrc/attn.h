@@ -3,6 +3,7 @@
 #pragma once
 
 #include "internal.h"
+#include "meet.h"
 
 namespace moe {
 
@@ -13,8 +14,8 @@ constexpr int kAttnCounters = 960;
 struct AttnHeader {
   int32_t err;                       // device error bits (MOE_DEVERR_*)
   int32_t plan_ticket;               // blocks of the running plan that have read *free_head
-  int32_t met, left;                 // blocks of a cooperative launch that came to a meeting, that left
-  int32_t pad[60];
+  int32_t met[kMeetWords], left;     // blocks of a cooperative launch that came to meetings, that left
+  int32_t pad[61 - kMeetWords];
   int32_t counters[kAttnCounters];   // blocks of a split group that have stored their partial
 };
 static_assert(sizeof(AttnHeader) == MOE_ATTN_HEADER_BYTES, "attention workspace header");

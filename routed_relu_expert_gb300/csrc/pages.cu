@@ -14,54 +14,57 @@ constexpr int kThreads = 256;
 
 __device__ __forceinline__ int held(int64_t tokens, int shift) { return (int)((tokens + (1ll << shift) - 1) >> shift); }
 
-// Blocks of a cooperative launch that wait for one another.  The counters return to
+// Blocks of a cooperative launch that wait for one another (meet.h).  The counters return to
 // zero by themselves: the last block to leave resets them.  A wait ends after
 // tc::kWaitLimitNs at the latest, with MOE_DEVERR_TIMEOUT.
 struct GridMeet {
   AttnHeader* hdr;
-  int blocks, met = 0;
+  int blocks, arrived = 0, waited = 0;         // meetings that this block came to, that it waited for
   bool ok = true;
   __device__ GridMeet(AttnHeader* h, int n) : hdr(h), blocks(n) {}
-  // what this block has read until here (and, WRITTEN, written) is done for who waits for it.  Reads need no fence: they
-  // have returned their values.
+  // at the next meeting: what this block has read until here (and, WRITTEN, written) is done for who waits for it.
+  // Reads need no fence: they have returned their values.
   template <bool WRITTEN>
   __device__ void arrive() {
+    const int number = arrived++;
     __syncthreads();
     if (blocks > 1 && threadIdx.x == 0) {
       if (WRITTEN) __threadfence();
-      atomicAdd(&hdr->met, 1);
+      atomicAdd(&hdr->met[meet_word(number)], 1);
     }
   }
-  // until every block has arrived `times` times
-  __device__ bool wait(int times) {
+  // until every block has come to the next meeting that this one has not waited for
+  __device__ bool wait() {
+    const int number = waited++;
     if (blocks == 1) return true;
     __shared__ int good[2];                    // (in turn: a word is written again two waits later)
     if (threadIdx.x == 0) {
       const uint64_t t0 = globaltimer();
+      const int need = meet_count(number, blocks);
       int seen, tries = 0, fine = 1;
       while (true) {
-        asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(seen) : "l"(&hdr->met) : "memory");
-        if (seen >= times * blocks) break;
+        asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(seen) : "l"(&hdr->met[meet_word(number)]) : "memory");
+        if (seen >= need) break;
         if ((++tries & 255) == 0 && globaltimer() - t0 > tc::kWaitLimitNs) {
           fine = 0;
           set_error(&hdr->err, MOE_DEVERR_TIMEOUT);
           break;
         }
       }
-      good[times & 1] = fine;
+      good[number & 1] = fine;
     }
     __syncthreads();
-    ok = ok && good[times & 1];
+    ok = ok && good[number & 1];
     return ok;
   }
   __device__ bool operator()() {
     arrive<true>();
-    return wait(++met);
+    return wait();
   }
   __device__ void leave() {
     __syncthreads();
     if (blocks > 1 && threadIdx.x == 0 && atomicAdd(&hdr->left, 1) == blocks - 1) {
-      hdr->met = 0;
+      for (int i = 0; i < kMeetWords; ++i) hdr->met[i] = 0;
       hdr->left = 0;
     }
   }
@@ -289,14 +292,13 @@ __global__ void __launch_bounds__(kThreads) compact_moves_kernel(const CompactAr
 
 // The second moves the tokens in waves: all blocks read their part of a wave into shared
 // memory, meet, and write it; the next two waves' reads are on their way meanwhile, and a
-// block has met the others for the next wave before it writes this one.  Token i of the lists
+// block comes to the next wave's meeting before it waits for this one's.  Token i of the lists
 // goes to a place at or before its source, so what a wave writes lies behind every later
 // wave's sources and only its own wave and earlier ones read there.  A thread reads and
 // writes its own 16-byte pieces.  Bound: HBM, reads and writes in turn.  66667 of 100001
-// tokens of 4 KB (546 MB): 94 us, 5.8 TB/s or 86 % of a plain copy (a wave at a time 155,
-// the next one's reads beside the meeting 133, two waves' reads 110, without a fence for
-// writes that nobody waits for 94); a wave costs half a microsecond beside its bytes, so
-// that more and smaller ones are slower (four of 48 KB 101, four of 32 KB 111).
+// tokens of 4 KB (546 MB): 99 us, 5.5 TB/s or 82 % of a plain copy, and 104 us the call (with
+// one wave ahead of the writes 126, with one of 104 KB a block 114; more and smaller waves,
+// each of which costs half a microsecond beside its bytes: four of 48 KB 112, of 32 KB 125).
 constexpr int kWaveThreads = 512;
 constexpr int kWaves = 3;                      // in a block's shared memory
 constexpr int kWaveAhead = 9;                  // pieces of a thread a wave (72 KB a block)
@@ -340,14 +342,14 @@ __global__ void __launch_bounds__(kWaveThreads, 1) compact_wave_kernel(const Com
   }
   moves_of(kWaves - 1, true, from);
   asm volatile("cp.async.wait_group %0;" ::"n"(kWaves - 2) : "memory");
-  meet.arrive<false>();                        // wave 0 is read
+  meet.arrive<false>();                        // at the meeting of wave 0: it is read
   for (int w = 0; w < waves; ++w) {
     read(w + kWaves - 1);
     moves_of(w + kWaves, true, from);
     moves_of(w, false, to);
     asm volatile("cp.async.wait_group %0;" ::"n"(kWaves - 2) : "memory");
-    meet.arrive<false>();                      // wave w + 1 is
-    if (!meet.wait(w + 1)) break;
+    meet.arrive<false>();                      // of wave w + 1
+    if (!meet.wait()) break;                   // for wave w
 #pragma unroll
     for (int j = 0; j < kWaveAhead; ++j)
       if (to[j] >= 0) *reinterpret_cast<uint4*>(cache + to[j]) = *piece(w, j);

@@ -525,6 +525,43 @@ def test_compact_of_long_lists_and_wide_tokens(Hkv, dt):
     assert _err(s.ws) == 0
 
 
+def dense(kind, n):
+    """Lists whose places lie among the sources of the blocks beside them, wave after wave."""
+    return {"behind 1": np.arange(1, n), "behind 2": np.arange(2, n), "behind 17": np.arange(17, n),
+            "every second": np.arange(0, n, 2), "all but one in 50": np.flatnonzero(np.arange(n) % 50)}[kind]
+
+
+DENSE = ["behind 1", "behind 2", "behind 17", "every second", "all but one in 50"]
+
+
+@pytest.mark.parametrize("kind", DENSE)
+@pytest.mark.parametrize("tokens,Hkv,D,dt", [
+    (70, 8, 128, BF), (200, 8, 128, BF), (400, 8, 128, BF),                 # two blocks, seven, and one wave of them
+    (30000, 8, 128, BF), (60000, 2, 64, BF), (7000, 20, 128, FP),           # many waves, narrow and wide tokens
+])
+def test_no_block_writes_over_what_another_has_not_read(kind, tokens, Hkv, D, dt):
+    """Long lists beside copies on another stream, which hold some blocks up; again and again."""
+    M = _m()
+    s = Compact([5], [tokens], [dense(kind, tokens)], 16, dt=dt, Hkv=Hkv, D=D)
+    want = s.want()
+    d = lambda x: torch.from_numpy(np.asarray(x, np.int32)).cuda()
+    lists = d(s.first), d([0, len(s.keep[0])]), d(s.keep[0]), d(s.table)
+    k, v = s.k.clone(), s.v.clone()
+    src = torch.zeros(1 << 27, dtype=torch.uint8, device="cuda")
+    dst, side = torch.empty_like(src), torch.cuda.Stream()
+    for it in range(20):
+        k.copy_(s.k)
+        v.copy_(s.v)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            for i in range(it % 4):
+                dst[i << 10:].copy_(src[i << 10:])
+        M.moe_paged_compact(s.cfg, *lists, k, v, s.ws)
+        assert torch.equal(k, want[0]) and torch.equal(v, want[1]), it
+    torch.cuda.synchronize()
+    assert _err(s.ws) == 0
+
+
 # ---------------------------------------------------------------------------
 # offsets past 32 bits
 # ---------------------------------------------------------------------------
