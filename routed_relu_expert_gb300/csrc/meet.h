@@ -20,4 +20,14 @@ MOE_MEET int meet_word(int number) { return number % kMeetWords; }
 // what the word holds, at least, once all have arrived at this meeting
 MOE_MEET int meet_count(int number, int blocks) { return (number / kMeetWords + 1) * blocks; }
 
+// A block whose wait takes too long marks the word, by compare-and-swap of what it has read there while
+// that was too little: then nobody has passed this meeting, and nobody does.  Where no block comes
+// ahead, a meeting so ends in the same way for all of them.  (Ahead, a block that still waits for meeting
+// k may find the mark of meeting k + 2, and gives up before the others.)
+constexpr int kMeetGaveUp = 1 << 30;           // above every count
+enum MeetState { kMeetWait, kMeetMet, kMeetEnded };
+MOE_MEET int meet_state(int seen, int number, int blocks) {
+  return seen & kMeetGaveUp ? kMeetEnded : seen >= meet_count(number, blocks) ? kMeetMet : kMeetWait;
+}
+
 }  // namespace moe

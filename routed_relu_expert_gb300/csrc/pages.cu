@@ -16,11 +16,10 @@ __device__ __forceinline__ int held(int64_t tokens, int shift) { return (int)((t
 
 // Blocks of a cooperative launch that wait for one another (meet.h).  The counters return to
 // zero by themselves: the last block to leave resets them.  A wait ends after
-// tc::kWaitLimitNs at the latest, with MOE_DEVERR_TIMEOUT.
+// tc::kWaitLimitNs, with MOE_DEVERR_TIMEOUT, for all blocks of the meeting.
 struct GridMeet {
   AttnHeader* hdr;
   int blocks, arrived = 0, waited = 0;         // meetings that this block came to, that it waited for
-  bool ok = true;
   __device__ GridMeet(AttnHeader* h, int n) : hdr(h), blocks(n) {}
   // at the next meeting: what this block has read until here (and, WRITTEN, written) is done for who waits for it.
   // Reads need no fence: they have returned their values.
@@ -40,22 +39,20 @@ struct GridMeet {
     __shared__ int good[2];                    // (in turn: a word is written again two waits later)
     if (threadIdx.x == 0) {
       const uint64_t t0 = globaltimer();
-      const int need = meet_count(number, blocks);
-      int seen, tries = 0, fine = 1;
+      int32_t* word = &hdr->met[meet_word(number)];
+      int seen, tries = 0, state;
       while (true) {
-        asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(seen) : "l"(&hdr->met[meet_word(number)]) : "memory");
-        if (seen >= need) break;
-        if ((++tries & 255) == 0 && globaltimer() - t0 > tc::kWaitLimitNs) {
-          fine = 0;
+        asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(seen) : "l"(word) : "memory");
+        state = meet_state(seen, number, blocks);
+        if (state != kMeetWait) break;
+        // (a swap that fails: a block has come meanwhile, or another has given up)
+        if ((++tries & 255) == 0 && globaltimer() - t0 > tc::kWaitLimitNs && atomicCAS(word, seen, seen | kMeetGaveUp) == seen)
           set_error(&hdr->err, MOE_DEVERR_TIMEOUT);
-          break;
-        }
       }
-      good[number & 1] = fine;
+      good[number & 1] = state == kMeetMet;
     }
     __syncthreads();
-    ok = ok && good[number & 1];
-    return ok;
+    return good[number & 1];
   }
   __device__ bool operator()() {
     arrive<true>();
@@ -488,7 +485,7 @@ __global__ void __launch_bounds__(kRelThreads, 1) release_kernel(const ReleaseAr
       for (int j = 0; j < kAhead; ++j)
         if (p[j] >= 0) a.last[p[j]] = -1;
     });
-    meet();
+    if (!meet()) return meet.leave();          // (every block does: list and table stay as they are)
     walk([&](int (&at)[kAhead], int (&p)[kAhead]) {
 #pragma unroll
       for (int j = 0; j < kAhead; ++j)
@@ -497,7 +494,7 @@ __global__ void __launch_bounds__(kRelThreads, 1) release_kernel(const ReleaseAr
           atomicSub(&a.shares[p[j]], 1);
         }
     });
-    meet();
+    if (!meet()) return meet.leave();
   }
   // freed: no holder is left, and this is the last of the entries that gave it back
   auto freed = [&](int (&at)[kAhead], int (&p)[kAhead], bool (&is)[kAhead], int (&left)[kAhead]) {
@@ -524,7 +521,7 @@ __global__ void __launch_bounds__(kRelThreads, 1) release_kernel(const ReleaseAr
   int all = own;
   if (ctas > 1) {
     if (tid == 0) a.counts[rank] = own;
-    meet();
+    if (!meet()) return meet.leave();
     int before = 0, sum = 0;
     for (int c = tid; c < ctas; c += kRelThreads) {
       const int n = __ldcg(&a.counts[c]);
@@ -535,10 +532,6 @@ __global__ void __launch_bounds__(kRelThreads, 1) release_kernel(const ReleaseAr
     block_scan(before, tmp, &ignored);
     place += ignored;
     block_scan(sum, tmp, &all);
-  }
-  if (!meet.ok) {                              // (a wait that gave up: the free list stays as it is)
-    meet.leave();
-    return;
   }
   if (all > head || head > a.n_free) bad |= MOE_DEVERR_CACHE;    // more than the list gave out
   place += head - all;

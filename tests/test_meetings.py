@@ -20,7 +20,9 @@ def rules(tmp_path_factory):
     src, lib = str(d / "meet.cpp"), str(d / "meet.so")
     with open(src, "w") as f:
         f.write('#include "meet.h"\nextern "C" {\nint word(int n) { return moe::meet_word(n); }\n'
-                "int count(int n, int b) { return moe::meet_count(n, b); }\nint words() { return moe::kMeetWords; }\n}\n")
+                "int count(int n, int b) { return moe::meet_count(n, b); }\nint words() { return moe::kMeetWords; }\n"
+                "int state(int seen, int n, int b) { return moe::meet_state(seen, n, b); }\n"
+                "int gave_up() { return moe::kMeetGaveUp; }\n}\n")
     subprocess.run([cxx, "-std=c++17", "-shared", "-fPIC", "-I", CSRC, src, "-o", lib], check=True)
     return ctypes.CDLL(lib)
 
@@ -87,3 +89,68 @@ def test_one_word_for_all_meetings_would_be_found():
     assert sum(early(OneWord, 2, 1, True, seed) for seed in range(40)) > 0
     assert sum(early(OneWord, 20, 5, True, seed) for seed in range(5)) > 0
     assert sum(early(OneWord, 20, 5, False, seed) for seed in range(5)) == 0     # (nobody ahead: one word is enough)
+
+
+WAIT, MET, ENDED = range(3)
+
+
+def outcomes(rules, blocks, meetings, seed, swap=True):
+    """Of each block: what its waits came to, over one random order of steps in which waits may give up.  A block
+    ends with its first wait that fails.  swap: a word is marked by compare-and-swap; else each block goes by
+    the time alone."""
+    rng = random.Random(seed)
+    mark = rules.gave_up()
+    met, got = [0] * rules.words(), [[] for _ in range(blocks)]
+    came, seen = [False] * blocks, [None] * blocks           # at the meeting len(got[b]); what was read of its word
+    left = set(range(blocks))
+    for _ in range(400 * blocks * meetings):
+        if not left:
+            break
+        b = rng.choice(sorted(left))
+        n = len(got[b])
+        w, state = rules.word(n), None
+        if not came[b]:
+            if rng.random() < 0.3:
+                met[w] += 1
+                came[b] = True
+        elif seen[b] is None:                                # a look at the word
+            state = rules.state(met[w], n, blocks)
+            seen[b] = met[w] if state == WAIT else None
+        elif rng.random() < 0.05:                            # it has taken too long
+            if not swap:
+                state = ENDED
+            elif met[w] == seen[b]:
+                met[w] |= mark
+            seen[b] = None
+        else:
+            seen[b] = None
+        if state in (MET, ENDED):
+            got[b].append(state)
+            came[b] = False
+            if state == ENDED or len(got[b]) == meetings:
+                left.discard(b)
+    assert not left, "a block waits for ever"
+    return got
+
+
+@pytest.mark.parametrize("blocks", [2, 3, 20, 152])
+def test_a_meeting_ends_in_one_way_for_all(rules, blocks):
+    """A release either changes the table and the list in all of its blocks or in none."""
+    ends = set()
+    for seed in range(300 if blocks < 20 else 20 if blocks < 152 else 2):
+        got = outcomes(rules, blocks, 3, seed)
+        assert all(g == got[0] for g in got), seed
+        ends.add(tuple(got[0]))
+    assert len(ends) > 1 or blocks > 3                       # (some of them met three times, some gave up)
+
+
+def test_waits_that_give_up_by_themselves_would_be_found(rules):
+    assert any(any(g != got[0] for g in got) for got in (outcomes(rules, 3, 3, seed, swap=False) for seed in range(100)))
+
+
+def test_the_mark_is_above_every_count(rules):
+    for number, blocks in ((0, 1), (0, 152), (200_000, 152)):
+        n = rules.count(number, blocks)
+        assert 0 < n < rules.gave_up()
+        assert [rules.state(x, number, blocks) for x in (n - 1, n, n + 1, (n - 1) | rules.gave_up(), n | rules.gave_up())] == [
+            WAIT, MET, MET, ENDED, ENDED]
