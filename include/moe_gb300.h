@@ -615,8 +615,8 @@ moe_status_t moe_paged_release(const moe_attn_config_t* cfg, int32_t R, const in
  * context's start as there, prefix included.  A request whose context (kv_len
  * without its nodes) is shorter than the prefix's whole pages, and a group of fewer
  * than two requests, are attended through their own rows alone.  Bad groups (bounds
- * or rows out of range, not ascending, a prefix past the table's row):
- * MOE_DEVERR_CACHE, and they share nothing.  (2 T + R + n_groups) * Hkv *
+ * or rows out of range, a prefix past the table's row): MOE_DEVERR_CACHE, and they
+ * share nothing; where group_start does not ascend, no group of the call does.  (2 T + R + n_groups) * Hkv *
  * (ceil(max_pages * page_size / 128) + 5) and 32 * T * H must stay below 2^31.
  * FP32 reads the prefix through prefix_row for each row by itself.                  */
 size_t moe_prefix_workspace_bytes(const moe_attn_config_t* cfg, int32_t T);

@@ -69,7 +69,14 @@ __global__ void __launch_bounds__(kThreads) attention_f32_kernel(const AttnArgs 
     }
     s_q[h][d] = v;
   }
-  __syncthreads();
+  // groups whose bounds do not ascend share nothing
+  bool mixed = false;
+  if (SHARED) {
+    for (int g = tid; g < a.n_groups; g += kThreads) mixed |= a.group_start[g + 1] < a.group_start[g];
+    mixed = __syncthreads_or(mixed);
+  } else {
+    __syncthreads();
+  }
 
   float m[kHeads], l[kHeads];
   float4 o[kHeads];
@@ -98,7 +105,7 @@ __global__ void __launch_bounds__(kThreads) attention_f32_kernel(const AttnArgs 
     const int32_t* table0 = table;             // of the first `shared` pages
     int shared = 0;
     if (SHARED) {
-      const int g = group_of(a.group_start, a.n_groups, r);
+      const int g = mixed ? -1 : group_of(a.group_start, a.n_groups, r);
       if (g >= 0) {
         const PrefixGroup p = prefix_group(a.group_start, a.prefix_row, a.prefix_len, g, a.R, a.max_pages, a.page_shift,
                                            nullptr);

@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) attention_few_kernel(const 
   using X = Geo<DP>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t s_scan[kWarps];
-  __shared__ int s_most;
+  __shared__ int s_most, s_mixed;
   const int walk_n = a.n_groups + a.R;
   int* prefix = reinterpret_cast<int*>(smem + X::SMEM);      // [walk_n + 1] cost before each step of the walk
   int* skip = prefix + walk_n + 1;                           // [R] pages of the request's group's prefix
@@ -116,8 +116,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) attention_few_kernel(const 
 
   // the walk, as the other kernel has it: cost before each step, runs of the total
   auto at_walk = [&](int v, int* bad) {
-    Req q = v < a.n_groups ? group_request(a, prefix_group(a.group_start, a.prefix_row, a.prefix_len, v, a.R, a.max_pages,
-                                                           a.page_shift, bad), tb)
+    Req q = v < a.n_groups ? group_request(a, v, s_mixed, tb, bad)
                            : own_request(a, v - a.n_groups, skip[v - a.n_groups], tb, bad);
     q.tiles = max((q.kv + grain - 1) / grain, 1);
     if (!few(a, q)) q.blocks = 0;
@@ -128,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) attention_few_kernel(const 
   {
     int bad = 0;
     if (tid == 0) s_most = 0;
-    prefix_pages<kThreads>(a, reinterpret_cast<int32_t*>(smem), skip);
+    prefix_pages<kThreads>(a, reinterpret_cast<int32_t*>(smem), skip, &s_mixed);
     const int per = (walk_n + kThreads - 1) / kThreads, v0 = min(tid * per, walk_n), v1 = min(v0 + per, walk_n);
     auto cost = [&](const Req& q) { return (q.tiles + kUnitCost) * q.blocks * a.Hkv; };
     Req q;

@@ -85,6 +85,7 @@ struct Small {
   Piece piece[kQueue];
   Req first;                                   // step of the walk that the run begins in
   int first_v;
+  int mixed;                                   // the groups' bounds do not ascend
   uint32_t tmem;
   int abort;
   int64_t scan[kThreads / 32];
@@ -149,8 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto at_walk = [&](int v, int* bad) {
     Req q;
     if (v < groups_n)
-      q = group_request(
-          a, prefix_group(a.group_start, a.prefix_row, a.prefix_len, v, a.R, a.max_pages, a.page_shift, bad), tb);
+      q = group_request(a, v, sm.mixed, tb, bad);
     else
       q = own_request(a, v - groups_n, skip[v - groups_n], tb, bad);
     if (few(a, q)) q.blocks = 0;
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Req q;
     const bool ahead = v0 < v1 && v0 >= groups_n;
     if (ahead) q = own_request(a, v0 - groups_n, 0, tb, &bad);
-    prefix_pages<kThreads>(a, reinterpret_cast<int32_t*>(ring_ptr), skip);
+    prefix_pages<kThreads>(a, reinterpret_cast<int32_t*>(ring_ptr), skip, &sm.mixed);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");       // (before TMA writes there)
     auto cost = [&](const Req& q) { return (q.tiles + kPieceCost) * q.blocks * a.Hkv; };
     int64_t local = 0;                                     // (one step's cost fits 31 bits; row starts that are no

@@ -37,7 +37,11 @@ __device__ __forceinline__ Req request(const AttnArgs& a, int r, int tb, int* ba
 // counts as a request whose nodes are all of its requests' rows and whose tokens
 // are the prefix, all of them before the nodes; a request of it keeps the tokens
 // behind the prefix.
-__device__ __forceinline__ Req group_request(const AttnArgs& a, const PrefixGroup& g, int tb) {
+// Groups whose bounds do not ascend (`mixed`: in one place at least, so that some of them may overlap, and a row
+// would have the partials of two) share nothing.
+__device__ __forceinline__ Req group_request(const AttnArgs& a, int group, bool mixed, int tb, int* bad) {
+  PrefixGroup g = prefix_group(a.group_start, a.prefix_row, a.prefix_len, group, a.R, a.max_pages, a.page_shift, bad);
+  if (mixed) g.pages = 0;
   Req q;
   q.q0 = min(max(a.q_start[g.begin], 0), a.T);
   const int q1 = min(max(a.q_start[g.end], q.q0), a.T);
@@ -73,21 +77,28 @@ __device__ __forceinline__ bool few(const AttnArgs& a, const Req& q) {
   return q.n <= a.few_tokens;
 }
 
-// pages of each request's group's prefix, into shared memory; `start`: 3 n_groups + 1 words of it for the meanwhile
+// pages of each request's group's prefix, into shared memory; `start`: 3 n_groups + 1 words of it for the meanwhile;
+// *mixed (in shared memory, too): whether the groups' bounds do not ascend
 template <int kThreads>
-__device__ __forceinline__ void prefix_pages(const AttnArgs& a, int32_t* start, int* skip) {
+__device__ __forceinline__ void prefix_pages(const AttnArgs& a, int32_t* start, int* skip, int* mixed) {
   int32_t *rows = start + a.n_groups + 1, *lens = rows + a.n_groups;
+  bool descends = false;
   if (a.n_groups)
     for (int g = threadIdx.x; g <= a.n_groups; g += kThreads) {
-      start[g] = a.group_start[g];
-      if (g < a.n_groups) {
-        rows[g] = a.prefix_row[g];
-        lens[g] = a.prefix_len[g];
+      const bool group = g < a.n_groups;
+      const int at = a.group_start[g], next = group ? a.group_start[g + 1] : at;
+      const int row = group ? a.prefix_row[g] : 0, len = group ? a.prefix_len[g] : 0;
+      start[g] = at;                           // (all loads come before the stores)
+      if (group) {
+        rows[g] = row;
+        lens[g] = len;
       }
+      descends |= next < at;
     }
-  __syncthreads();
+  descends = __syncthreads_or(descends);
+  if (threadIdx.x == 0) *mixed = descends;
   for (int r = threadIdx.x; r < a.R; r += kThreads) {
-    const int g = group_of(start, a.n_groups, r);
+    const int g = descends ? -1 : group_of(start, a.n_groups, r);
     int pages = 0;
     if (g >= 0) {
       const PrefixGroup p = prefix_group(start, rows, lens, g, a.R, a.max_pages, a.page_shift, nullptr);

@@ -205,6 +205,27 @@ def test_bad_groups_are_flagged_and_share_nothing(dt):
 
 
 @pytest.mark.parametrize("dt", [BF, FP])
+@pytest.mark.parametrize("start", [[0, 5, 3, 8], [0, 3, 2, 8], [4, 4, 0, 6], [0, 8, 7, 8], [2, 6, 4, 1]])
+def test_groups_that_overlap_share_nothing(dt, start):
+    """Each of the outer groups is in order by itself."""
+    M = _m()
+    ctx, new = [80 + 3 * r for r in range(8)], [2, 1, 3, 9, 40, 1, 2, 5]
+    plain = Step(ctx, new, 8, 2, 64, 16, dt, seed=8)
+    want, want_lse = plain.run()
+    s = Shared(ctx, new, 8, 2, 64, 16, dt, [(0, 3, 64, 0), (3, 5, 48, 3), (5, 8, 80, 7)], seed=8)
+    s.k, s.v = plain.k, plain.v
+    s.widen(plain.table)                                     # every request has pages of its own
+    s.start = _i32(start)
+    out, lse = s.run()
+    assert _err(s.ws) == M.MOE_DEVERR_CACHE
+    tol = 2 ** -7 if dt is BF else 2 ** -18                  # |v| < 6, two evaluations of the same sums
+    assert float((out.float() - want.float()).abs().max()) <= 6 * tol
+    assert float((lse - want_lse).abs().max()) <= 2 ** -14
+    again, lse2 = s.run()
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
 def test_bad_pages_of_the_prefix_are_flagged(dt):
     M = _m()
     s = Shared([80, 70, 33], [2, 3, 1], 8, 2, 64, 16, dt, [(0, 2, 64, 0)], seed=9)
