@@ -5,6 +5,11 @@
 
 namespace moe {
 
+// For a kernel whose successor hardly depends on it (no other kernel lets its successor start early): its blocks call
+// this after their own pdl_wait, so that the successor, which then need not wait to read what came before both, may
+// start where they end; it still waits before it ends.
+__device__ __forceinline__ void pdl_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // flags of a Req: a group's prefix; own tokens of rows that have a prefix beside them
 constexpr int kPrefix = 8, kJoined = 16;
 

@@ -98,10 +98,6 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32
 // an early release gained at most 1 us on the single-chain steps.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-// The exception: a kernel whose successor hardly depends on it.  Its blocks call this
-// after their own pdl_wait, so that the successor, which then need not wait to read what
-// came before both, may start where they end; it still waits before it ends.
-__device__ __forceinline__ void pdl_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ---------------------------------------------------------------------------
 // shared-memory addresses, the global nanosecond timer (bounded waits) and

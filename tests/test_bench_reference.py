@@ -100,3 +100,10 @@ def test_committed_traffic_rows_parse():
             assert int(cells[2].replace(",", "")) > 0
             rows += 1
     assert rows >= 1
+
+
+def test_committed_traffic_is_of_the_committed_sources():
+    """The workload that the bench runs by default has its DRAM traffic: both products' kernels are the captured ones."""
+    for kernel in ("gemv_bf16_kernel<0, 0, 16>", "gemv_bf16_kernel<1, 1, 32>"):
+        traffic, captured = bench.recorded_traffic(kernel, "nano_decode T=64", "gemv")
+        assert traffic is not None, f"{kernel}: captured from sources {captured}, now {bench.sources_sha16('gemv')}"
