@@ -594,7 +594,10 @@ moe_status_t moe_paged_compact(const moe_attn_config_t* cfg, int32_t R, int32_t 
  * cache, a page given back more often than it is held, and more pages than the list
  * gave out (the first ones are dropped): MOE_DEVERR_CACHE.  Blocks wait for one
  * another as in moe_paged_compact where R * max_pages is above 4096; after
- * MOE_DEVERR_TIMEOUT the list and the table are as they were, the counts need not be.  */
+ * MOE_DEVERR_TIMEOUT the list and the table are as they were, the counts need not be.
+ * It may overlap with moe_rope_append, moe_tree_attention and moe_prefix_attention of
+ * the same workspace and configuration that do not look at what it gives back
+ * (requests that ended before their step, on another stream).                        */
 moe_status_t moe_paged_release(const moe_attn_config_t* cfg, int32_t R, const int32_t* held_len,
                                const int32_t* keep_len, int32_t* block_table, int32_t* page_shares,
                                int32_t* free_pages, int32_t n_free, int32_t* free_head, void* ws, size_t ws_bytes,

@@ -397,7 +397,9 @@ class PagedKVCache:
     error word that moe_get_device_error reads).  A step is plan -> append -> attend, all on the
     current stream, nothing on the host.  A call that is given another
     stream makes its tensors from that stream's memory; they are used on a third one
-    as any tensor is (after an event, with ``record_stream``).
+    as any tensor is (after an event, with ``record_stream``).  All calls share ``ws``:
+    those on different streams are ordered by the caller, but ``release`` may run beside
+    the ``append`` and ``attend`` of requests that keep what they have.
 
     ``prefix_rows``: rows of the largest step that ``attend`` gets groups for (it sizes the
     workspace).  ``sections``: pairs a rotary axis, for positions with several

@@ -29,6 +29,8 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kHeads = 4;                      // query heads a block
+constexpr int kMaxParts = 640;                 // splits of all units together
+static_assert((size_t)kMaxParts * kHeads <= kAttnPartSlots * kAttnRows, "partials in the workspace");
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
@@ -283,8 +285,8 @@ __global__ void __launch_bounds__(kThreads) attention_f32_kernel(const AttnArgs 
 }  // namespace
 
 // Splits: of at least 128 keys each if the tables' rows are full (a tile for each
-// of the four warps), at most 32, while the grid is under two blocks an SM and the
-// workspace holds their counters and partials.
+// of the four warps), at most 32, while the grid is about four blocks an SM at most and
+// the workspace holds their counters.
 template <bool SHARED>
 static cudaError_t launch_f32(const AttnArgs& a, cudaStream_t s) {
   if (a.T <= 0) return cudaSuccess;
@@ -292,9 +294,8 @@ static cudaError_t launch_f32(const AttnArgs& a, cudaStream_t s) {
   const int64_t units = (int64_t)a.T * a.Hkv * groups;
   int64_t splits = 1;
   if (units <= kAttnCounters / 4) {
-    const int64_t room = (int64_t)kAttnPartSlots * kAttnRows / kHeads / units;
     const int64_t keys = (int64_t)a.max_pages << a.page_shift;
-    splits = std::max<int64_t>(1, std::min<int64_t>({32, 4 * kAttnMaxCtas / units, room, ceil_div(keys, 128)}));
+    splits = std::max<int64_t>(1, std::min<int64_t>({32, kMaxParts / units, ceil_div(keys, 128)}));
   }
   launch_k(attention_f32_kernel<SHARED>, dim3((unsigned)(units * splits)), kThreads, 0, s, a, groups, (int)splits);
   return cudaGetLastError();

@@ -22,7 +22,7 @@ static_assert(sizeof(AttnHeader) == MOE_ATTN_HEADER_BYTES, "attention workspace 
 
 // Split partials: kAttnMaxCtas blocks own two slots of 128 rows each: the rows'
 // FP32 output sums ([four columns][row]) and, after all of them, (max, sum).
-constexpr int kAttnMaxCtas = 160;
+constexpr int kAttnMaxCtas = 152;          // a GB300's SMs
 constexpr int kAttnRows = 128;
 constexpr int kAttnTile = 128;             // keys a tile
 constexpr int kAttnPartDim = 128;

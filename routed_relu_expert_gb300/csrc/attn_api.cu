@@ -63,12 +63,18 @@ inline bool meet(const int32_t* a, int64_t n, const int32_t* b, int64_t m) {
   return a && b && (uintptr_t)a < (uintptr_t)b + 4 * m && (uintptr_t)b < (uintptr_t)a + 4 * n;
 }
 
-constexpr size_t kWorkspaceBytes = MOE_ATTN_HEADER_BYTES + kAttnPartBytes + kAttnJoinBytes;
+// Behind attention's partials (kPartsEnd) moe_paged_release has a word a block and, where pages are shared, a word a
+// page, so that it may run beside attention: kReleasePages of them in the workspace that every call asks for, more
+// where a configuration has more pages.
+constexpr size_t kPartsEnd = MOE_ATTN_HEADER_BYTES + kAttnPartBytes + kAttnJoinBytes;
+constexpr size_t kReleasePages = 1 << 18;
+constexpr size_t release_end(size_t pages) { return (kPartsEnd + (kAttnMaxCtas + pages) * 4 + 15) / 16 * 16; }
+constexpr size_t kWorkspaceBytes = release_end(kReleasePages);
+static_assert(kPartsEnd % 16 == 0, "16-byte pieces");
 
-// of a configuration: moe_paged_release has a word a page where attention has its partials
+// of a configuration
 size_t workspace_bytes(const moe_attn_config_t* c) {
-  const size_t pages = (MOE_ATTN_HEADER_BYTES + (kAttnMaxCtas + (size_t)c->n_pages) * 4 + 15) / 16 * 16;
-  return pages > kWorkspaceBytes ? pages : kWorkspaceBytes;
+  return (size_t)c->n_pages > kReleasePages ? release_end(c->n_pages) : kWorkspaceBytes;
 }
 
 moe_status_t check_ws(const void* ws, size_t ws_bytes) {
@@ -523,7 +529,7 @@ moe_status_t moe_paged_compact(const moe_attn_config_t* cfg, int32_t R, int32_t 
   const int es = elem_bytes(cfg);
   CompactArgs a{};
   a.scratch = reinterpret_cast<uint8_t*>(ws) + MOE_ATTN_HEADER_BYTES;
-  a.scratch_bytes = kWorkspaceBytes - MOE_ATTN_HEADER_BYTES;
+  a.scratch_bytes = kPartsEnd - MOE_ATTN_HEADER_BYTES;
   a.first = first;
   a.keep_start = keep_start;
   a.keep = keep;
@@ -568,7 +574,7 @@ moe_status_t moe_paged_release(const moe_attn_config_t* cfg, int32_t R, const in
   a.free_pages = free_pages;
   a.free_head = free_head;
   a.hdr = reinterpret_cast<AttnHeader*>(ws);
-  a.counts = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(ws) + MOE_ATTN_HEADER_BYTES);
+  a.counts = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(ws) + kPartsEnd);
   a.last = a.counts + kAttnMaxCtas;
   a.R = R;
   a.n_free = n_free;

@@ -301,6 +301,44 @@ def test_a_larger_workspace_serves_every_call():
     assert torch.equal(s.run()[0], a)
 
 
+@pytest.mark.parametrize("dt", [BF, FP])
+@pytest.mark.parametrize("groups", [[], [(0, 5, 2000, 0), (5, 12, 700, 6)]])
+def test_release_beside_attention_of_the_same_workspace(dt, groups):
+    """Pages of requests that have ended go back on another stream while a step runs."""
+    from test_gpu_shared_pages import Release, release_reference
+    M = _m()
+    ctx = [2100, 2000, 2500, 2001, 4000] + [700 + 9 * i for i in range(7)]
+    s = Shared(ctx, [1 + i % 4 for i in range(12)], 8, 2, 128, 16, dt, groups, own_rows=True, seed=14)
+    s.table = s.table_d.cpu().numpy()
+    r = Release([8000, 4001], [(7 * i) % 1000 for i in range(300)], 16, group=16)
+    assert s.ws.numel() >= M.attn_workspace_bytes(r.cfg)
+    d = lambda x: torch.from_numpy(np.asarray(x, np.int32).copy()).cuda()
+    begin = [d(r.table), d(r.shares), d(r.free), _i32([r.head])]
+    state, now, keep = [x.clone() for x in begin], d(r.now), d(r.now * 0)
+    want = release_reference(r.table, r.shares, r.free, r.head, r.now, r.now * 0, 16)
+    out = torch.empty((s.T, s.H, s.D), dtype=dt, device="cuda")
+
+    def attend():
+        if groups:
+            return s.run(out)[0]
+        M.moe_tree_attention(s.cfg, s.q, s.q_start, s.kv_len, s.table_d, s.k, s.v, out, s.ws, tree_mask=s.mask)
+        return out
+
+    good = attend().clone()
+    side = torch.cuda.Stream()
+    for _ in range(10):
+        for x, y in zip(state, begin):
+            x.copy_(y)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            M.moe_paged_release(r.cfg, now, keep, state[0], state[2], state[3], s.ws, page_shares=state[1])
+        for _ in range(4):
+            assert torch.equal(attend(), good)
+        torch.cuda.current_stream().wait_stream(side)
+        assert all(np.array_equal(x.cpu().numpy().reshape(-1), np.asarray(y).reshape(-1)) for x, y in zip(state, want))
+    assert _err(s.ws) == 0
+
+
 # ---------------------------------------------------------------------------
 # together
 # ---------------------------------------------------------------------------

@@ -168,6 +168,17 @@ def test_axes_table_refusals(lib):  # noqa: F811
         assert call(**kw) == N.MOE_ERR_INVALID_ARG, kw
 
 
+def test_release_has_words_of_its_own_behind_attentions_partials(lib):  # noqa: F811
+    """A word a page, whatever else lies in the workspace: past the pages that the common size has room for it
+    grows with every page."""
+    size = lambda n, **kw: lib.moe_attn_workspace_bytes(ctypes.byref(_cfg(n_pages=n, **kw)))
+    common = size(8)
+    assert size(1) == common and size(1 << 18) == common
+    for n in ((1 << 18) + 64, 1 << 19, 1 << 20, 20_000_000):
+        assert size(n) - common == 4 * (n - (1 << 18))
+        assert lib.moe_prefix_workspace_bytes(ctypes.byref(_cfg(n_pages=n)), 3) > size(n)
+
+
 # ---------------------------------------------------------------------------
 # the binding
 # ---------------------------------------------------------------------------
