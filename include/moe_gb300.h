@@ -552,7 +552,12 @@ moe_status_t moe_tree_attention(const moe_attn_config_t* cfg, int32_t R, int32_t
  * still takes its page if its rows and length are in range.  Page ids outside the cache
  * become -1 entries (MOE_DEVERR_CACHE); out of free pages: entry -1, MOE_DEVERR_PAGES.
  * 2 * n_kv_heads * head_dim * page_size elements in pieces of 16 bytes must be below
- * 2^31 (MOE_ERR_UNSUPPORTED).                                                     */
+ * 2^31 (MOE_ERR_UNSUPPORTED).
+ * Layers that share a table, its counts and its list: one call as above, with another
+ * free_head_out than free_head; then, for each other layer, the same call with its
+ * caches, src_table the table, and a dst_table, page_shares and free_head_out that
+ * nobody reads (memory of their own): it takes the same pages, and copies its tokens
+ * there.  (A fork of a row onto itself would take a page in these calls.)            */
 moe_status_t moe_paged_fork(const moe_attn_config_t* cfg, int32_t n, const int32_t* src_rows, const int32_t* dst_rows,
                             const int32_t* lengths, int32_t R, const int32_t* src_table, int32_t* dst_table,
                             int32_t* page_shares, const int32_t* free_pages, int32_t n_free, const int32_t* free_head,

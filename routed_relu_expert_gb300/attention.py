@@ -315,7 +315,9 @@ def moe_paged_fork(cfg, src_rows, dst_rows, lengths, block_table, page_shares, f
     """Row dst_rows[i] of dst_table (default: block_table, the sources') goes on from the
     first lengths[i] tokens of row src_rows[i]: whole pages shared, the last one's tokens
     copied.  Written: dst_table, page_shares, the caches, free_head_out (default:
-    free_head, in place)."""
+    free_head, in place).  One layer's K and V: of layers that share a table the others follow
+    with the same free_head, their caches, and a dst_table, page_shares and free_head_out that
+    nobody reads."""
     dev, n, R, i32 = _device(ws, "ws"), src_rows.shape[0], block_table.shape[0], torch.int32
     _, Hkv, D, page, pages, max_pages, _, _, _, dtype, sp, st, sh = _FIELDS.unpack_from(cfg)
     dt = _TORCH.get(dtype)

@@ -120,6 +120,25 @@ def test_beams_change_places_from_one_table_to_another():
     assert _err(s.ws) == 0
 
 
+@pytest.mark.parametrize("short", [0, 2])
+def test_layers_that_share_a_table_fork_one_after_another(short):
+    """The first call changes the table, counts and list; the others copy their layers' tokens to the same pages."""
+    M = _m()
+    s = Fork([300, 77, 40], [(1, 3, 77), (0, 4, 250), (0, 5, 256), (2, 6, 0), (1, 7, 1), (2, 8, 33)], 16, short=short)
+    d = lambda x: torch.from_numpy(x.copy()).cuda()
+    table, shares, free, head, after = d(s.table), d(s.shares), d(s.free), _i32([s.head]), _i32([-5])
+    lists = [_i32(list(c)) for c in zip(*s.forks)]
+    for layer in range(3):
+        s.k, s.v = _cache(s.k.shape, BF, False, 20 + layer)
+        k, v = s.k.clone(), s.v.clone()
+        first = layer == 0
+        M.moe_paged_fork(s.cfg, *lists, table, shares if first else torch.zeros_like(shares), free, head, k, v, s.ws,
+                         free_head_out=after if first else torch.zeros_like(after),
+                         dst_table=None if first else torch.zeros_like(table))
+        s.check(dict(table=_np(table), to=None, shares=_np(shares), head=int(after[0]), k=k, v=v))
+    assert _err(s.ws) == (M.MOE_DEVERR_PAGES if short else 0)
+
+
 @pytest.mark.parametrize("short", [1, 4])
 def test_fork_out_of_pages(short):
     M = _m()
