@@ -403,8 +403,10 @@ class PagedKVCache:
     those on different streams are ordered by the caller, but ``release`` may run beside
     the ``append`` and ``attend`` of requests that keep what they have.
 
-    ``prefix_rows``: rows of the largest step that ``attend`` gets groups for (it sizes the
-    workspace).  ``sections``: pairs a rotary axis, for positions with several
+    ``prefix_rows``: rows of the largest step that ``attend`` gets groups for, of 2048 requests at
+    most (it sizes the workspace: some 95 MB and the rows' own for BF16 heads of 128, 21 MB
+    without it).  Caches of one configuration whose calls are ordered may have one workspace: set
+    ``ws`` of the others to the first one's.  ``sections``: pairs a rotary axis, for positions with several
     (``interleaved_axes``, ``own_ladders``: as in rope_axes_table)."""
 
     def __init__(self, cfg: N.MoeAttnConfig, max_requests: int, device="cuda", theta: float = 10000.0, *,

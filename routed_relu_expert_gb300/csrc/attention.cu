@@ -47,7 +47,7 @@ __device__ __forceinline__ int request_of(const int32_t* q_start, int R, int t) 
 
 // SHARED: the tokens of a group's prefix are read through the group's row of the table (every row of the group by
 // itself: the pages come from memory once and from L2 after that).  4 requests of up to 3 nodes behind 600 common
-// tokens, 8 heads over 2 of 64: 13.3 us, the latency of one pass over 128 keys a block and of the join of its splits.
+// tokens, 8 heads over 2 of 64: 12.5 us, the latency of one pass over 128 keys a block and of the join of its splits.
 template <bool SHARED>
 __global__ void __launch_bounds__(kThreads) attention_f32_kernel(const AttnArgs a, int groups, int splits) {
   pdl_wait();

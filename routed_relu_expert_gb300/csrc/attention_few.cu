@@ -18,7 +18,7 @@
 // The other kernel lets this one's blocks start as its own ones end (they need nothing of it).
 //
 // Bound: HBM, where there are enough keys; else the latency of a run (lengths, table, keys,
-// softmax, the join).  128 requests' 131 MB of own tokens: 37 us beside the other kernel's end,
+// softmax, the join).  128 requests' 131 MB of own tokens: 38 us beside the other kernel's end,
 // about 20 of them the loop (6.5 TB/s), the rest start and partials; two samples behind 500 tokens
 // (no other kernel): 10 us, and the join.
 #include "attn_walk.cuh"

@@ -26,9 +26,9 @@
 //
 // Bound: a step of two row tiles takes about 3500 cycles where its products need 2048: the
 // chain of scores, exponentials and P of the tile whose turn it is.  128 requests of up to 4
-// nodes behind 8000 common tokens (32 heads over 8 of 128): 48 us for the prefix's 34 GFLOP, 700
-// TFLOP/s (in full row tiles 42 GFLOP, 870); with all keys through this kernel the call took 104 us, with attention_few.cu
-// beside it 89; every request through tree attention reads the prefix 128 times.
+// nodes behind 8000 common tokens (32 heads over 8 of 128): 49 us for the prefix's 34 GFLOP, 700
+// TFLOP/s (in full row tiles 42 GFLOP, 870); with all keys through this kernel the call, replayed alone, took 104 us, with
+// attention_few.cu beside it 88; every request through tree attention reads the prefix 128 times.
 #include "attn_tc.cuh"
 #include "attn_walk.cuh"
 
@@ -759,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // group's prefix, in order, then those of its own tokens.  Where they are stands in parts_of;
 // their maxima and sums come a lane each, so that a row waits for one round of them.
 // Bound: latency of the record, the pairs and the columns, then HBM and L2; 128 requests (30
-// MB of partials) 9.7 us, 17 requests 6 to 8 us.  Done in the kernel for few rows,
+// MB of partials) 9.0 us, 17 requests 5.7 us.  Done in the kernel for few rows,
 // prefix partials cost it more than this launch.
 // kAhead: a row's partials in flight, 16 where all rows are resident at once with as many registers, else 8 (16 / 8, us
 // a call: two samples behind 2000 tokens 15.1 / 16.1, 17 requests 20.9 / 21.3, 128 requests 88 / 84).

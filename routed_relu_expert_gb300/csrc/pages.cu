@@ -84,8 +84,8 @@ __device__ __forceinline__ int block_sum(int v, int* tmp) {
 // Every block adds up the pages that the forks before its own take, shares its source's
 // whole pages and copies a part of the last one's tokens: one launch, no order among blocks.
 // Bound: L2 and HBM for many forks, the chain of dependent loads (rows, table, page, tokens)
-// for few.  512 forks of 16 prompts of up to 8000 tokens (120 MB of copied tokens): 24.8 us,
-// 4.8 TB/s, as with 8 and 32 pieces a thread (64: 26 to 30); one fork 4.2 us.
+// for few.  512 forks of 16 prompts of up to 8000 tokens (120 MB of copied tokens): 24.4 us,
+// 4.9 TB/s, as with 8 and 32 pieces a thread (64: 26 to 30); one fork 4.0 us.
 constexpr int kForkAhead = 4;                  // 16-byte pieces that a thread has in flight
 // blockIdx.x: the fork; blockIdx.y: a part of its page's tokens
 __global__ void __launch_bounds__(kThreads) fork_kernel(const ForkArgs a) {
@@ -223,7 +223,7 @@ __device__ __forceinline__ void list_of(const CompactArgs& a, int r, int& first,
 
 // Short lists: a block has a request and kThreads of a token's 16-byte pieces, a thread
 // one of them for token after token.  Bound: the chain of dependent loads (list, table,
-// tokens), a list's tokens eight at a time; 64 requests that keep 6 of 16 nodes: 2.8 us.
+// tokens), a list's tokens eight at a time; 64 requests that keep 6 of 16 nodes: 2.5 us.
 constexpr int kStage = 256;                    // moves worked out at a time
 constexpr int kMoveAhead = 8;                  // tokens whose loads a thread has in flight
 __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a) {
@@ -258,8 +258,8 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a) 
   if (bad) set_error(&a.hdr->err, bad);
 }
 
-// Which of the two, graph replay, us, short / long: lists of 8 on average (512 requests) 6.2 / 13.1, of 16 (64) 8.2 / 12.3,
-// of 32 (16) 10.3 / 12.3, of 64 (16) 17.8 / 12.3; one list of 200 24.6 / 12.3, of 4000 474 / 16.4, of 66667 31000 / 113.
+// Which of the two, replayed alone, us, short / long: lists of 8 on average (512 requests) 8.3 / 14.5, of 16 (64) 6.3 / 10.4,
+// of 32 (16) 8.2 / 10.4, of 64 (16) 10.4 / 10.4; one list of 200 22.9 / 10.3, of 4000 407 / 14.4, of 66667 9800 / 103.
 // kShortAll: so that one list among short ones cannot take longer than a few hundred us.
 constexpr int kShortList = 32, kShortAll = 4096;
 // Long lists, in two launches.  The first works the moves out, a thread a token (of all
@@ -293,9 +293,9 @@ __global__ void __launch_bounds__(kThreads) compact_moves_kernel(const CompactAr
 // goes to a place at or before its source, so what a wave writes lies behind every later
 // wave's sources and only its own wave and earlier ones read there.  A thread reads and
 // writes its own 16-byte pieces.  Bound: HBM, reads and writes in turn.  66667 of 100001
-// tokens of 4 KB (546 MB): 99 us, 5.5 TB/s or 82 % of a plain copy, and 104 us the call (with
-// one wave ahead of the writes 126, with one of 104 KB a block 114; more and smaller waves,
-// each of which costs half a microsecond beside its bytes: four of 48 KB 112, of 32 KB 125).
+// tokens of 4 KB (546 MB): 97 us, 5.6 TB/s or 84 % of a plain copy, and 99.5 us the call; 104
+// replayed alone (so, with one wave ahead of the writes 126, with one of 104 KB a block 114; more and
+// smaller waves, each of which costs half a microsecond beside its bytes: four of 48 KB 112, of 32 KB 125).
 constexpr int kWaveThreads = 512;
 constexpr int kWaves = 3;                      // in a block's shared memory
 constexpr int kWaveAhead = 9;                  // pieces of a thread a wave (72 KB a block)
@@ -397,7 +397,7 @@ __device__ __forceinline__ int block_scan(int v, int* tmp, int* total) {
 // down by atomics on whole numbers, whose order does not matter; which of its entries is the last
 // in the table, and so gives it back, is a maximum; places in the list come from prefix sums
 // of warps, blocks and the grid.  Bound: the latency of the phases and of up to three meetings
-// (2 us each).  1024 requests, most of their pages shared by 16: 18.7 us; 64 requests: 6.0 us;
+// (2 us each).  1024 requests, most of their pages shared by 16: 18.6 us; 64 requests: 5.8 us;
 // with one block for everything the 1024 took 142 us.
 __global__ void __launch_bounds__(kRelThreads, 1) release_kernel(const ReleaseArgs a) {
   extern __shared__ int prefix[];              // [R + 1] entries before each request

@@ -22,9 +22,9 @@
 // that every load and store is of whole lines.  The angles of a block's tokens are
 // computed once for all of its pieces, into shared memory.  16384 BF16 tokens of
 // 32 + 2 x 8 heads of 128 (403 MB): 73 us with half of the head turned = 5.5 TB/s, 76
-// with all of it, 66 with none (a plain cache write), 69 interleaved, 122 where 22 of
-// 128 turn; three axes, all of the head: 79: a rotating part that is no whole number of pieces (of pairs of pieces in the
-// half layout) goes by single elements, 2-byte loads and stores.
+// with all of it, 77 with all of it by three axes, 66 with none (a plain cache write), 69
+// interleaved.  122 where 22 of 128 turn: a rotating part that is no whole number of pieces
+// (of pairs of pieces in the half layout) goes by single elements, 2-byte loads and stores.
 #include "attn.h"
 
 #include <algorithm>

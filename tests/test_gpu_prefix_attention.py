@@ -410,6 +410,31 @@ def test_samples_of_one_prompt_share_its_pages(dt):
     assert sorted(shared.free_pages.tolist()) == list(range(120)) and _err(shared.ws) == 0
 
 
+def test_layers_may_have_one_workspace():
+    """The caches of two layers, whose calls follow one another."""
+    M = _m()
+    cfg = M.make_attn_config(8, 2, 64, n_pages=60, max_pages=20, rot_dim=64)
+    own, one = ([M.PagedKVCache(cfg, 2, prefix_rows=6) for _ in range(2)] for _ in range(2))
+    one[1].ws = one[0].ws
+    g = torch.Generator("cuda").manual_seed(8)
+    groups = M.PrefixGroups(_i32([0, 2]), _i32([0]), _i32([150]))
+    prompt, nodes = (torch.randn((2, n, 12, 64), generator=g, device="cuda").to(BF) for n in (150, 6))
+    cut = lambda t: (t[:, :8], t[:, 8:10], t[:, 10:])
+    outs = []
+    for caches in (own, one):
+        for c, p in zip(caches, prompt):
+            c.append(c.plan(_i32([0, 0]), _i32([150, 0]), 150), *cut(p))
+            c.fork(_i32([0]), _i32([1]), _i32([150]))
+        for c, x in zip(caches, nodes):
+            step = c.plan(_i32([150, 150]), _i32([2, 4]), 6)
+            outs.append(c.attend(step, c.append(step, *cut(x)), groups=groups))
+            c.release(step.kv_len, c.compact(_i32([150, 150]), _i32([0, 1, 3]), _i32([0, 1, 3])))
+            outs.append(c.k_cache)
+        assert all(_err(c.ws) == 0 for c in caches)
+    for a, b in zip(outs[:4], outs[4:]):
+        assert torch.equal(a, b)
+
+
 def test_cache_refusals():
     M = _m()
     cfg = M.make_attn_config(8, 2, 64, n_pages=8, max_pages=4, rot_dim=64)
